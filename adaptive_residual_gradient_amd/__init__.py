@@ -82,9 +82,40 @@ class Adam(ctypes.Structure):
                 ("scale", ctypes.c_float), ("step", ctypes.c_uint32)]
 
 
+class _Tensor(ctypes.Structure):
+    _fields_ = [("offset", ctypes.c_uint64), ("numel", ctypes.c_uint64),
+                ("weight_decay", ctypes.c_float), ("lr_scale", ctypes.c_float)]
+
+
+class OptimizerInfo(ctypes.Structure):
+    _fields_ = [("ntensors", ctypes.c_uint64), ("total_numel", ctypes.c_uint64),
+                ("span", ctypes.c_uint64), ("nblocks", ctypes.c_uint64),
+                ("norm_workspace_bytes", ctypes.c_uint64)]
+
+    def as_dict(self):
+        return {name: int(getattr(self, name)) for name, _ in self._fields_}
+
+
+class AdamW(ctypes.Structure):
+    """One AdamW step; see include/adacomp.h."""
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("step", ctypes.c_uint32)]
+
+
+class _ScanShape(ctypes.Structure):
+    _fields_ = [("length", ctypes.c_uint64), ("batch", ctypes.c_uint32), ("channels", ctypes.c_uint32),
+                ("type", ctypes.c_int), ("sigmoid", ctypes.c_int)]
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_uint64),
+                ("time_stride", ctypes.c_uint64)]
+
+
 # Every exported symbol, with its C signature (argtypes, restype).
 _P = ctypes.c_void_p
-_U32, _U64, _INT = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int
+_U32, _U64, _INT, _F32 = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
+_SHAPE, _VIEW = ctypes.POINTER(_ScanShape), ctypes.POINTER(_View)
 SIGNATURES = {
     "adacomp_plan_query": ([ctypes.POINTER(_Segment), _U32, ctypes.POINTER(PlanInfo)], _INT),
     "adacomp_plan_create": ([ctypes.POINTER(_Segment), _U32, ctypes.POINTER(_P)], _INT),
@@ -110,6 +141,22 @@ SIGNATURES = {
     "adacomp_timer_destroy": ([_P], _INT),
     "adacomp_timer_read": ([_P, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_U64), _U32], _INT),
     "adacomp_timer_reset": ([_P], _INT),
+    "adacomp_optimizer_query": ([ctypes.POINTER(_Tensor), _U32, ctypes.POINTER(OptimizerInfo)], _INT),
+    "adacomp_optimizer_create": ([ctypes.POINTER(_Tensor), _U32, ctypes.POINTER(_P)], _INT),
+    "adacomp_optimizer_destroy": ([_P], _INT),
+    "adacomp_optimizer_get_info": ([_P, ctypes.POINTER(OptimizerInfo)], _INT),
+    "adacomp_grad_norm": ([_P, _P, _INT, _U64, _F32, _F32, _P, _P, _U64, _P], _INT),
+    "adacomp_adamw_step": ([_P, _P, _P, _INT, _P, _P, _P, _U64, ctypes.POINTER(AdamW), _P, _P], _INT),
+    "adacomp_adamw_packed_step": ([_P, _P, _P, _INT, _P, _P, _P, _P, _U64, ctypes.POINTER(AdamW), _U32,
+                                   _P, _P], _INT),
+    "adacomp_layer_norm": ([_P, _U64, _P, _P, _P, _U64, _P, _P, _U64, _U32, _INT, _F32, _P], _INT),
+    "adacomp_layer_norm_backward": ([_P, _U64, _P, _U64, _P, _P, _P, _P, _U64, _P, _P, _U64, _U32, _INT,
+                                     _P, _U64, _P], _INT),
+    "adacomp_layer_norm_workspace_bytes": ([_U64, _U32, ctypes.POINTER(_U64)], _INT),
+    "adacomp_gated_scan": ([_SHAPE, _VIEW, _VIEW, _VIEW, _P, _P, _P, _P, _U64, _P], _INT),
+    "adacomp_gated_scan_backward": ([_SHAPE, _VIEW, _VIEW, _VIEW, _VIEW, _VIEW, _VIEW, _P, _P, _P, _P, _P,
+                                     _U64, _P], _INT),
+    "adacomp_gated_scan_workspace_bytes": ([_SHAPE, ctypes.POINTER(_U64)], _INT),
     "adacomp_status_str": ([_INT], ctypes.c_char_p),
 }
 
@@ -341,3 +388,282 @@ def message_header(plan: Plan, msg):
     from .stats import read_header
     raw = bytes(msg[: int(plan.info.header_bytes)].cpu().numpy().tobytes())
     return read_header(raw, int(plan.info.nseg))
+
+
+# --------------------------------------------------------------------------
+# Operators of the training step around the compressor (include/adacomp.h).
+# --------------------------------------------------------------------------
+
+MOMENT_BLOCK = 32        # elements of one tensor that share the scales of their 8-bit moments
+NORM_MAX_COLS = 65536    # longest row of layer_norm
+
+
+def _types():
+    import torch
+    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+_TYPES = None
+
+
+def _type_of(t, name: str) -> int:
+    global _TYPES
+    if _TYPES is None:
+        _TYPES = _types()
+    code = _TYPES.get(t.dtype)
+    if code is None or not t.is_cuda:
+        raise TypeError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
+    return code
+
+
+def _typed_ptr(t, dtypes, name: str) -> int:
+    if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, dtypes))}")
+    return t.data_ptr()
+
+
+def _f32_opt(t, n: int, name: str):
+    """Pointer of a nullable float32 tensor of n elements."""
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return _f32_ptr(t, name)
+
+
+class Optimizer:
+    """A table of tensors made into the work tiles of the optimizer kernels on
+    the current device.
+
+    ``tensors``: (offset, numel, weight_decay, lr_scale) per tensor, offsets in
+    elements of the flat buffers (multiples of 4)."""
+
+    def __init__(self, tensors):
+        self.tensors = [(int(o), int(n), float(d), float(r)) for o, n, d, r in tensors]
+        arr, n = _tensors(self.tensors)
+        h = _P()
+        _check("adacomp_optimizer_create", lib().adacomp_optimizer_create(arr, n, ctypes.byref(h)))
+        self.handle = h
+        info = OptimizerInfo()
+        _check("adacomp_optimizer_get_info", lib().adacomp_optimizer_get_info(h, ctypes.byref(info)))
+        self.info = info
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().adacomp_optimizer_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def norm_workspace(self, device="cuda"):
+        import torch
+        return torch.empty(int(self.info.norm_workspace_bytes), dtype=torch.uint8, device=device)
+
+    def moment_scales(self, device="cuda"):
+        """The scale bytes of 8-bit moments before the first step."""
+        import torch
+        return torch.zeros(2 * int(self.info.nblocks), dtype=torch.uint8, device=device)
+
+
+def _tensors(tensors):
+    arr = (_Tensor * max(1, len(tensors)))()
+    for i, t in enumerate(tensors):
+        arr[i] = _Tensor(int(t[0]), int(t[1]), float(t[2]), float(t[3]))
+    return arr, len(tensors)
+
+
+def optimizer_query(tensors) -> OptimizerInfo:
+    """Host-only: validate a table of tensors and return the sizes its optimizer would have."""
+    arr, n = _tensors(list(tensors))
+    info = OptimizerInfo()
+    _check("adacomp_optimizer_query", lib().adacomp_optimizer_query(arr, n, ctypes.byref(info)))
+    return info
+
+
+def _grad(grad):
+    code = _type_of(grad, "grad")
+    if not grad.is_contiguous():
+        raise TypeError("grad must be contiguous")
+    return code, grad.data_ptr()
+
+
+def _clip_ptr(clip):
+    if clip is None:
+        return None
+    if clip.numel() != 2:
+        raise ValueError("clip must have 2 elements")
+    return _f32_ptr(clip, "clip")
+
+
+def _bf16_ptr(t, n: int):
+    if t is None:
+        return None
+    import torch
+    if t.numel() < n:
+        raise ValueError("weights_bf16 shorter than the other buffers")
+    return _typed_ptr(t, (torch.bfloat16,), "weights_bf16")
+
+
+def grad_norm(opt: Optimizer, grad, clip, ws, max_norm: float, scale: float = 1.0, stream=None) -> None:
+    """clip[0] = norm of scale * grad over the table's tensors, clip[1] = the factor that brings it
+    down to max_norm."""
+    code, ptr = _grad(grad)
+    st = lib().adacomp_grad_norm(opt.handle, ptr, code, grad.numel(), max_norm, scale, _clip_ptr(clip),
+                                 _u8_ptr(ws, "ws"), ws.numel(), _stream_handle(stream))
+    _check("adacomp_grad_norm", st)
+
+
+def adamw(opt: Optimizer, weights, grad, m, v, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+          eps: float = 1e-8, step: int = 1, scale: float = 1.0, clip=None, weights_bf16=None,
+          stream=None) -> None:
+    """AdamW step number ``step`` (>= 1) on weights, m and v (float32, in place) with the gradient
+    scale * clip[1] * grad; weights_bf16 receives the new weights rounded."""
+    code, ptr = _grad(grad)
+    n = min(weights.numel(), grad.numel(), m.numel(), v.numel())
+    p = AdamW(lr, beta1, beta2, eps, scale, int(step))
+    st = lib().adacomp_adamw_step(
+        opt.handle, _f32_ptr(weights, "weights"), ptr, code, _f32_ptr(m, "m"), _f32_ptr(v, "v"),
+        _bf16_ptr(weights_bf16, opt.info.span), n, ctypes.byref(p), _clip_ptr(clip), _stream_handle(stream))
+    _check("adacomp_adamw_step", st)
+
+
+def adamw_packed(opt: Optimizer, weights, grad, m, v, scales, lr: float, beta1: float = 0.9,
+                 beta2: float = 0.999, eps: float = 1e-8, step: int = 1, scale: float = 1.0, seed: int = 0,
+                 clip=None, weights_bf16=None, stream=None) -> None:
+    """As adamw with moments in 8 bits: m and v e4m3 codes (float8_e4m3fn or uint8), scales as
+    Optimizer.moment_scales gives them, updated in place; ``seed`` chooses the rounding's random bits."""
+    import torch
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    if scales.numel() < 2 * opt.info.nblocks:
+        raise ValueError("scales shorter than the optimizer's blocks")
+    code, ptr = _grad(grad)
+    n = min(weights.numel(), grad.numel(), m.numel(), v.numel())
+    p = AdamW(lr, beta1, beta2, eps, scale, int(step))
+    st = lib().adacomp_adamw_packed_step(
+        opt.handle, _f32_ptr(weights, "weights"), ptr, code, _typed_ptr(m, codes, "m"),
+        _typed_ptr(v, codes, "v"), _u8_ptr(scales, "scales"), _bf16_ptr(weights_bf16, opt.info.span), n,
+        ctypes.byref(p), int(seed) & 0xFFFFFFFF, _clip_ptr(clip), _stream_handle(stream))
+    _check("adacomp_adamw_packed_step", st)
+
+
+def _rows(t, name: str, like=None):
+    """(pointer, row stride, rows, cols, type) of a tensor whose last axis is adjacent and whose
+    other axes have one stride between them."""
+    code = _type_of(t, name)
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name} must have the shape and type of the input")
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one axis")
+    cols = t.shape[-1]
+    rows = t.numel() // cols if cols else 0
+    if t.is_contiguous() or rows <= 1 and (t.stride(-1) == 1 or cols == 1):
+        stride = cols
+    elif t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
+        stride = t.stride(0)
+    else:
+        raise TypeError(f"{name} must be contiguous, or a matrix with adjacent columns")
+    return t.data_ptr(), stride, rows, cols, code
+
+
+def layer_norm(x, weight, bias, out, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """Layer norm of x over its last axis into out; weight and bias float32 or None; mean and rstd
+    (float32, one a row) are what layer_norm_backward needs."""
+    px, sx, rows, cols, code = _rows(x, "x")
+    po, so, _, _, _ = _rows(out, "out", x)
+    st = lib().adacomp_layer_norm(px, sx, _f32_opt(weight, cols, "weight"), _f32_opt(bias, cols, "bias"),
+                                  po, so, _f32_opt(mean, rows, "mean"), _f32_opt(rstd, rows, "rstd"), rows,
+                                  cols, code, eps, _stream_handle(stream))
+    _check("adacomp_layer_norm", st)
+
+
+def layer_norm_workspace(rows: int, cols: int, device="cuda"):
+    import torch
+    n = _U64(0)
+    _check("adacomp_layer_norm_workspace_bytes",
+           lib().adacomp_layer_norm_workspace_bytes(int(rows), int(cols), ctypes.byref(n)))
+    return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, ws=None,
+                        stream=None) -> None:
+    """Gradients of layer_norm: dx, and dweight and dbias (float32, both or neither)."""
+    pd, sd, rows, cols, code = _rows(dy, "dy")
+    px, sx, _, _, _ = _rows(x, "x", dy)
+    po, so, _, _, _ = _rows(dx, "dx", dy)
+    st = lib().adacomp_layer_norm_backward(
+        pd, sd, px, sx, _f32_opt(weight, cols, "weight"), _f32_opt(mean, rows, "mean"),
+        _f32_opt(rstd, rows, "rstd"), po, so, _f32_opt(dweight, cols, "dweight"),
+        _f32_opt(dbias, cols, "dbias"), rows, cols, code, None if ws is None else _u8_ptr(ws, "ws"),
+        0 if ws is None else ws.numel(), _stream_handle(stream))
+    _check("adacomp_layer_norm_backward", st)
+
+
+def _scan_view(t, shape, dtype, name: str):
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of the gate's shape and type")
+    B, T, D = shape
+    if D > 1 and t.stride(2) != 1 and t.numel():
+        raise TypeError(f"{name} must have adjacent channels")
+    return _View(t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1) if T > 1 else D)
+
+
+def _scan_shape(gate, sigmoid: bool):
+    code = _type_of(gate, "gate")
+    if gate.dim() != 3:
+        raise ValueError("gate must be [batch, length, channels]")
+    B, T, D = gate.shape
+    return _ScanShape(T, B, D, code, 1 if sigmoid else 0)
+
+
+def _lengths_ptr(lengths, batch: int):
+    if lengths is None:
+        return None
+    import torch
+    if lengths.numel() != batch:
+        raise ValueError("lengths must have one element a sequence")
+    return _typed_ptr(lengths, (torch.int32,), "lengths")
+
+
+def gated_scan_workspace(batch: int, length: int, channels: int, device="cuda"):
+    """Workspace of gated_scan and gated_scan_backward for one shape."""
+    import torch
+    n = _U64(0)
+    shape = _ScanShape(int(length), int(batch), int(channels), 0, 0)
+    _check("adacomp_gated_scan_workspace_bytes",
+           lib().adacomp_gated_scan_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)))
+    return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+
+def gated_scan(gate, x, h, h0=None, h_last=None, lengths=None, sigmoid: bool = True, ws=None,
+               stream=None) -> None:
+    """h_t = a_t h_(t-1) + k_t x_t along axis 1 of [batch, length, channels] tensors, with
+    (a, k) = (sigmoid(gate), sigmoid(-gate)) or (gate, 1); h0 and h_last float32 [batch, channels]."""
+    shape = _scan_shape(gate, sigmoid)
+    s, dt = gate.shape, gate.dtype
+    n = shape.batch * shape.channels
+    views = [_scan_view(t, s, dt, name) for t, name in ((gate, "gate"), (x, "x"), (h, "h"))]
+    st = lib().adacomp_gated_scan(
+        ctypes.byref(shape), *[ctypes.byref(v) for v in views], _f32_opt(h0, n, "h0"),
+        _f32_opt(h_last, n, "h_last"), _lengths_ptr(lengths, shape.batch),
+        None if ws is None else _u8_ptr(ws, "ws"), 0 if ws is None else ws.numel(), _stream_handle(stream))
+    _check("adacomp_gated_scan", st)
+
+
+def gated_scan_backward(gate, x, h, dh, dgate, dx, h0=None, dh_last=None, dh0=None, lengths=None,
+                        sigmoid: bool = True, ws=None, stream=None) -> None:
+    """Gradients of gated_scan from the states h it wrote (x is not needed, and may be None, without
+    the sigmoid)."""
+    shape = _scan_shape(gate, sigmoid)
+    s, dt = gate.shape, gate.dtype
+    n = shape.batch * shape.channels
+    views = [None if t is None else _scan_view(t, s, dt, name)
+             for t, name in ((gate, "gate"), (x, "x"), (h, "h"), (dh, "dh"), (dgate, "dgate"), (dx, "dx"))]
+    st = lib().adacomp_gated_scan_backward(
+        ctypes.byref(shape), *[None if v is None else ctypes.byref(v) for v in views], _f32_opt(h0, n, "h0"),
+        _f32_opt(dh_last, n, "dh_last"), _f32_opt(dh0, n, "dh0"), _lengths_ptr(lengths, shape.batch),
+        None if ws is None else _u8_ptr(ws, "ws"), 0 if ws is None else ws.numel(), _stream_handle(stream))
+    _check("adacomp_gated_scan_backward", st)

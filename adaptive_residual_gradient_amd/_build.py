@@ -6,7 +6,7 @@ import pathlib
 import subprocess
 
 HERE = pathlib.Path(__file__).resolve().parent
-SRC = HERE / "csrc" / "adacomp.hip"
+SOURCES = [HERE / "csrc" / "adacomp.hip", HERE / "csrc" / "training.hip"]
 LIB = HERE / "libadacomp.so"
 
 HIPCC_FLAGS = [
@@ -22,7 +22,7 @@ HIPCC_FLAGS = [
 def build(verbose: bool = False) -> pathlib.Path:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     tmp = LIB.with_suffix(".so.tmp")
-    cmd = [hipcc, *HIPCC_FLAGS, "-o", str(tmp), str(SRC)]
+    cmd = [hipcc, *HIPCC_FLAGS, "-o", str(tmp), *map(str, SOURCES)]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

@@ -15,10 +15,16 @@
 #include <vector>
 
 #include "../../include/adacomp.h"
+#include "host_checks.hpp"
 #include "kernels.hpp"
 #include "layout.hpp"
 
+using adacomp::aligned16;
+using adacomp::launch_status;
 using adacomp::Layout;
+using adacomp::overlaps;
+using adacomp::Range;
+using adacomp::range_of;
 using adacomp::SegDev;
 
 // Device copies of one tiling's tables.
@@ -122,17 +128,6 @@ struct adacomp_timer {
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-Range range_of(const void* p, uint64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + static_cast<uintptr_t>(bytes)};
-}
-
 int check_device(const adacomp_plan* plan) {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess) return ADACOMP_ERR_HIP;
@@ -186,10 +181,6 @@ struct CallTimer {
 uint32_t encode_blocks(const Layout& L) {
     const uint64_t b = (L.total_numel + 8191) / 8192;
     return static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(b, 1), adacomp::kEncMaxBlocks));
-}
-
-int launch_status() {
-    return hipGetLastError() == hipSuccess ? ADACOMP_OK : ADACOMP_ERR_HIP;
 }
 
 // Plain decode of long-bin tiles with the whole tile in LDS (one 1024-thread

@@ -1,0 +1,44 @@
+// Element types of the training-step operators: vectors of float32, bfloat16
+// and half in memory, float32 in registers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace adacomp {
+
+typedef __bf16 bf16;
+typedef _Float16 f16;
+
+template <int N>
+using FVec = float __attribute__((ext_vector_type(N)));
+
+// N elements at any address aligned to one element: gfx950 reads and writes
+// 16 bytes from any address, so rows of odd widths keep wide accesses (a row
+// that starts inside a 16-byte granule costs one more cache line, not a loop
+// over its elements).
+template <typename T, int N>
+struct Packed {
+    typedef T V __attribute__((ext_vector_type(N)));
+    typedef V Any __attribute__((aligned(sizeof(T))));
+};
+
+template <int N, typename T>
+__device__ __forceinline__ typename Packed<T, N>::V load_any(const T* p) {
+    return *reinterpret_cast<const typename Packed<T, N>::Any*>(p);
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_any(T* p, typename Packed<T, N>::V v) {
+    *reinterpret_cast<typename Packed<T, N>::Any*>(p) = v;
+}
+template <int N, typename T>
+__device__ __forceinline__ FVec<N> to_float(typename Packed<T, N>::V v) {
+    return __builtin_convertvector(v, FVec<N>);
+}
+// rounded to nearest, ties to even
+template <typename T, int N>
+__device__ __forceinline__ typename Packed<T, N>::V from_float(FVec<N> v) {
+    return __builtin_convertvector(v, typename Packed<T, N>::V);
+}
+
+}  // namespace adacomp

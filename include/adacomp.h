@@ -330,6 +330,198 @@ int adacomp_timer_destroy(adacomp_timer* timer);
 int adacomp_timer_read(adacomp_timer* timer, double* ms, uint64_t* launches, uint32_t nstages);
 int adacomp_timer_reset(adacomp_timer* timer);
 
+/* ------------------------------------------------------------------------
+ * Operators of the training step around the compressor: the optimizer step on
+ * the flat buffers decode writes, layer norm and the gated linear recurrence,
+ * each with its gradient.  The conventions above hold (device pointers of the
+ * current device, asynchronous on `stream`, errors found on the host before
+ * anything is enqueued, nothing allocated, deterministic); additions are
+ * named at each call.  An output buffer must not overlap any other buffer of
+ * the call. */
+
+/* Element types of the operators' activations and gradients. */
+#define ADACOMP_FLOAT 0
+#define ADACOMP_BFLOAT 1
+#define ADACOMP_HALF 2
+
+/* One tensor of an optimizer's table: numel consecutive elements of the flat
+ * buffers from element `offset` (a multiple of 4), its decoupled weight decay
+ * and its factor on the learning rate. */
+typedef struct adacomp_tensor {
+    uint64_t offset;
+    uint64_t numel;
+    float weight_decay;
+    float lr_scale;
+} adacomp_tensor;
+
+typedef struct adacomp_optimizer_info {
+    uint64_t ntensors;
+    uint64_t total_numel;
+    uint64_t span;                 /* max(offset + numel) rounded up to a multiple of 4 */
+    uint64_t nblocks;              /* sum over tensors of ceil(numel / ADACOMP_MOMENT_BLOCK) */
+    uint64_t norm_workspace_bytes; /* ws of adacomp_grad_norm */
+} adacomp_optimizer_info;
+
+typedef struct adacomp_optimizer adacomp_optimizer; /* opaque, immutable once created */
+
+/* Host-only: validate a table and report its sizes.  ERR_INVALID_ARGUMENT for
+ * an empty table, a tensor without elements or a factor that is not finite;
+ * ERR_MISALIGNED, ERR_OVERLAP and ERR_TOO_LARGE as for a segment table. */
+int adacomp_optimizer_query(const adacomp_tensor* tensors, uint32_t ntensors,
+                            adacomp_optimizer_info* info);
+/* Validate the table and copy its work tiles to the current device. */
+int adacomp_optimizer_create(const adacomp_tensor* tensors, uint32_t ntensors,
+                             adacomp_optimizer** optimizer);
+int adacomp_optimizer_destroy(adacomp_optimizer* optimizer);
+int adacomp_optimizer_get_info(const adacomp_optimizer* optimizer, adacomp_optimizer_info* info);
+
+/* Norm of the scaled gradient over every tensor of the table, and the factor
+ * that brings it down to max_norm:
+ *   clip[0] = scale * sqrt(sum g^2),  clip[1] = clip[0] > max_norm ? max_norm / clip[0] : 1
+ * summed, divided and compared in float64, each rounded once to float32.  A
+ * norm of NaN gives the factor 1, an infinite one 0.
+ *   grad  [span] of grad_type, read only; 16-byte aligned; elements outside
+ *         every tensor do not count.
+ *   clip  device float32[2] (8-byte aligned).
+ *   ws    16-byte aligned, ws_bytes >= info.norm_workspace_bytes; no initial
+ *         contents required. */
+int adacomp_grad_norm(const adacomp_optimizer* optimizer, const void* grad, int grad_type,
+                      uint64_t n_elems, float max_norm, float scale, float* clip, void* ws,
+                      uint64_t ws_bytes, void* stream);
+
+/* One AdamW step.  Per element of tensor i, with lr_i = lr * lr_scale_i:
+ *   g = grad * scale * (clip ? clip[1] : 1)
+ *   m = beta1 * m + (1 - beta1) * g;   v = beta2 * v + (1 - beta2) * (g * g)
+ *   w = w * (1 - lr_i * weight_decay_i)
+ *         - lr_i / (1 - beta1^step) * (m / (sqrt(v) / sqrt(1 - beta2^step) + eps))
+ * 1 - beta, the bias corrections, lr_i and the decay factor are formed in
+ * float64.  step >= 1 counts the calls made so far, this one included; it and
+ * lr are values of the call, so a captured step replays with the same ones. */
+typedef struct adacomp_adamw {
+    float lr;
+    float beta1;
+    float beta2;
+    float eps;
+    float scale;
+    uint32_t step;
+} adacomp_adamw;
+
+/* The step with float32 moments.
+ *   weights, m, v  [span] float32, updated in place.
+ *   grad           [span] of grad_type, read only.
+ *   weights_bf16   nullable [span] bfloat16: the new weights rounded once.
+ *   clip           nullable device float32[2], as adacomp_grad_norm writes it.
+ * Every [span] buffer is 16-byte aligned; elements outside every tensor are
+ * not written. */
+int adacomp_adamw_step(const adacomp_optimizer* optimizer, float* weights, const void* grad,
+                       int grad_type, float* m, float* v, void* weights_bf16, uint64_t n_elems,
+                       const adacomp_adamw* adamw, const float* clip, void* stream);
+
+/* The step with moments in 8 bits: blocks of ADACOMP_MOMENT_BLOCK consecutive
+ * elements of one tensor (the last one shorter) share one power-of-two scale
+ * for each moment, and an element holds an e4m3 code of m and one of v.
+ *   m_codes, v_codes  [span] bytes, 16-byte aligned: value = e4m3(code) * 2^(scale - 127).
+ *   scales            [2 * info.nblocks] bytes, 16-byte aligned: of block b (tensors
+ *                     in table order), m's at 2b and v's at 2b + 1.  All zeros
+ *                     is the state before the first step.
+ * g, m and v are formed in float64 (the weights' step from them in float32)
+ * and rounded once: the scale is the smallest in 0..254 under which the
+ * block's largest magnitude, cut to 20 fraction bits, is at most 448; each
+ * magnitude, cut to a multiple of 2^-17 of its code's step, is rounded up with
+ * the probability of its remainder.  The random bits of an element are a hash
+ * of its index, seed and step, so the same call gives the same codes whatever
+ * the table around it.  A v above zero never becomes zero; what no code
+ * holds, and NaN, becomes NaN. */
+#define ADACOMP_MOMENT_BLOCK 32u
+int adacomp_adamw_packed_step(const adacomp_optimizer* optimizer, float* weights,
+                              const void* grad, int grad_type, void* m_codes, void* v_codes,
+                              void* scales, void* weights_bf16, uint64_t n_elems,
+                              const adacomp_adamw* adamw, uint32_t seed, const float* clip,
+                              void* stream);
+
+/* Layer norm over the last axis of `rows` rows of `cols` elements:
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ * in float32 whatever the type, y rounded once.
+ *   x, y          rows of `type`, x_stride and y_stride (>= cols) elements apart;
+ *                 aligned to their element.
+ *   weight, bias  nullable [cols] float32 (absent: 1, 0).
+ *   mean, rstd    nullable [rows] float32 outputs, as the backward pass takes them.
+ * rows = 0 is no work; cols from 1 to ADACOMP_NORM_MAX_COLS, else ERR_TOO_LARGE. */
+#define ADACOMP_NORM_MAX_COLS 65536u
+int adacomp_layer_norm(const void* x, uint64_t x_stride, const float* weight, const float* bias,
+                       void* y, uint64_t y_stride, float* mean, float* rstd, uint64_t rows,
+                       uint32_t cols, int type, float eps, void* stream);
+
+/* Its gradients, with xhat = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum g / cols - xhat * sum (g * xhat) / cols)
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * in float32, the sums over rows joined in float64 in a fixed order.
+ *   weight          nullable (1).
+ *   dweight, dbias  [cols] float32, both or neither (NULL: not computed);
+ *                   with rows = 0 they become zero.
+ *   ws              16-byte aligned, ws_bytes >= adacomp_layer_norm_workspace_bytes(rows,
+ *                   cols); not used, and may be NULL, without dweight and dbias.  No
+ *                   initial contents required. */
+int adacomp_layer_norm_backward(const void* dy, uint64_t dy_stride, const void* x,
+                                uint64_t x_stride, const float* weight, const float* mean,
+                                const float* rstd, void* dx, uint64_t dx_stride, float* dweight,
+                                float* dbias, uint64_t rows, uint32_t cols, int type, void* ws,
+                                uint64_t ws_bytes, void* stream);
+int adacomp_layer_norm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t* bytes);
+
+/* Gated linear recurrence along the sequence, per sequence b and channel c:
+ *   h_t = a_t * h_(t-1) + k_t * x_t,   t = 0 .. n_b - 1
+ *   sigmoid = 1:  a = 1 / (1 + exp(-gate)),  k = 1 / (1 + exp(gate))  (= 1 - a)
+ *   sigmoid = 0:  a = gate,  k = 1
+ * states in float32.  The sequence is cut into chunks whose gate products are
+ * formed, so with sigmoid = 0 products of up to 512 consecutive gates have to
+ * stay within float32's range (gates in [-1, 1] always do). */
+typedef struct adacomp_scan_shape {
+    uint64_t length;      /* steps, n_b <= length; may be 0 */
+    uint32_t batch;       /* sequences; may be 0 */
+    uint32_t channels;    /* >= 1 */
+    int type;             /* element type of gate, x, h and their gradients */
+    int sigmoid;          /* 0 or 1 */
+} adacomp_scan_shape;
+
+/* A [batch, length, channels] tensor whose channels are adjacent; strides in
+ * elements, time_stride >= channels.  Aligned to its element. */
+typedef struct adacomp_view {
+    void* data;
+    uint64_t batch_stride;
+    uint64_t time_stride;
+} adacomp_view;
+
+/* Forward.
+ *   gate, x   inputs;  h  output, zero at steps from n_b on.
+ *   h0        nullable [batch, channels] float32: the state before step 0 (NULL: 0).
+ *   h_last    nullable [batch, channels] float32 output: the state after the
+ *             last step (h0 for an empty sequence).
+ *   lengths   nullable device int32[batch]: n_b, taken into 0 .. length; what lies at
+ *             steps from n_b on is not used, whatever it holds.  NULL: length.
+ *   ws        16-byte aligned, ws_bytes >= adacomp_gated_scan_workspace_bytes(shape);
+ *             no initial contents required. */
+int adacomp_gated_scan(const adacomp_scan_shape* shape, const adacomp_view* gate,
+                       const adacomp_view* x, const adacomp_view* h, const float* h0,
+                       float* h_last, const int32_t* lengths, void* ws, uint64_t ws_bytes,
+                       void* stream);
+
+/* Gradients, from the states h that the forward call wrote:
+ *   l_t = dh_t + a_(t+1) * l_(t+1),  dh_last added at the last step
+ *   dx = l * k;  sigmoid = 1: dgate = l * (h_(t-1) - x) * a * k, 0: dgate = l * h_(t-1)
+ *   dh0 = a_0 * l_0   (dh_last for an empty sequence)
+ *   x        not read, and may be NULL, with sigmoid = 0.
+ *   dgate, dx  outputs, zero at steps from n_b on.
+ *   h0, dh_last  nullable (0);  dh0  nullable output. */
+int adacomp_gated_scan_backward(const adacomp_scan_shape* shape, const adacomp_view* gate,
+                                const adacomp_view* x, const adacomp_view* h,
+                                const adacomp_view* dh, const adacomp_view* dgate,
+                                const adacomp_view* dx, const float* h0, const float* dh_last,
+                                float* dh0, const int32_t* lengths, void* ws, uint64_t ws_bytes,
+                                void* stream);
+int adacomp_gated_scan_workspace_bytes(const adacomp_scan_shape* shape, uint64_t* bytes);
+
 const char* adacomp_status_str(int status);
 
 #ifdef __cplusplus
