@@ -114,7 +114,7 @@ class _View(ctypes.Structure):
 
 # Every exported symbol, with its C signature (argtypes, restype).
 _P = ctypes.c_void_p
-_U32, _U64, _INT, _F32 = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
+_U32, _U64, _INT, _FLT = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
 _SHAPE, _VIEW = ctypes.POINTER(_ScanShape), ctypes.POINTER(_View)
 SIGNATURES = {
     "adacomp_plan_query": ([ctypes.POINTER(_Segment), _U32, ctypes.POINTER(PlanInfo)], _INT),
@@ -145,11 +145,11 @@ SIGNATURES = {
     "adacomp_optimizer_create": ([ctypes.POINTER(_Tensor), _U32, ctypes.POINTER(_P)], _INT),
     "adacomp_optimizer_destroy": ([_P], _INT),
     "adacomp_optimizer_get_info": ([_P, ctypes.POINTER(OptimizerInfo)], _INT),
-    "adacomp_grad_norm": ([_P, _P, _INT, _U64, _F32, _F32, _P, _P, _U64, _P], _INT),
+    "adacomp_grad_norm": ([_P, _P, _INT, _U64, _FLT, _FLT, _P, _P, _U64, _P], _INT),
     "adacomp_adamw_step": ([_P, _P, _P, _INT, _P, _P, _P, _U64, ctypes.POINTER(AdamW), _P, _P], _INT),
     "adacomp_adamw_packed_step": ([_P, _P, _P, _INT, _P, _P, _P, _P, _U64, ctypes.POINTER(AdamW), _U32,
                                    _P, _P], _INT),
-    "adacomp_layer_norm": ([_P, _U64, _P, _P, _P, _U64, _P, _P, _U64, _U32, _INT, _F32, _P], _INT),
+    "adacomp_layer_norm": ([_P, _U64, _P, _P, _P, _U64, _P, _P, _U64, _U32, _INT, _FLT, _P], _INT),
     "adacomp_layer_norm_backward": ([_P, _U64, _P, _U64, _P, _P, _P, _P, _U64, _P, _P, _U64, _U32, _INT,
                                      _P, _U64, _P], _INT),
     "adacomp_layer_norm_workspace_bytes": ([_U64, _U32, ctypes.POINTER(_U64)], _INT),
@@ -209,9 +209,13 @@ def plan_query(segments) -> PlanInfo:
 
 
 def _stream_handle(stream) -> Optional[int]:
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    try:   # the handle alone, without the Stream object around it (2.7 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _f32_ptr(t, name: str) -> int:
@@ -398,27 +402,31 @@ MOMENT_BLOCK = 32        # elements of one tensor that share the scales of their
 NORM_MAX_COLS = 65536    # longest row of layer_norm
 
 
-def _types():
+# Operand types, filled in at the first call: importing this module does not import torch.
+_TYPES: dict = {}
+_F32 = _I32 = _U8 = _BF16 = _CODES = None
+
+
+def _load_types() -> None:
+    global _F32, _I32, _U8, _BF16, _CODES
     import torch
-    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-
-
-_TYPES = None
+    _F32, _I32, _U8, _BF16 = torch.float32, torch.int32, torch.uint8, torch.bfloat16
+    _CODES = (torch.float8_e4m3fn, torch.uint8)
+    _TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
 
 
 def _type_of(t, name: str) -> int:
-    global _TYPES
-    if _TYPES is None:
-        _TYPES = _types()
+    if not _TYPES:
+        _load_types()
     code = _TYPES.get(t.dtype)
     if code is None or not t.is_cuda:
         raise TypeError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
     return code
 
 
-def _typed_ptr(t, dtypes, name: str) -> int:
-    if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, dtypes))}")
+def _ptr(t, dtype, name: str) -> int:
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA tensor of {dtype}")
     return t.data_ptr()
 
 
@@ -428,7 +436,12 @@ def _f32_opt(t, n: int, name: str):
         return None
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements")
-    return _f32_ptr(t, name)
+    return _ptr(t, _F32, name)
+
+
+def _ws(t):
+    """(pointer, bytes) of a nullable workspace."""
+    return (None, 0) if t is None else (_ptr(t, _U8, "ws"), t.numel())
 
 
 class Optimizer:
@@ -447,6 +460,7 @@ class Optimizer:
         info = OptimizerInfo()
         _check("adacomp_optimizer_get_info", lib().adacomp_optimizer_get_info(h, ctypes.byref(info)))
         self.info = info
+        self.span, self.nblocks = int(info.span), int(info.nblocks)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -491,29 +505,26 @@ def _grad(grad):
     return code, grad.data_ptr()
 
 
-def _clip_ptr(clip):
-    if clip is None:
-        return None
-    if clip.numel() != 2:
-        raise ValueError("clip must have 2 elements")
-    return _f32_ptr(clip, "clip")
-
-
-def _bf16_ptr(t, n: int):
+def _bf16_opt(t, n: int):
     if t is None:
         return None
-    import torch
     if t.numel() < n:
         raise ValueError("weights_bf16 shorter than the other buffers")
-    return _typed_ptr(t, (torch.bfloat16,), "weights_bf16")
+    return _ptr(t, _BF16, "weights_bf16")
+
+
+def _codes(t, name: str) -> int:
+    if t.dtype not in _CODES or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float8_e4m3fn or uint8 CUDA tensor")
+    return t.data_ptr()
 
 
 def grad_norm(opt: Optimizer, grad, clip, ws, max_norm: float, scale: float = 1.0, stream=None) -> None:
     """clip[0] = norm of scale * grad over the table's tensors, clip[1] = the factor that brings it
     down to max_norm."""
     code, ptr = _grad(grad)
-    st = lib().adacomp_grad_norm(opt.handle, ptr, code, grad.numel(), max_norm, scale, _clip_ptr(clip),
-                                 _u8_ptr(ws, "ws"), ws.numel(), _stream_handle(stream))
+    st = lib().adacomp_grad_norm(opt.handle, ptr, code, grad.numel(), max_norm, scale,
+                                 _f32_opt(clip, 2, "clip"), *_ws(ws), _stream_handle(stream))
     _check("adacomp_grad_norm", st)
 
 
@@ -526,8 +537,8 @@ def adamw(opt: Optimizer, weights, grad, m, v, lr: float, beta1: float = 0.9, be
     n = min(weights.numel(), grad.numel(), m.numel(), v.numel())
     p = AdamW(lr, beta1, beta2, eps, scale, int(step))
     st = lib().adacomp_adamw_step(
-        opt.handle, _f32_ptr(weights, "weights"), ptr, code, _f32_ptr(m, "m"), _f32_ptr(v, "v"),
-        _bf16_ptr(weights_bf16, opt.info.span), n, ctypes.byref(p), _clip_ptr(clip), _stream_handle(stream))
+        opt.handle, _ptr(weights, _F32, "weights"), ptr, code, _ptr(m, _F32, "m"), _ptr(v, _F32, "v"),
+        _bf16_opt(weights_bf16, opt.span), n, p, _f32_opt(clip, 2, "clip"), _stream_handle(stream))
     _check("adacomp_adamw_step", st)
 
 
@@ -536,17 +547,15 @@ def adamw_packed(opt: Optimizer, weights, grad, m, v, scales, lr: float, beta1: 
                  clip=None, weights_bf16=None, stream=None) -> None:
     """As adamw with moments in 8 bits: m and v e4m3 codes (float8_e4m3fn or uint8), scales as
     Optimizer.moment_scales gives them, updated in place; ``seed`` chooses the rounding's random bits."""
-    import torch
-    codes = (torch.float8_e4m3fn, torch.uint8)
-    if scales.numel() < 2 * opt.info.nblocks:
+    if scales.numel() < 2 * opt.nblocks:
         raise ValueError("scales shorter than the optimizer's blocks")
     code, ptr = _grad(grad)
     n = min(weights.numel(), grad.numel(), m.numel(), v.numel())
     p = AdamW(lr, beta1, beta2, eps, scale, int(step))
     st = lib().adacomp_adamw_packed_step(
-        opt.handle, _f32_ptr(weights, "weights"), ptr, code, _typed_ptr(m, codes, "m"),
-        _typed_ptr(v, codes, "v"), _u8_ptr(scales, "scales"), _bf16_ptr(weights_bf16, opt.info.span), n,
-        ctypes.byref(p), int(seed) & 0xFFFFFFFF, _clip_ptr(clip), _stream_handle(stream))
+        opt.handle, _ptr(weights, _F32, "weights"), ptr, code, _codes(m, "m"), _codes(v, "v"),
+        _ptr(scales, _U8, "scales"), _bf16_opt(weights_bf16, opt.span), n, p, int(seed) & 0xFFFFFFFF,
+        _f32_opt(clip, 2, "clip"), _stream_handle(stream))
     _check("adacomp_adamw_packed_step", st)
 
 
@@ -554,7 +563,7 @@ def _rows(t, name: str, like=None):
     """(pointer, row stride, rows, cols, type) of a tensor whose last axis is adjacent and whose
     other axes have one stride between them."""
     code = _type_of(t, name)
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype):
         raise ValueError(f"{name} must have the shape and type of the input")
     if t.dim() == 0:
         raise ValueError(f"{name} must have at least one axis")
@@ -597,35 +606,36 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None,
     st = lib().adacomp_layer_norm_backward(
         pd, sd, px, sx, _f32_opt(weight, cols, "weight"), _f32_opt(mean, rows, "mean"),
         _f32_opt(rstd, rows, "rstd"), po, so, _f32_opt(dweight, cols, "dweight"),
-        _f32_opt(dbias, cols, "dbias"), rows, cols, code, None if ws is None else _u8_ptr(ws, "ws"),
-        0 if ws is None else ws.numel(), _stream_handle(stream))
+        _f32_opt(dbias, cols, "dbias"), rows, cols, code, *_ws(ws), _stream_handle(stream))
     _check("adacomp_layer_norm_backward", st)
 
 
 def _scan_view(t, shape, dtype, name: str):
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of the gate's shape and type")
+    if t.is_contiguous():
+        return _View(t.data_ptr(), shape[1] * shape[2], shape[2])
     B, T, D = shape
-    if D > 1 and t.stride(2) != 1 and t.numel():
+    sb, st, sd = t.stride()
+    if D > 1 and sd != 1:
         raise TypeError(f"{name} must have adjacent channels")
-    return _View(t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1) if T > 1 else D)
+    return _View(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else D)
 
 
 def _scan_shape(gate, sigmoid: bool):
     code = _type_of(gate, "gate")
-    if gate.dim() != 3:
+    s = gate.shape
+    if len(s) != 3:
         raise ValueError("gate must be [batch, length, channels]")
-    B, T, D = gate.shape
-    return _ScanShape(T, B, D, code, 1 if sigmoid else 0)
+    return s, s[0] * s[2], _ScanShape(s[1], s[0], s[2], code, 1 if sigmoid else 0)
 
 
-def _lengths_ptr(lengths, batch: int):
+def _lengths_opt(lengths, batch: int):
     if lengths is None:
         return None
-    import torch
     if lengths.numel() != batch:
         raise ValueError("lengths must have one element a sequence")
-    return _typed_ptr(lengths, (torch.int32,), "lengths")
+    return _ptr(lengths, _I32, "lengths")
 
 
 def gated_scan_workspace(batch: int, length: int, channels: int, device="cuda"):
@@ -642,14 +652,12 @@ def gated_scan(gate, x, h, h0=None, h_last=None, lengths=None, sigmoid: bool = T
                stream=None) -> None:
     """h_t = a_t h_(t-1) + k_t x_t along axis 1 of [batch, length, channels] tensors, with
     (a, k) = (sigmoid(gate), sigmoid(-gate)) or (gate, 1); h0 and h_last float32 [batch, channels]."""
-    shape = _scan_shape(gate, sigmoid)
-    s, dt = gate.shape, gate.dtype
-    n = shape.batch * shape.channels
-    views = [_scan_view(t, s, dt, name) for t, name in ((gate, "gate"), (x, "x"), (h, "h"))]
+    s, n, shape = _scan_shape(gate, sigmoid)
+    dt = gate.dtype
     st = lib().adacomp_gated_scan(
-        ctypes.byref(shape), *[ctypes.byref(v) for v in views], _f32_opt(h0, n, "h0"),
-        _f32_opt(h_last, n, "h_last"), _lengths_ptr(lengths, shape.batch),
-        None if ws is None else _u8_ptr(ws, "ws"), 0 if ws is None else ws.numel(), _stream_handle(stream))
+        shape, _scan_view(gate, s, dt, "gate"), _scan_view(x, s, dt, "x"), _scan_view(h, s, dt, "h"),
+        _f32_opt(h0, n, "h0"), _f32_opt(h_last, n, "h_last"), _lengths_opt(lengths, s[0]), *_ws(ws),
+        _stream_handle(stream))
     _check("adacomp_gated_scan", st)
 
 
@@ -657,13 +665,11 @@ def gated_scan_backward(gate, x, h, dh, dgate, dx, h0=None, dh_last=None, dh0=No
                         sigmoid: bool = True, ws=None, stream=None) -> None:
     """Gradients of gated_scan from the states h it wrote (x is not needed, and may be None, without
     the sigmoid)."""
-    shape = _scan_shape(gate, sigmoid)
-    s, dt = gate.shape, gate.dtype
-    n = shape.batch * shape.channels
-    views = [None if t is None else _scan_view(t, s, dt, name)
-             for t, name in ((gate, "gate"), (x, "x"), (h, "h"), (dh, "dh"), (dgate, "dgate"), (dx, "dx"))]
+    s, n, shape = _scan_shape(gate, sigmoid)
+    dt = gate.dtype
     st = lib().adacomp_gated_scan_backward(
-        ctypes.byref(shape), *[None if v is None else ctypes.byref(v) for v in views], _f32_opt(h0, n, "h0"),
-        _f32_opt(dh_last, n, "dh_last"), _f32_opt(dh0, n, "dh0"), _lengths_ptr(lengths, shape.batch),
-        None if ws is None else _u8_ptr(ws, "ws"), 0 if ws is None else ws.numel(), _stream_handle(stream))
+        shape, _scan_view(gate, s, dt, "gate"), None if x is None else _scan_view(x, s, dt, "x"),
+        _scan_view(h, s, dt, "h"), _scan_view(dh, s, dt, "dh"), _scan_view(dgate, s, dt, "dgate"),
+        _scan_view(dx, s, dt, "dx"), _f32_opt(h0, n, "h0"), _f32_opt(dh_last, n, "dh_last"),
+        _f32_opt(dh0, n, "dh0"), _lengths_opt(lengths, s[0]), *_ws(ws), _stream_handle(stream))
     _check("adacomp_gated_scan_backward", st)

@@ -430,7 +430,8 @@ int adacomp_layer_norm_backward(const void* dy, uint64_t dy_stride, const void* 
 namespace {
 
 struct ScanLayout {
-    uint32_t chunks, chunk;
+    uint32_t lanes, groups, threads, steps, tiles;
+    bool chain;
     uint64_t ws;
 };
 
@@ -443,17 +444,37 @@ int check_shape(const adacomp_scan_shape* s) {
     return ADACOMP_OK;
 }
 
-// Chunks long enough that their states are few against the sequence, short
-// enough that the threads fill the chip.
-ScanLayout scan_layout(const adacomp_scan_shape& s) {
-    constexpr uint64_t kThreads = 131072;
+// Tiles of one shape for vectors of vw channels.
+ScanLayout scan_layout(const adacomp_scan_shape& s, uint32_t vw, bool back) {
+    using namespace adacomp;
     ScanLayout l{};
-    const uint64_t lanes = uint64_t(std::max(s.batch, 1u)) * ((s.channels + 1) / 2);
-    const uint64_t want = lanes * s.length / kThreads;
-    l.chunk = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(want, 16), 512));
-    l.chunks = static_cast<uint32_t>(std::max<uint64_t>((s.length + l.chunk - 1) / l.chunk, 1));
-    l.ws = l.chunks > 1 ? uint64_t(2) * 4 * s.batch * l.chunks * s.channels : 0;
+    const uint32_t per = scan_thread_steps(back);
+    if (s.length <= kScanShort) {   // one thread per vector
+        l.lanes = (s.channels + vw - 1) / vw;
+        return l;
+    }
+    l.lanes = 4;
+    while (l.lanes < 32 && l.lanes * vw < s.channels) l.lanes *= 2;
+    l.groups = (s.channels + l.lanes * vw - 1) / (l.lanes * vw);
+    uint32_t subs = std::max(64 / l.lanes, 2u);
+    while (subs * l.lanes < kScanThreads && uint64_t(subs) * per < s.length) subs *= 2;
+    l.threads = subs * l.lanes;
+    l.steps = subs * per;
+    l.tiles = static_cast<uint32_t>((s.length + l.steps - 1) / l.steps);
+    const uint64_t chains = uint64_t(s.batch) * l.groups;
+    l.chain = chains >= kScanQueues;
+    // a word of 8 bytes, or two floats, of every slot
+    if (l.tiles > 1) l.ws = kScanCountBytes + chains * l.tiles * l.lanes * vw * 8;
     return l;
+}
+// Channels of one thread: 4 bytes.
+uint32_t scan_vector(const adacomp_scan_shape& s) { return s.type == ADACOMP_FLOAT || s.channels < 2 ? 1 : 2; }
+// What either direction and any type of this shape needs.
+uint64_t scan_workspace(const adacomp_scan_shape& s) {
+    uint64_t most = 0;
+    for (const bool back : {false, true})
+        for (uint32_t vw = 1; vw <= std::min(s.channels, 2u); ++vw) most = std::max(most, scan_layout(s, vw, back).ws);
+    return most;
 }
 
 int check_view(const adacomp_view* v, const adacomp_scan_shape& s) {
@@ -516,11 +537,11 @@ int check_scan(const ScanCall& c) {
     if (!aligned_to(c.states_in[0], 4) || !aligned_to(c.states_in[1], 4) || !aligned_to(c.state_out, 4) ||
         !aligned_to(c.lengths, 4) || !aligned16(c.ws))
         return ADACOMP_ERR_MISALIGNED;
-    const ScanLayout l = scan_layout(s);
-    if (l.ws > 0 && c.ws == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
-    if (c.ws_bytes < l.ws) return ADACOMP_ERR_CAPACITY;
+    const uint64_t need = scan_workspace(s);
+    if (need > 0 && c.ws == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
+    if (c.ws_bytes < need) return ADACOMP_ERR_CAPACITY;
     const uint64_t state = 4 * uint64_t(s.batch) * s.channels;
-    Range r[11] = {range_of(c.state_out, c.state_out ? state : 0), range_of(c.ws, l.ws)};
+    Range r[11] = {range_of(c.state_out, c.state_out ? state : 0), range_of(c.ws, need)};
     int n = 2;
     for (int i = 0; i < c.nout && steps; ++i) r[n++] = view_range(*c.out[i], s);
     const int nout = n, nview = steps ? n + c.nin : n;
@@ -539,51 +560,71 @@ int check_scan(const ScanCall& c) {
     return ADACOMP_OK;
 }
 
-template <typename T, int VW, bool SIG>
-int launch_scan_as(adacomp::ScanArgs& a, bool back, hipStream_t s) {
+template <typename T, int VW, bool SIG, bool BACK>
+int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t s) {
     using namespace adacomp;
-    a.lanes = (a.channels + VW - 1) / VW;
-    const uint64_t threads = uint64_t(a.batch) * a.chunks * a.lanes;
-    const uint64_t blocks = (threads + 255) / 256;
-    if (blocks * 256 >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;
-    const dim3 grid(static_cast<uint32_t>(blocks)), block(256);
-    if (a.chunks > 1) {
-        const dim3 cgrid(static_cast<uint32_t>((uint64_t(a.batch) * a.channels + 63) / 64));
-        if (back) hipLaunchKernelGGL((k_scan_sum<T, VW, SIG, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_scan_sum<T, VW, SIG, false>), grid, block, 0, s, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        if (back) hipLaunchKernelGGL(k_scan_carry<true>, cgrid, dim3(64), 0, s, a);
-        else hipLaunchKernelGGL(k_scan_carry<false>, cgrid, dim3(64), 0, s, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    if (l.tiles == 0) {
+        const uint64_t blocks = (uint64_t(a.batch) * l.lanes + 255) / 256;
+        hipLaunchKernelGGL((k_scan_short<T, VW, SIG, BACK>), dim3(uint32_t(blocks)), dim3(256), 0, s, a);
+        return launch_status();
     }
-    if (back) hipLaunchKernelGGL((k_scan_backward<T, VW, SIG>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_scan_forward<T, VW, SIG>), grid, block, 0, s, a);
+    const uint64_t chains = uint64_t(a.batch) * l.groups, n = chains * l.tiles;
+    // work-items of one launch must fit in 32 bits (the queues round the chains up)
+    if ((chains + kScanQueues) * l.tiles * l.threads >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;
+    const dim3 block(l.threads);
+    if (l.tiles == 1) {
+        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanWhole>), dim3(uint32_t(n)), block, 0, s, a);
+        return launch_status();
+    }
+    if (l.chain) {
+        const uint64_t vecs = l.ws / 16;
+        a.tickets = static_cast<uint32_t*>(ws);
+        a.words = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(ws) + kScanCountBytes);
+        hipLaunchKernelGGL(k_scan_clear, dim3(uint32_t(std::min<uint64_t>((vecs + 255) / 256, 2048))), dim3(256), 0, s,
+                           static_cast<uint4*>(ws), vecs);
+        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+        const uint64_t grid = (chains + kScanQueues - 1) / kScanQueues * kScanQueues * l.tiles;
+        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain>), dim3(uint32_t(grid)), block, 0, s, a);
+        return launch_status();
+    }
+    a.agg_a = static_cast<float*>(ws);
+    a.agg_s = a.agg_a + n * l.lanes * VW;
+    hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanSum>), dim3(uint32_t(n)), block, 0, s, a);
+    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    hipLaunchKernelGGL(k_scan_carry<BACK>, dim3(uint32_t(chains)), dim3(1024), 0, s, a, uint32_t(VW));
+    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanCarry>), dim3(uint32_t(n)), block, 0, s, a);
     return launch_status();
 }
 
-template <typename T>
-int launch_scan(adacomp::ScanArgs& a, bool sigmoid, bool back, hipStream_t s) {
-    if (a.channels < 2)
-        return sigmoid ? launch_scan_as<T, 1, true>(a, back, s) : launch_scan_as<T, 1, false>(a, back, s);
-    return sigmoid ? launch_scan_as<T, 2, true>(a, back, s) : launch_scan_as<T, 2, false>(a, back, s);
+template <typename T, int VW>
+int launch_scan_as(adacomp::ScanArgs& a, bool sigmoid, bool back, const ScanLayout& l, void* ws, hipStream_t s) {
+    if (sigmoid)
+        return back ? launch_scan<T, VW, true, true>(a, l, ws, s) : launch_scan<T, VW, true, false>(a, l, ws, s);
+    return back ? launch_scan<T, VW, false, true>(a, l, ws, s) : launch_scan<T, VW, false, false>(a, l, ws, s);
 }
 
 int run_scan(const ScanCall& c, adacomp::ScanArgs& a, bool back, void* stream) {
     const adacomp_scan_shape& s = *c.shape;
-    const ScanLayout l = scan_layout(s);
+    const uint32_t vw = scan_vector(s);
+    const ScanLayout l = scan_layout(s, vw, back);
     a.lengths = c.lengths;
     a.last = c.state_out;
-    a.agg_a = static_cast<float*>(c.ws);
-    a.agg_s = a.agg_a + uint64_t(s.batch) * l.chunks * s.channels;
     a.length = s.length;
     a.batch = s.batch;
     a.channels = s.channels;
-    a.chunks = l.chunks;
-    a.chunk = l.chunk;
+    a.lanes = l.lanes;
+    a.groups = l.groups;
+    a.tiles = l.tiles;
+    a.steps = l.steps;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (s.type == ADACOMP_FLOAT) return launch_scan<float>(a, s.sigmoid != 0, back, hs);
-    if (s.type == ADACOMP_BFLOAT) return launch_scan<adacomp::bf16>(a, s.sigmoid != 0, back, hs);
-    return launch_scan<adacomp::f16>(a, s.sigmoid != 0, back, hs);
+    const bool sig = s.sigmoid != 0;
+    if (s.type == ADACOMP_FLOAT) return launch_scan_as<float, 1>(a, sig, back, l, c.ws, hs);
+    if (s.type == ADACOMP_BFLOAT)
+        return vw == 1 ? launch_scan_as<adacomp::bf16, 1>(a, sig, back, l, c.ws, hs)
+                       : launch_scan_as<adacomp::bf16, 2>(a, sig, back, l, c.ws, hs);
+    return vw == 1 ? launch_scan_as<adacomp::f16, 1>(a, sig, back, l, c.ws, hs)
+                   : launch_scan_as<adacomp::f16, 2>(a, sig, back, l, c.ws, hs);
 }
 
 }  // namespace
@@ -593,7 +634,7 @@ extern "C" {
 int adacomp_gated_scan_workspace_bytes(const adacomp_scan_shape* shape, uint64_t* bytes) {
     if (bytes == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
     const int st = check_shape(shape);
-    if (st == ADACOMP_OK) *bytes = scan_layout(*shape).ws;
+    if (st == ADACOMP_OK) *bytes = scan_workspace(*shape);
     return st;
 }
 

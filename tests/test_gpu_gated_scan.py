@@ -96,7 +96,9 @@ def test_channels(D, dtype):
 
 
 @pytest.mark.parametrize("B,T,D", [(1, 5000, 24), (64, 40, 33), (5, 700, 260), (300, 1, 7), (1, 20000, 3),
-                                   (16, 513, 128)])
+                                   (16, 513, 128),
+                                   # at least 64 chains of tiles: the state travels from tile to tile
+                                   (64, 600, 20), (70, 300, 33), (5, 1500, 1000), (1, 3000, 4101), (130, 270, 1)])
 @pytest.mark.parametrize("sigmoid", [True, False])
 def test_shapes(B, T, D, sigmoid):
     Case(B, T, D, torch.float32, sigmoid, seed=1).check()
@@ -113,6 +115,12 @@ def test_ragged(dtype, sigmoid):
     Case(len(lengths), T, 65, TYPES[dtype], sigmoid, lengths=lengths).check()
     Case(3, 1, 65, TYPES[dtype], sigmoid, lengths=[0, 1, 2]).check()
     Case(2, 1000, 65, TYPES[dtype], sigmoid, lengths=[0, 0]).check()
+    rng = np.random.default_rng(3)
+    T = 1100
+    lengths = [0, T, 1, 255, 256, 257, 511, 512, 513, 767, 768, 769] + rng.integers(0, T + 1, 60).tolist()
+    Case(len(lengths), T, 40, TYPES[dtype], sigmoid, lengths=lengths).check()
+    T = 3000
+    Case(6, T, 40, TYPES[dtype], sigmoid, lengths=[0, T, 1, 1024, 2047, 2050]).check()
 
 
 @pytest.mark.parametrize("layout", ["part", "time_first"])
@@ -255,12 +263,13 @@ def test_in_a_graph_and_on_another_stream():
 
 
 def test_refusals():
-    z = torch.zeros(2, 300, 8, device=DEV)
-    x, h, ws = z.clone(), z.clone(), A.gated_scan_workspace(2, 300, 8, DEV)
+    z = torch.zeros(2, 3000, 8, device=DEV)
+    x, h, ws = z.clone(), z.clone(), A.gated_scan_workspace(2, 3000, 8, DEV)
+    assert ws.numel() > 64      # several tiles: a workspace is needed
     for bad in (lambda: A.gated_scan(z, x, z, ws=ws), lambda: A.gated_scan(z, x, x, ws=ws),
                 lambda: A.gated_scan(z, x, h), lambda: A.gated_scan(z, x, h, ws=ws[:64]),
                 lambda: A.gated_scan_backward(z, None, h, x, z.clone(), z.clone(), ws=ws),
-                lambda: A.gated_scan(z, x, h[:1].expand(2, 300, 8), ws=ws)):
+                lambda: A.gated_scan(z, x, h[:1].expand(2, 3000, 8), ws=ws)):
         with pytest.raises(A.AdaCompError):
             bad()
     with pytest.raises(ValueError):
