@@ -42,7 +42,7 @@ def test_optimizer_table_refused(table, status):
 def test_optimizer_info():
     info = A.optimizer_query([(8, 33, 0.1, 1.0), (0, 5, 0.0, 0.5), (44, 8193, 0.0, 1.0)])
     assert info.as_dict() == {"ntensors": 3, "total_numel": 33 + 5 + 8193, "span": 8240,
-                              "nblocks": 2 + 1 + 257, "norm_workspace_bytes": 8 * (1 + 1 + 3)}
+                              "nblocks": 2 + 1 + 257, "norm_workspace_bytes": 8 * (1 + 1 + 9)}
     # more work tiles than the norm's first pass has workgroups
     assert A.optimizer_query([(0, 1 << 30, 0.0, 1.0)]).norm_workspace_bytes == 8 * 2048
 
