@@ -31,6 +31,15 @@ template <int N, typename T>
 __device__ __forceinline__ void store_any(T* p, typename Packed<T, N>::V v) {
     *reinterpret_cast<typename Packed<T, N>::Any*>(p) = v;
 }
+// The same, of data that is touched once.
+template <int N, typename T>
+__device__ __forceinline__ typename Packed<T, N>::V stream_load(const T* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const typename Packed<T, N>::Any*>(p));
+}
+template <int N, typename T>
+__device__ __forceinline__ void stream_store(T* p, typename Packed<T, N>::V v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<typename Packed<T, N>::Any*>(p));
+}
 template <int N, typename T>
 __device__ __forceinline__ FVec<N> to_float(typename Packed<T, N>::V v) {
     return __builtin_convertvector(v, FVec<N>);

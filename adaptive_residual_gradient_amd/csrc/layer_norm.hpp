@@ -20,6 +20,8 @@ namespace adacomp {
 constexpr int kNormElems = 16;                            // most elements of a row per lane
 constexpr uint32_t kNormWaveCols = 64 * kNormElems;       // one wavefront's columns
 constexpr uint32_t kNormRegCols = 16 * kNormWaveCols;     // a workgroup's
+constexpr uint32_t kNormMaxWaves = 4096;                  // wavefronts of a forward launch
+constexpr uint32_t kNormBackRegCols = 8 * kNormWaveCols;
 constexpr uint32_t kNormMaxPartials = 1024;               // workgroups of the weight gradients
 constexpr uint32_t kNormWideThreads = 1024;
 
@@ -69,123 +71,159 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
     }
     return v;
 }
-
 template <typename T>
 constexpr int norm_vec() {
     return 16 / int(sizeof(T));
 }
 
-// VEC elements from column c on as float, 0 past the row's end.
-template <typename T, int VEC>
-__device__ __forceinline__ FVec<VEC> load_cols(const T* row, uint32_t c, uint32_t cols) {
-    if (c + VEC <= cols) return to_float<VEC, T>(load_any<VEC>(row + c));
-    FVec<VEC> v = 0.f;
+// A thread's columns.  Vector j covers VEC columns from at[j] on, and at[j]
+// never reaches past the row: where the columns are no multiple of the team's,
+// the last vectors move back over columns that other lanes hold too.  Loads and
+// results need no care then (both lanes form the same bits); sums leave the
+// first skip[j] elements of a vector out.  Needs cols >= VEC.
+template <int VEC, int NV>
+struct NormCols {
+    uint32_t at[NV];
+    int skip[NV];
+    bool ragged;   // some lane of the wavefront has elements to leave out
+    __device__ NormCols(uint32_t cols, uint32_t lane, uint32_t team) {
+        bool any = false;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k)
-        if (c + k < cols) v[k] = float(row[c + k]);
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t c = (j * team + lane) * VEC;
+            at[j] = min(c, cols - VEC);
+            skip[j] = int(c - at[j]);
+            any |= skip[j] > 0;
+        }
+        ragged = __any(any);
+    }
+};
+
+// Weight or bias, which every row reads.
+template <int VEC>
+__device__ __forceinline__ FVec<VEC> load_param(const float* p, uint32_t c, float absent) {
+    FVec<VEC> v = absent;
+    if (p != nullptr) v = load_any<VEC>(p + c);
     return v;
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store_cols(T* row, uint32_t c, uint32_t cols, FVec<VEC> v) {
-    const typename Packed<T, VEC>::V o = from_float<T, VEC>(v);
-    if (c + VEC <= cols) {
-        store_any<VEC>(row + c, o);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < VEC; ++k)
-        if (c + k < cols) row[c + k] = o[k];
+
+// The thread's team.  A whole wavefront's is told to be the same in every
+// lane, so that its rows' addresses and statistics take scalar registers.
+template <int LANES, bool BLOCK>
+__device__ __forceinline__ uint32_t team_index() {
+    if (BLOCK) return 0;
+    const uint32_t i = threadIdx.x / LANES;
+    return LANES == 64 ? uint32_t(__builtin_amdgcn_readfirstlane(int(i))) : i;
 }
 
 // ---- forward ----
 
-template <typename T, int NV, int LANES, bool BLOCK>
+// The next row is requested before the present one is joined; weight and bias
+// stay in registers over a workgroup's rows (read anew for each row they are
+// four times a 16-bit row's bytes).
+template <typename T, int VEC, int NV, int LANES, bool BLOCK>
 __global__ __launch_bounds__(BLOCK ? 1024 : 256) void k_layer_norm(NormArgs a) {
-    constexpr int VEC = norm_vec<T>();
-    const uint32_t team = BLOCK ? blockDim.x : LANES;
-    const uint32_t lane = BLOCK ? threadIdx.x : threadIdx.x % LANES;
-    const uint64_t row = BLOCK ? blockIdx.x : uint64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-    const bool live = BLOCK || row < a.rows;   // all lanes take part in the sums
+    typedef typename Packed<T, VEC>::V V;
+    constexpr uint32_t TEAMS = BLOCK ? 1 : 256 / LANES;
+    const uint32_t team = BLOCK ? blockDim.x : LANES, lane = threadIdx.x % team;
+    const uint32_t mine = team_index<LANES, BLOCK>();
+    const NormCols<VEC, NV> cols(a.cols, lane, team);
     __shared__ float slots[2][16];
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    FVec<VEC> v[NV];
-    float sum = 0.f;
+    FVec<VEC> w[NV], b[NV];
+    V next[NV];
+    auto request = [&](uint64_t row) {   // past the last row: the last row again
+        const T* x = static_cast<const T*>(a.x) + min(row, a.rows - 1) * a.x_stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) next[j] = stream_load<VEC>(x + cols.at[j]);
+    };
+    const uint64_t step = uint64_t(gridDim.x) * TEAMS;
+    request(uint64_t(blockIdx.x) * TEAMS + mine);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        v[j] = 0.f;
-        if (live) v[j] = load_cols<T, VEC>(x, (j * team + lane) * VEC, a.cols);
+        w[j] = load_param<VEC>(a.weight, cols.at[j], 1.f);
+        b[j] = load_param<VEC>(a.bias, cols.at[j], 0.f);
     }
+    for (uint64_t r0 = uint64_t(blockIdx.x) * TEAMS; r0 < a.rows; r0 += step) {
+        const uint64_t row = r0 + mine;
+        FVec<VEC> v[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) v[j] = to_float<VEC, T>(next[j]);
+        if (r0 + step < a.rows) request(row + step);
+        float sum = 0.f, square = 0.f;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) sum += v[j][k];
-    const float mean = row_sum<LANES, BLOCK>(sum, slots[0]) * a.inv_cols;
-    float square = 0.f;
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+            for (int k = 0; k < VEC; ++k) sum += cols.ragged && k < cols.skip[j] ? 0.f : v[j][k];
+        // all lanes take part in the sums, those without a row too; the two sums' barriers keep
+        // each slot until all have read it
+        const float mean = row_sum<LANES, BLOCK>(sum, slots[0]) * a.inv_cols;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const bool in = (j * team + lane) * VEC + k < a.cols;
-            v[j][k] = in ? v[j][k] - mean : 0.f;
-            square = __builtin_fmaf(v[j][k], v[j][k], square);
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                v[j][k] -= mean;
+                const float d = cols.ragged && k < cols.skip[j] ? 0.f : v[j][k];
+                square = __builtin_fmaf(d, d, square);
+            }
+        const float var = row_sum<LANES, BLOCK>(square, slots[1]) * a.inv_cols;
+        const float rstd = 1.0f / sqrtf(var + a.eps);
+        if (row >= a.rows) continue;
+        T* y = static_cast<T*>(a.out) + row * a.out_stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            FVec<VEC> o;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) o[k] = __builtin_fmaf(v[j][k] * rstd, w[j][k], b[j][k]);
+            if (cols.skip[j] < VEC) stream_store<VEC>(y + cols.at[j], from_float<T, VEC>(o));
         }
-    const float var = row_sum<LANES, BLOCK>(square, slots[1]) * a.inv_cols;
-    const float rstd = 1.0f / sqrtf(var + a.eps);
-    if (!live) return;
-    T* y = static_cast<T*>(a.out) + row * a.out_stride;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const uint32_t c = (j * team + lane) * VEC;
-        if (c >= a.cols) continue;
-        FVec<VEC> w = 1.f, b = 0.f;
-        if (a.weight) w = load_cols<float, VEC>(a.weight, c, a.cols);
-        if (a.bias) b = load_cols<float, VEC>(a.bias, c, a.cols);
-        FVec<VEC> o;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) o[k] = __builtin_fmaf(v[j][k] * rstd, w[k], b[k]);
-        store_cols<T, VEC>(y, c, a.cols, o);
-    }
-    if (lane == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
     }
 }
 
 // Rows past kNormRegCols columns: one workgroup a row, read once per pass.
+template <typename T, int VEC, typename F>
+__device__ __forceinline__ void each_vector(uint32_t cols, F f) {
+    for (uint32_t c = threadIdx.x * VEC; c < cols; c += kNormWideThreads * VEC) {
+        const uint32_t at = min(c, cols - VEC);
+        f(at, int(c - at));
+    }
+}
+
 template <typename T>
 __global__ __launch_bounds__(kNormWideThreads) void k_layer_norm_wide(NormArgs a) {
     constexpr int VEC = norm_vec<T>();
     __shared__ float slots[2][16];
     const uint64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    float sum = 0.f;
-    for (uint32_t c = threadIdx.x * VEC; c < a.cols; c += kNormWideThreads * VEC) {
-        const FVec<VEC> v = load_cols<T, VEC>(x, c, a.cols);
+    float sum = 0.f, square = 0.f;
+    each_vector<T, VEC>(a.cols, [&](uint32_t at, int skip) {
+        const FVec<VEC> v = to_float<VEC, T>(load_any<VEC>(x + at));
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) sum += v[k];
-    }
+        for (int k = 0; k < VEC; ++k) sum += k < skip ? 0.f : v[k];
+    });
     const float mean = row_sum<64, true>(sum, slots[0]) * a.inv_cols;
-    float square = 0.f;
-    for (uint32_t c = threadIdx.x * VEC; c < a.cols; c += kNormWideThreads * VEC) {
-        const FVec<VEC> v = load_cols<T, VEC>(x, c, a.cols);
+    each_vector<T, VEC>(a.cols, [&](uint32_t at, int skip) {
+        const FVec<VEC> v = to_float<VEC, T>(load_any<VEC>(x + at));
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            const float d = c + k < a.cols ? v[k] - mean : 0.f;
+            const float d = k < skip ? 0.f : v[k] - mean;
             square = __builtin_fmaf(d, d, square);
         }
-    }
+    });
     const float var = row_sum<64, true>(square, slots[1]) * a.inv_cols;
     const float rstd = 1.0f / sqrtf(var + a.eps);
     T* y = static_cast<T*>(a.out) + row * a.out_stride;
-    for (uint32_t c = threadIdx.x * VEC; c < a.cols; c += kNormWideThreads * VEC) {
-        const FVec<VEC> v = load_cols<T, VEC>(x, c, a.cols);
-        FVec<VEC> w = 1.f, b = 0.f, o;
-        if (a.weight) w = load_cols<float, VEC>(a.weight, c, a.cols);
-        if (a.bias) b = load_cols<float, VEC>(a.bias, c, a.cols);
+    each_vector<T, VEC>(a.cols, [&](uint32_t at, int) {
+        const FVec<VEC> v = to_float<VEC, T>(load_any<VEC>(x + at));
+        const FVec<VEC> w = load_param<VEC>(a.weight, at, 1.f), b = load_param<VEC>(a.bias, at, 0.f);
+        FVec<VEC> o;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) o[k] = __builtin_fmaf((v[k] - mean) * rstd, w[k], b[k]);
-        store_cols<T, VEC>(y, c, a.cols, o);
-    }
+        store_any<VEC>(y + at, from_float<T, VEC>(o));
+    });
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
@@ -196,104 +234,125 @@ __global__ __launch_bounds__(kNormWideThreads) void k_layer_norm_wide(NormArgs a
 
 // Each team steps over rows and adds its columns' share of dweight and dbias
 // in registers; the workgroup's teams are joined in LDS in team order and
-// written as one partial row pair, which k_norm_weight_grad adds up.
-template <typename T, int NV, int LANES, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 1024 : 256) void k_layer_norm_backward(NormArgs a) {
-    constexpr int VEC = norm_vec<T>();
+// written as one partial row pair, which k_norm_weight_grad adds up.  The next
+// row is requested before the present one is joined, and the weight waits in
+// LDS, for registers decide how many wavefronts keep a row in flight.  A team
+// is LANES lanes of a wavefront or, BLOCK, a workgroup.
+template <typename T, int VEC, int NV, int LANES, bool BLOCK>
+__global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormArgs a) {
+    typedef typename Packed<T, VEC>::V V;
     constexpr uint32_t TEAMS = BLOCK ? 1 : 256 / LANES;
-    const uint32_t team = BLOCK ? blockDim.x : LANES;
-    const uint32_t lane = BLOCK ? threadIdx.x : threadIdx.x % LANES;
-    const uint32_t mine = BLOCK ? 0 : threadIdx.x / LANES;
-    __shared__ float slots[4][16];
-    __shared__ float joined[BLOCK ? 1 : 2 * 256 * NV * VEC];
-    FVec<VEC> w[NV], dw[NV], db[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const uint32_t c = (j * team + lane) * VEC;
-        dw[j] = db[j] = 0.f;
-        w[j] = 1.f;
-        if (a.weight) w[j] = load_cols<float, VEC>(a.weight, c, a.cols);
-    }
-    uint32_t turn = 0;
-    for (uint64_t r0 = uint64_t(blockIdx.x) * TEAMS; r0 < a.rows; r0 += uint64_t(gridDim.x) * TEAMS) {
-        const uint64_t row = r0 + mine;
-        const bool live = row < a.rows;
-        const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
-        FVec<VEC> h[NV], g[NV];
-        float mean = 0.f, rstd = 0.f;
-        if (live) {
-            mean = a.mean[row];
-            rstd = a.rstd[row];
-        }
+    const uint32_t team = BLOCK ? blockDim.x : LANES, lane = threadIdx.x % team;
+    const uint32_t mine = team_index<LANES, BLOCK>();
+    const NormCols<VEC, NV> cols(a.cols, lane, team);
+    __shared__ float slots[2][16];
+    extern __shared__ float dynamic[];   // the weight, then the teams' sums
+    FVec<VEC> dw[NV], db[NV];
+    V nx[NV], ng[NV];
+    float nmean, nrstd;
+    auto request = [&](uint64_t row) {   // past the last row: the last row again
+        const uint64_t r = min(row, a.rows - 1);
+        nmean = a.mean[r];
+        nrstd = a.rstd[r];
+        const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+        const T* dy = static_cast<const T*>(a.dy) + r * a.dy_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const uint32_t c = (j * team + lane) * VEC;
-            h[j] = g[j] = 0.f;
-            if (live) {
-                h[j] = load_cols<T, VEC>(x, c, a.cols);
-                g[j] = load_cols<T, VEC>(dy, c, a.cols);
-            }
+            nx[j] = stream_load<VEC>(x + cols.at[j]);
+            ng[j] = stream_load<VEC>(dy + cols.at[j]);
         }
-        float sum = 0.f, along = 0.f;
+    };
+    const uint64_t step = uint64_t(gridDim.x) * TEAMS;
+    request(uint64_t(blockIdx.x) * TEAMS + mine);
+    FVec<VEC>* wl = reinterpret_cast<FVec<VEC>*>(dynamic) + lane;   // vector j at wl[j * team]
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        dw[j] = db[j] = 0.f;
+        if (BLOCK || threadIdx.x < LANES) wl[j * team] = load_param<VEC>(a.weight, cols.at[j], 1.f);
+    }
+    __syncthreads();
+    uint32_t turn = 0;
+    for (uint64_t r0 = uint64_t(blockIdx.x) * TEAMS; r0 < a.rows; r0 += step) {
+        const uint64_t row = r0 + mine;
+        const bool live = row < a.rows;
+        const bool masked = cols.ragged || r0 + TEAMS > a.rows;   // some elements do not count
+        const float mean = nmean, rstd = nrstd;
+        FVec<VEC> h[NV], g[NV];
+        float sum = 0.f, along = 0.f;
+        asm volatile("" ::: "memory");   // the weight stays in LDS, not in registers across rows
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            h[j] = to_float<VEC, T>(nx[j]);
+            g[j] = to_float<VEC, T>(ng[j]);
+        }
+        if (r0 + step < a.rows) request(row + step);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const FVec<VEC> w = wl[j * team];
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
-                // past the row's end dy is 0: xhat does not count there
+                const bool out = masked && (!live || k < cols.skip[j]);
                 h[j][k] = (h[j][k] - mean) * rstd;
-                dw[j][k] = __builtin_fmaf(g[j][k], h[j][k], dw[j][k]);
-                db[j][k] += g[j][k];
-                g[j][k] *= w[j][k];
-                sum += g[j][k];
-                along = __builtin_fmaf(g[j][k], h[j][k], along);
+                const float d = out ? 0.f : g[j][k], hm = out ? 0.f : h[j][k];
+                dw[j][k] = __builtin_fmaf(d, hm, dw[j][k]);
+                db[j][k] += d;
+                g[j][k] *= w[k];
+                const float e = d * w[k];
+                sum += e;
+                along = __builtin_fmaf(e, hm, along);
             }
-        const float c1 = row_sum<LANES, BLOCK>(sum, slots[turn]) * a.inv_cols;
-        const float c2 = row_sum<LANES, BLOCK>(along, slots[turn + 1]) * a.inv_cols;
-        turn ^= 2;   // a slot is written again two barriers after its last reader
+        }
+        sum = team_sum<LANES>(sum);
+        along = team_sum<LANES>(along);
+        if (BLOCK) {
+            float* slot = slots[turn];
+            turn ^= 1;   // a slot is written again a barrier after its last reader
+            if ((threadIdx.x & 63) == 0) {
+                slot[threadIdx.x >> 6] = sum;
+                slot[8 + (threadIdx.x >> 6)] = along;
+            }
+            __syncthreads();
+            sum = along = 0.f;
+            for (uint32_t i = 0; i < blockDim.x / 64; ++i) {
+                sum += slot[i];
+                along += slot[8 + i];
+            }
+        }
         if (!live) continue;
+        const float c1 = sum * a.inv_cols, c2 = along * a.inv_cols;
         T* dx = static_cast<T*>(a.out) + row * a.out_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const uint32_t c = (j * team + lane) * VEC;
-            if (c >= a.cols) continue;
             FVec<VEC> o;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) o[k] = rstd * (g[j][k] - c1 - h[j][k] * c2);
-            store_cols<T, VEC>(dx, c, a.cols, o);
+            if (cols.skip[j] < VEC) stream_store<VEC>(dx + cols.at[j], from_float<T, VEC>(o));
         }
     }
     if (a.partial == nullptr) return;
     float* out = a.partial + uint64_t(blockIdx.x) * 2 * a.cols;
-    if (BLOCK) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const uint32_t c = (j * team + lane) * VEC;
-            store_cols<float, VEC>(out, c, a.cols, dw[j]);
-            store_cols<float, VEC>(out + a.cols, c, a.cols, db[j]);
-        }
-        return;
-    }
-    constexpr uint32_t SPAN = LANES * NV * VEC;   // columns a team holds
+    float* sums = BLOCK ? out : dynamic;
+    const uint32_t span = BLOCK ? a.cols : LANES * NV * VEC;   // from one row of sums to the next
+    __syncthreads();   // the weight has been read
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            const uint32_t c = (j * LANES + lane) * VEC + k;
-            joined[mine * SPAN + c] = dw[j][k];
-            joined[(TEAMS + mine) * SPAN + c] = db[j][k];
+            if (k < cols.skip[j]) continue;
+            sums[mine * span + cols.at[j] + k] = dw[j][k];
+            sums[(TEAMS + mine) * span + cols.at[j] + k] = db[j][k];
         }
+    if (BLOCK) return;
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < 2 * SPAN; i += 256) {
-        const uint32_t which = i / SPAN, c = i % SPAN;
-        if (c >= a.cols) continue;
+    for (uint32_t i = threadIdx.x; i < 2 * a.cols; i += 256) {
+        const uint32_t which = i >= a.cols, c = i - which * a.cols;
         float s = 0.f;
-        for (uint32_t t = 0; t < TEAMS; ++t) s += joined[(which * TEAMS + t) * SPAN + c];
-        out[which * a.cols + c] = s;
+        for (uint32_t t = 0; t < TEAMS; ++t) s += sums[(which * TEAMS + t) * span + c];
+        out[i] = s;
     }
 }
 
-// Rows past kNormRegCols columns.
+// Rows past kNormBackRegCols columns.
 template <typename T>
 __global__ __launch_bounds__(kNormWideThreads) void k_layer_norm_backward_wide(NormArgs a) {
     constexpr int VEC = norm_vec<T>();
@@ -304,26 +363,26 @@ __global__ __launch_bounds__(kNormWideThreads) void k_layer_norm_backward_wide(N
     T* dx = static_cast<T*>(a.out) + row * a.out_stride;
     const float mean = a.mean[row], rstd = a.rstd[row];
     float sum = 0.f, along = 0.f;
-    for (uint32_t c = threadIdx.x * VEC; c < a.cols; c += kNormWideThreads * VEC) {
-        const FVec<VEC> h = load_cols<T, VEC>(x, c, a.cols);
-        FVec<VEC> g = load_cols<T, VEC>(dy, c, a.cols);
-        if (a.weight) g *= load_cols<float, VEC>(a.weight, c, a.cols);
+    each_vector<T, VEC>(a.cols, [&](uint32_t at, int skip) {
+        const FVec<VEC> h = to_float<VEC, T>(load_any<VEC>(x + at));
+        const FVec<VEC> g = to_float<VEC, T>(load_any<VEC>(dy + at)) * load_param<VEC>(a.weight, at, 1.f);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
+            if (k < skip) continue;
             sum += g[k];
             along = __builtin_fmaf(g[k], (h[k] - mean) * rstd, along);
         }
-    }
+    });
     const float c1 = row_sum<64, true>(sum, slots[0]) * a.inv_cols;
     const float c2 = row_sum<64, true>(along, slots[1]) * a.inv_cols;
-    for (uint32_t c = threadIdx.x * VEC; c < a.cols; c += kNormWideThreads * VEC) {
-        const FVec<VEC> h = load_cols<T, VEC>(x, c, a.cols);
-        FVec<VEC> g = load_cols<T, VEC>(dy, c, a.cols), o;
-        if (a.weight) g *= load_cols<float, VEC>(a.weight, c, a.cols);
+    each_vector<T, VEC>(a.cols, [&](uint32_t at, int) {
+        const FVec<VEC> h = to_float<VEC, T>(load_any<VEC>(x + at));
+        const FVec<VEC> g = to_float<VEC, T>(load_any<VEC>(dy + at)) * load_param<VEC>(a.weight, at, 1.f);
+        FVec<VEC> o;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) o[k] = rstd * (g[k] - c1 - (h[k] - mean) * rstd * c2);
-        store_cols<T, VEC>(dx, c, a.cols, o);
-    }
+        store_any<VEC>(dx + at, from_float<T, VEC>(o));
+    });
 }
 
 // Their partial weight gradients: workgroup (x, y) adds rows y, y + gridDim.y,
@@ -344,25 +403,30 @@ __global__ __launch_bounds__(256) void k_norm_partial_wide(NormArgs a) {
     out[a.cols + c] = db;
 }
 
-// dweight (blockIdx.y 0) and dbias (1) from the n partial rows: 64 columns by
-// 16 groups of partial rows, in float64, joined in group order.
+// dweight (blockIdx.y 0) and dbias (1) from the n partial rows: 16 columns by
+// 64 groups of partial rows, in float64, joined in group order.
 __global__ __launch_bounds__(1024) void
 k_norm_weight_grad(const float* __restrict__ partial, uint32_t n, uint32_t cols, float* __restrict__ dweight,
                    float* __restrict__ dbias) {
-    __shared__ double part[16][64];
-    const uint32_t lane = threadIdx.x & 63, group = threadIdx.x >> 6;
-    const uint32_t c = blockIdx.x * 64 + lane;
+    __shared__ double part[64][16];
+    const uint32_t lane = threadIdx.x % 16, group = threadIdx.x / 16;
+    const uint32_t c = blockIdx.x * 16 + lane;
     double sum = 0.0;
     if (c < cols) {
         const float* p = partial + uint64_t(blockIdx.y) * cols + c;
-#pragma unroll 4
-        for (uint32_t i = group; i < n; i += 16) sum += double(p[uint64_t(i) * 2 * cols]);
+        float v[8];
+        for (uint32_t i0 = group; i0 < n; i0 += 8 * 64) {
+#pragma unroll
+            for (uint32_t u = 0; u < 8; ++u) v[u] = i0 + u * 64 < n ? p[uint64_t(i0 + u * 64) * 2 * cols] : 0.f;
+#pragma unroll
+            for (uint32_t u = 0; u < 8; ++u) sum += double(v[u]);
+        }
     }
     part[group][lane] = sum;
     __syncthreads();
-    if (group == 0 && c < cols) {
+    if (threadIdx.x < 16 && c < cols) {
         sum = 0.0;
-        for (int i = 0; i < 16; ++i) sum += part[i][lane];
+        for (int i = 0; i < 64; ++i) sum += part[i][lane];
         (blockIdx.y ? dbias : dweight)[c] = float(sum);
     }
 }

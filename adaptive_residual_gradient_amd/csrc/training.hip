@@ -243,44 +243,57 @@ int team_lanes(uint32_t cols, uint32_t vec) {
     return lanes;
 }
 
+// Workgroups for `need` shares of rows: at most `most`, each with as many shares as the others
+// but for one.
+uint32_t norm_blocks(uint64_t need, uint32_t most) {
+    const uint64_t turns = (need + most - 1) / most;
+    return static_cast<uint32_t>((need + turns - 1) / turns);
+}
+
+// The kernel of one row length: rows shorter than a vector by single elements, up to one
+// wavefront's columns by teams of its lanes, longer ones by whole workgroups.
+#define ADACOMP_NORM_TEAMS(LAUNCH)                                   \
+    do {                                                             \
+        if (a.cols < VEC) LAUNCH(1, 1, 8);                           \
+        else if (a.cols > 64 * VEC * 2) LAUNCH(VEC, NVMAX, 64);      \
+        else if (a.cols > 64 * VEC) LAUNCH(VEC, 2, 64);              \
+        else switch (team_lanes(a.cols, VEC)) {                      \
+            case 4: LAUNCH(VEC, 1, 4); break;                        \
+            case 8: LAUNCH(VEC, 1, 8); break;                        \
+            case 16: LAUNCH(VEC, 1, 16); break;                      \
+            case 32: LAUNCH(VEC, 1, 32); break;                      \
+            default: LAUNCH(VEC, 1, 64); break;                      \
+        }                                                            \
+    } while (0)
+
 template <typename T>
 void launch_norm(const adacomp::NormArgs& a, hipStream_t s) {
     using namespace adacomp;
-    constexpr uint32_t VEC = norm_vec<T>();
-    constexpr int NVMAX = kNormElems / int(VEC);
+    constexpr int VEC = norm_vec<T>(), NVMAX = kNormElems / VEC;
     const uint32_t rows = uint32_t(a.rows);
     if (a.cols > kNormRegCols) {
         hipLaunchKernelGGL(k_layer_norm_wide<T>, dim3(rows), dim3(kNormWideThreads), 0, s, a);
-        return;
-    }
-    if (a.cols > kNormWaveCols) {
+    } else if (a.cols > kNormWaveCols) {
         const uint32_t waves = (a.cols + kNormWaveCols - 1) / kNormWaveCols;
-        hipLaunchKernelGGL((k_layer_norm<T, NVMAX, 64, true>), dim3(rows), dim3(64 * waves), 0, s, a);
-        return;
-    }
-#define ADACOMP_LN(NV, LANES) \
-    hipLaunchKernelGGL((k_layer_norm<T, NV, LANES, false>), dim3((rows + 256 / LANES - 1) / (256 / LANES)), dim3(256), 0, s, a)
-    if (a.cols > 64 * VEC * 2) ADACOMP_LN(NVMAX, 64);
-    else if (a.cols > 64 * VEC) ADACOMP_LN(2, 64);
-    else switch (team_lanes(a.cols, VEC)) {
-        case 4: ADACOMP_LN(1, 4); break;
-        case 8: ADACOMP_LN(1, 8); break;
-        case 16: ADACOMP_LN(1, 16); break;
-        case 32: ADACOMP_LN(1, 32); break;
-        default: ADACOMP_LN(1, 64); break;
-    }
+        hipLaunchKernelGGL((k_layer_norm<T, VEC, NVMAX, 64, true>), dim3(norm_blocks(rows, kNormMaxWaves / waves)),
+                           dim3(64 * waves), 0, s, a);
+    } else {
+#define ADACOMP_LN(V, NV, LANES)                                                              \
+    hipLaunchKernelGGL((k_layer_norm<T, V, NV, LANES, false>),                                \
+                       dim3(norm_blocks((rows + 256 / LANES - 1) / (256 / LANES), kNormMaxWaves / 4)), dim3(256), 0, \
+                       s, a)
+        ADACOMP_NORM_TEAMS(ADACOMP_LN);
 #undef ADACOMP_LN
+    }
 }
 
 // Returns the number of partial rows written.
 template <typename T>
 uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
     using namespace adacomp;
-    constexpr uint32_t VEC = norm_vec<T>();
-    constexpr int NVMAX = kNormElems / int(VEC);
-    const uint32_t rows = uint32_t(a.rows);
-    const uint32_t most = norm_partials(a.rows);
-    if (a.cols > kNormRegCols) {
+    constexpr int VEC = norm_vec<T>(), NVMAX = kNormElems / VEC;
+    const uint32_t rows = uint32_t(a.rows), most = norm_partials(a.rows);
+    if (a.cols > kNormBackRegCols) {
         hipLaunchKernelGGL(k_layer_norm_backward_wide<T>, dim3(rows), dim3(kNormWideThreads), 0, s, a);
         if (a.partial == nullptr) return 0;
         const uint32_t n = std::min(most, 64u);
@@ -289,27 +302,23 @@ uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
     }
     if (a.cols > kNormWaveCols) {
         const uint32_t waves = (a.cols + kNormWaveCols - 1) / kNormWaveCols;
-        hipLaunchKernelGGL((k_layer_norm_backward<T, NVMAX, 64, true>), dim3(most), dim3(64 * waves), 0, s, a);
-        return most;
+        const uint32_t n = norm_blocks(rows, std::min(most, kNormMaxPartials * 4 / waves));
+        hipLaunchKernelGGL((k_layer_norm_backward<T, VEC, NVMAX, 64, true>), dim3(n), dim3(64 * waves),
+                           4 * kNormWaveCols * waves, s, a);
+        return n;
     }
     uint32_t n = 0;
-#define ADACOMP_LNB(NV, LANES)                                                        \
-    do {                                                                              \
-        n = std::min<uint32_t>((rows + 256 / LANES - 1) / (256 / LANES), most);       \
-        hipLaunchKernelGGL((k_layer_norm_backward<T, NV, LANES, false>), dim3(n), dim3(256), 0, s, a); \
+#define ADACOMP_LNB(V, NV, LANES)                                                               \
+    do {                                                                                        \
+        n = norm_blocks((rows + 256 / LANES - 1) / (256 / LANES), most);                        \
+        hipLaunchKernelGGL((k_layer_norm_backward<T, V, NV, LANES, false>), dim3(n), dim3(256), \
+                           2 * 4 * 256 * NV * V, s, a);                                         \
     } while (0)
-    if (a.cols > 64 * VEC * 2) ADACOMP_LNB(NVMAX, 64);
-    else if (a.cols > 64 * VEC) ADACOMP_LNB(2, 64);
-    else switch (team_lanes(a.cols, VEC)) {
-        case 4: ADACOMP_LNB(1, 4); break;
-        case 8: ADACOMP_LNB(1, 8); break;
-        case 16: ADACOMP_LNB(1, 16); break;
-        case 32: ADACOMP_LNB(1, 32); break;
-        default: ADACOMP_LNB(1, 64); break;
-    }
+    ADACOMP_NORM_TEAMS(ADACOMP_LNB);
 #undef ADACOMP_LNB
     return n;
 }
+#undef ADACOMP_NORM_TEAMS
 
 }  // namespace
 
@@ -416,7 +425,7 @@ int adacomp_layer_norm_backward(const void* dy, uint64_t dy_stride, const void* 
         if ((st = launch_status()) != ADACOMP_OK) return st;
     }
     if (sums) {
-        hipLaunchKernelGGL(adacomp::k_norm_weight_grad, dim3((cols + 63) / 64, 2), dim3(1024), 0, s, a.partial, n,
+        hipLaunchKernelGGL(adacomp::k_norm_weight_grad, dim3((cols + 15) / 16, 2), dim3(1024), 0, s, a.partial, n,
                            cols, dweight, dbias);
         st = launch_status();
     }
