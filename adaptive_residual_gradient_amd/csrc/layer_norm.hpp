@@ -22,7 +22,7 @@ constexpr uint32_t kNormWaveCols = 64 * kNormElems;       // one wavefront's col
 constexpr uint32_t kNormRegCols = 16 * kNormWaveCols;     // a workgroup's
 constexpr uint32_t kNormMaxWaves = 4096;                  // wavefronts of a forward launch
 constexpr uint32_t kNormBackRegCols = 8 * kNormWaveCols;
-constexpr uint32_t kNormMaxPartials = 1024;               // workgroups of the weight gradients
+constexpr uint32_t kNormMaxPartials = 512;                // workgroups of the weight gradients
 constexpr uint32_t kNormWideThreads = 1024;
 
 struct NormArgs {
@@ -236,8 +236,9 @@ __global__ __launch_bounds__(kNormWideThreads) void k_layer_norm_wide(NormArgs a
 // in registers; the workgroup's teams are joined in LDS in team order and
 // written as one partial row pair, which k_norm_weight_grad adds up.  The next
 // row is requested before the present one is joined, and the weight waits in
-// LDS, for registers decide how many wavefronts keep a row in flight.  A team
-// is LANES lanes of a wavefront or, BLOCK, a workgroup.
+// LDS, for registers decide how many wavefronts keep a row in flight; it is 0
+// there in columns that another lane holds, which takes them out of the row's
+// sums.  A team is LANES lanes of a wavefront or, BLOCK, a workgroup.
 template <typename T, int VEC, int NV, int LANES, bool BLOCK>
 __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormArgs a) {
     typedef typename Packed<T, VEC>::V V;
@@ -250,16 +251,25 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
     FVec<VEC> dw[NV], db[NV];
     V nx[NV], ng[NV];
     float nmean, nrstd;
+    // The statistics take vector loads, in order with the row's: scalar ones would be waited for with
+    // the weight's LDS reads, a row too early.
+    uint32_t zero;
+    asm("v_mov_b32 %0, 0" : "=v"(zero));
     auto request = [&](uint64_t row) {   // past the last row: the last row again
         const uint64_t r = min(row, a.rows - 1);
-        nmean = a.mean[r];
-        nrstd = a.rstd[r];
+        nmean = a.mean[r + zero];
+        nrstd = a.rstd[r + zero];
         const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
         const T* dy = static_cast<const T*>(a.dy) + r * a.dy_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             nx[j] = stream_load<VEC>(x + cols.at[j]);
             ng[j] = stream_load<VEC>(dy + cols.at[j]);
+        }
+        if (LANES < 64 && row >= a.rows) {   // a team without a row beside teams that have one
+            nmean = nrstd = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) nx[j] = ng[j] = V{};
         }
     };
     const uint64_t step = uint64_t(gridDim.x) * TEAMS;
@@ -268,14 +278,16 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         dw[j] = db[j] = 0.f;
-        if (BLOCK || threadIdx.x < LANES) wl[j * team] = load_param<VEC>(a.weight, cols.at[j], 1.f);
+        FVec<VEC> w = load_param<VEC>(a.weight, cols.at[j], 1.f);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) w[k] = k < cols.skip[j] ? 0.f : w[k];
+        if (BLOCK || threadIdx.x < LANES) wl[j * team] = w;
     }
     __syncthreads();
     uint32_t turn = 0;
     for (uint64_t r0 = uint64_t(blockIdx.x) * TEAMS; r0 < a.rows; r0 += step) {
         const uint64_t row = r0 + mine;
-        const bool live = row < a.rows;
-        const bool masked = cols.ragged || r0 + TEAMS > a.rows;   // some elements do not count
+        if (LANES == 64 && !BLOCK && row >= a.rows) break;
         const float mean = nmean, rstd = nrstd;
         FVec<VEC> h[NV], g[NV];
         float sum = 0.f, along = 0.f;
@@ -291,15 +303,12 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
             const FVec<VEC> w = wl[j * team];
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
-                const bool out = masked && (!live || k < cols.skip[j]);
                 h[j][k] = (h[j][k] - mean) * rstd;
-                const float d = out ? 0.f : g[j][k], hm = out ? 0.f : h[j][k];
-                dw[j][k] = __builtin_fmaf(d, hm, dw[j][k]);
-                db[j][k] += d;
+                dw[j][k] = __builtin_fmaf(g[j][k], h[j][k], dw[j][k]);
+                db[j][k] += g[j][k];
                 g[j][k] *= w[k];
-                const float e = d * w[k];
-                sum += e;
-                along = __builtin_fmaf(e, hm, along);
+                sum += g[j][k];
+                along = __builtin_fmaf(g[j][k], h[j][k], along);
             }
         }
         sum = team_sum<LANES>(sum);
@@ -318,7 +327,7 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
                 along += slot[8 + i];
             }
         }
-        if (!live) continue;
+        if (row >= a.rows) continue;
         const float c1 = sum * a.inv_cols, c2 = along * a.inv_cols;
         T* dx = static_cast<T*>(a.out) + row * a.out_stride;
 #pragma unroll
@@ -326,7 +335,14 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
             FVec<VEC> o;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) o[k] = rstd * (g[j][k] - c1 - h[j][k] * c2);
-            if (cols.skip[j] < VEC) stream_store<VEC>(dx + cols.at[j], from_float<T, VEC>(o));
+            const V out = from_float<T, VEC>(o);
+            if (cols.skip[j] == 0) {
+                stream_store<VEC>(dx + cols.at[j], out);
+            } else {
+#pragma unroll
+                for (int k = 1; k < VEC; ++k)
+                    if (k >= cols.skip[j]) dx[cols.at[j] + k] = out[k];
+            }
         }
     }
     if (a.partial == nullptr) return;
