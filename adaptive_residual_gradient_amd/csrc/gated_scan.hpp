@@ -11,7 +11,7 @@
 // state and gate product stay in registers between the two halves, so inputs
 // are read once and results written once.  The tile's threads join their
 // steps through LDS.  The state travels from tile to tile
-//   - not at all, where one tile holds the whole sequence (kScanWhole);
+//   - not at all, where one tile holds the whole sequence (kScanCarry alone);
 //   - through one 8-byte word a channel that each tile leaves for its
 //     successor (kScanChain), where there are enough independent chains of
 //     tiles to hide that hop;
@@ -34,7 +34,7 @@ constexpr uint32_t kScanShort = 16;     // longest sequence of the short kernels
 constexpr uint32_t kScanThreads = 512;  // most threads of a tile
 constexpr uint32_t kScanQueues = 64;    // tickets of kScanChain
 constexpr uint32_t kScanCountBytes = kScanQueues * 64;   // each on a line of its own
-constexpr int kScanWhole = 0, kScanSum = 1, kScanCarry = 2, kScanChain = 3;
+constexpr int kScanSum = 0, kScanCarry = 1, kScanChain = 2;
 
 struct ScanView {
     void* p;
@@ -48,7 +48,7 @@ struct ScanArgs {
     float* last;             // h_last or dh0; nullable
     const int32_t* lengths;  // nullable
     uint32_t* tickets;       // kScanChain
-    uint64_t* words;         // kScanChain: [chain][tile][slot] {state, 1 once it is there}
+    uint32_t* words;         // kScanChain: [chain][tile][slot] the state, kScanEmpty until it is there
     float* agg_a;            // kScanSum, kScanCarry: [chain][tile][slot]
     float* agg_s;            // the same; then the carried states
     uint64_t length;
@@ -96,129 +96,114 @@ __device__ __forceinline__ T* view_at(const ScanView& v, uint32_t b, uint64_t t,
 
 // ---- tiles ----
 
-// The state of slot `s` that the predecessor left.  It is there sooner or
-// later: a tile waits only for tiles whose tickets were taken before its own,
-// so the earliest unfinished one waits for nobody.  The count bounds the wait
-// all the same; past it (seconds) the results become NaN.
-__device__ __forceinline__ float wait_for_state(const uint64_t* word) {
+// Non-temporal accesses where every row starts on a cache line; elsewhere the
+// lines at a tile's edges serve the neighbouring channels' tiles as well, which
+// run on the same chiplet, and have to stay in its cache.
+template <int N, bool NT, typename T>
+__device__ __forceinline__ typename Packed<T, N>::V load_hint(const T* p) {
+    return NT ? stream_load<N>(p) : load_any<N>(p);
+}
+template <int N, bool NT, typename T>
+__device__ __forceinline__ void store_hint(T* p, typename Packed<T, N>::V v) {
+    if (NT) stream_store<N>(p, v);
+    else store_any<N>(p, v);
+}
+
+// A state on its way to the next tile: its bits, of which this NaN's stand for
+// "not there yet".
+constexpr uint32_t kScanEmpty = 0xFFFFFFFFu;
+__device__ __forceinline__ void leave_state(uint32_t* word, float s) {
+    const uint32_t bits = __float_as_uint(s);
+    __hip_atomic_store(word, bits == kScanEmpty ? 0x7FC00000u : bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The state that the predecessor leaves.  It is there sooner or later: a tile
+// waits only for tiles whose tickets were taken before its own, so the earliest
+// unfinished one waits for nobody.  The count bounds the wait all the same;
+// past it (seconds) the results become NaN.
+__device__ __forceinline__ float wait_for_state(const uint32_t* word) {
     for (uint32_t i = 0; i < (1u << 22); ++i) {
-        const uint64_t w = __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (w >> 32) return __uint_as_float(uint32_t(w));
+        const uint32_t w = __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (w != kScanEmpty) return __uint_as_float(w);
         __builtin_amdgcn_s_sleep(1);
     }
     return __builtin_nanf("");
 }
 
-// One thread's pointers step through time; where the channels are no multiple
-// of the vector the last lanes move back and repeat their neighbours'
-// channels, with the same results.
-template <typename T, int VW, bool SIG, bool BACK, int MODE>
-__global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
+// Workgroups go to the 8 chiplets in turn.  Of 64 consecutive ones each
+// chiplet's eight take eight neighbouring chains: neighbouring channels of the
+// same rows.
+__device__ __forceinline__ uint32_t chiplet_order(uint32_t i) { return (i & ~63u) | (i & 7u) << 3 | (i >> 3 & 7u); }
+
+// A tile's place.
+struct ScanTile {
+    uint32_t chain, b, k, slot0;      // slot0: the channel of the group's first slot
+    uint64_t tend;                    // the tile's steps of the sequence end here
+    uint32_t count;                   // and are so many
+    bool first, last;                 // first: nothing is carried in but the given state;
+                                      // last: the state carried out is the call's
+};
+
+// One tile.  FULL: every thread has all its steps.  Else those past the
+// sequence's end read the last one again and leave the state as it is, so that
+// no load stands under a condition (one that does is waited for at once).
+// Where the channels are no multiple of the vector the last lanes move back and
+// repeat their neighbours' channels, with the same results.
+template <typename T, int VW, bool SIG, bool BACK, int MODE, bool NT, bool FULL>
+__device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& tile, float* sa, float* ss) {
     typedef typename Packed<T, VW>::V V;
-    constexpr int kScanSteps = scan_thread_steps(BACK);
-    __shared__ float sa[kScanThreads * VW], ss[kScanThreads * VW];   // [sub-chunk][slot]
-    __shared__ uint32_t ticket;
-    const uint32_t tid = threadIdx.x, R = a.lanes, slots = R * VW;
-    const uint32_t r = tid % R, g = tid / R, G = blockDim.x / R;
-    uint32_t chain, k;   // k: the tile along the chain's direction of travel
-    if (MODE == kScanChain) {
-        const uint32_t q = blockIdx.x % kScanQueues;
-        const uint32_t chains = a.batch * a.groups, mine = (chains - q + kScanQueues - 1) / kScanQueues;
-        if (tid == 0)
-            ticket = __hip_atomic_fetch_add(a.tickets + q * 16, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        const uint32_t n = ticket;
-        if (n >= mine * a.tiles) return;
-        chain = q + kScanQueues * (n % mine);
-        k = n / mine;
-    } else {
-        chain = blockIdx.x % (a.batch * a.groups);
-        k = blockIdx.x / (a.batch * a.groups);
-    }
-    const uint32_t b = chain / a.groups, group = chain % a.groups;
-    if (BACK) k = a.tiles - 1 - k;
-    const uint64_t n = scan_steps(a, b);
-    const uint64_t t0 = uint64_t(k) * a.steps;
-    const uint64_t t1 = t0 + a.steps < a.length ? t0 + a.steps : a.length;
-    const uint64_t tend = t1 < n ? t1 : (t0 < n ? n : t0);   // the tile's steps of the sequence end here
-    const uint32_t count = uint32_t(tend - t0);
-    const uint32_t c = min(group * slots + r * VW, a.channels - VW);
-
-    // zeros past the sequence's end
-    if (MODE != kScanSum && tend < t1) {
-        const V zero = {};
-        for (uint64_t t = tend + g; t < t1; t += G) {
-            if (BACK) {
-                store_any<VW>(view_at<T>(a.dgate, b, t, c), zero);
-                store_any<VW>(view_at<T>(a.dx, b, t, c), zero);
-            } else {
-                store_any<VW>(view_at<T>(a.h, b, t, c), zero);
-            }
-        }
-    }
-    const bool first = BACK ? tend == n : k == 0;    // nothing is carried in but the given state
-    const bool last = BACK ? k == 0 : tend == n;     // the carried-out state is the call's
-    if (count == 0 && !(n == 0 && k == 0)) return;   // no step of the sequence (an empty one has its tile 0)
-
-    // position i of the direction of travel is step t0 + i, or tend - 1 - i
-    const int64_t dir = BACK ? -1 : 1;
-    const uint32_t i0 = g * kScanSteps;
-    const uint64_t ta = BACK ? tend - 1 - i0 : t0 + i0;   // wraps where the thread has no step
-    const int left = int(count) - int(i0);               // steps the thread has
-    V zr[kScanSteps], xr[kScanSteps];
-    {
-        const T* z = view_at<T>(a.gate, b, ta, c);
-        const T* x = view_at<T>(BACK ? a.dh : a.x, b, ta, c);
-        const int64_t zs = dir * int64_t(a.gate.ts), xs = dir * int64_t(BACK ? a.dh.ts : a.x.ts);
-        if (left >= kScanSteps) {
-#pragma unroll
-            for (int u = 0; u < kScanSteps; ++u) {
-                zr[u] = load_any<VW>(z + u * zs);
-                xr[u] = load_any<VW>(x + u * xs);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < kScanSteps; ++u) {
-                zr[u] = xr[u] = V{};
-                if (u < left) {
-                    zr[u] = load_any<VW>(z + u * zs);
-                    xr[u] = load_any<VW>(x + u * xs);
-                }
-            }
-        }
-    }
-    // what the gradients need besides, requested before the wait
+    constexpr int N = scan_thread_steps(BACK);
     constexpr bool kGrad = BACK && MODE != kScanSum;
-    V hr[kGrad ? kScanSteps : 1], ur[kGrad && SIG ? kScanSteps : 1];
-    if (kGrad) {
-        const T* h = view_at<T>(a.h, b, ta - 1, c);
-        const T* x = SIG ? view_at<T>(a.x, b, ta, c) : nullptr;
+    const uint32_t tid = threadIdx.x, R = a.lanes, slots = R * VW;
+    const uint32_t r = tid % R, g = tid / R, G = blockDim.x / R, b = tile.b;
+    const uint32_t c = min(tile.slot0 + r * VW, a.channels - VW);
+    // position i of the direction of travel is step t0 + i, or tend - 1 - i
+    const uint32_t i0 = g * N;
+    const int left = FULL ? N : int(tile.count) - int(i0);   // steps the thread has
+    const uint32_t at = FULL ? i0 : min(i0, tile.count - 1);
+    const uint64_t ta = BACK ? tile.tend - 1 - at : tile.tend - tile.count + at;
+    auto walk = [&](const ScanView& view, uint64_t t, V(&v)[N]) {
+        const T* p = view_at<T>(view, b, t, c);
+        const int64_t step = BACK ? -int64_t(view.ts) : int64_t(view.ts);
 #pragma unroll
-        for (int u = 0; u < kScanSteps; ++u) {
-            hr[kGrad ? u : 0] = V{};
-            if (SIG) ur[kGrad && SIG ? u : 0] = V{};
-            if (u < left) {
-                // step 0 has no earlier state in h
-                if (ta != uint64_t(u)) hr[kGrad ? u : 0] = load_any<VW>(h - u * int64_t(a.h.ts));
-                if (SIG) ur[kGrad && SIG ? u : 0] = load_any<VW>(x - u * int64_t(a.x.ts));
-            }
+        for (int u = 0; u < N; ++u) {
+            v[u] = load_hint<VW, NT>(p);
+            if (u + 1 < N) p += FULL || u + 1 < left ? step : 0;
         }
+    };
+    V zr[N], xr[N], hr[N], ur[N];
+    walk(a.gate, ta, zr);
+    walk(BACK ? a.dh : a.x, ta, xr);
+    FVec<VW> h0 = 0.f;
+    if (kGrad) {   // requested before the wait
+        if (SIG) walk(a.x, ta, ur);
+        // the earlier states, the given one before step 0 (whose place reads step 0's)
+        const T* p = view_at<T>(a.h, b, ta, c);
+        uint64_t t = ta;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            if ((FULL || u < left) && t > 0) {
+                p -= a.h.ts;
+                --t;
+            }
+            hr[u] = load_hint<VW, NT>(p);
+        }
+        if (tile.k == 0 && a.h0) h0 = load_any<VW>(a.h0 + uint64_t(b) * a.channels + c);
     }
 
     // the thread's steps composed: s the state from 0, p the product of gates.  Backward keeps
-    // what reaches step t: q = dh + s before it, and p before it.
-    FVec<VW> S = 0.f, P = 1.f, sv[kScanSteps], pv[kScanSteps];
+    // what reaches step t: dh + s before it, and p before it.
+    FVec<VW> S = 0.f, P = 1.f, sv[N], pv[N];
 #pragma unroll
-    for (int u = 0; u < kScanSteps; ++u) {
+    for (int u = 0; u < N; ++u) {
         const FVec<VW> z = to_float<VW, T>(zr[u]), x = to_float<VW, T>(xr[u]);
 #pragma unroll
         for (int v = 0; v < VW; ++v) {
             float f, m;
             gates<T, SIG>(z[v], f, m);
-            const bool on = u < left;
-            f = on ? f : 1.f;     // steps past the end leave the state as it is
+            const bool on = FULL || u < left;
+            f = on ? f : 1.f;
             if (BACK) {
-                const float l = x[v] + S[v];   // x is 0 there
+                const float l = (on ? x[v] : 0.f) + S[v];
                 sv[u][v] = l;
                 pv[u][v] = P[v];
                 S[v] = f * l;
@@ -245,28 +230,26 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
             C = __builtin_fmaf(f, C, ss[i * slots + tid]);
             A *= f;
         }
-        const uint64_t at = (uint64_t(chain) * a.tiles + k) * slots + tid;
+        const uint64_t word = (uint64_t(tile.chain) * a.tiles + tile.k) * slots + tid;
         if (MODE == kScanSum) {
-            a.agg_a[at] = A;
-            a.agg_s[at] = C;
+            a.agg_a[word] = A;
+            a.agg_s[word] = C;
             return;
         }
-        const uint32_t sc = min(group * slots + tid / VW * VW, a.channels - VW) + tid % VW;   // the slot's channel
+        const uint32_t sc = min(tile.slot0 + tid / VW * VW, a.channels - VW) + tid % VW;   // the slot's channel
         const uint64_t state = uint64_t(b) * a.channels + sc;
         float s = 0.f;
-        if (first) {
+        if (tile.first) {
             const float* start = BACK ? a.dh_last : a.h0;
             if (start) s = start[state];
         } else if (MODE == kScanCarry) {
-            s = a.agg_s[at];
+            s = a.agg_s[word];
         } else if (MODE == kScanChain) {
-            s = wait_for_state(a.words + (BACK ? at + slots : at - slots));
+            s = wait_for_state(a.words + (BACK ? word + slots : word - slots));
         }
         const float out = __builtin_fmaf(A, s, C);
-        if (MODE == kScanChain && !last)
-            __hip_atomic_store(a.words + at, (uint64_t(1) << 32) | __float_as_uint(out), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-        if (last && a.last) a.last[state] = count ? out : s;
+        if (MODE == kScanChain && !tile.last) leave_state(a.words + word, out);
+        if (tile.last && a.last) a.last[state] = out;
         // the state each sub-chunk starts from takes the place of its product
 #pragma unroll 8
         for (uint32_t i = 0; i < G; ++i) {
@@ -283,24 +266,23 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
     if (!BACK) {
         T* h = view_at<T>(a.h, b, ta, c);
 #pragma unroll
-        for (int u = 0; u < kScanSteps; ++u) {
+        for (int u = 0; u < N; ++u) {
             FVec<VW> o;
 #pragma unroll
             for (int v = 0; v < VW; ++v) o[v] = __builtin_fmaf(pv[u][v], s[v], sv[u][v]);
-            if (u < left) store_any<VW>(h + u * a.h.ts, from_float<T, VW>(o));
+            if (FULL || u < left) store_hint<VW, NT>(h, from_float<T, VW>(o));
+            h += a.h.ts;
         }
     } else {
         T* dg = view_at<T>(a.dgate, b, ta, c);
         T* dx = view_at<T>(a.dx, b, ta, c);
 #pragma unroll
-        for (int u = 0; u < kScanSteps; ++u) {
-            if (u >= left) continue;
-            FVec<VW> z = to_float<VW, T>(zr[u]), before = to_float<VW, T>(hr[kGrad ? u : 0]), og, ox;
-            if (ta == uint64_t(u)) {
-                before = 0.f;
-                if (a.h0) before = load_any<VW>(a.h0 + uint64_t(b) * a.channels + c);
-            }
-            if (SIG) before -= to_float<VW, T>(ur[kGrad && SIG ? u : 0]);
+        for (int u = 0; u < N; ++u) {
+            const FVec<VW> z = to_float<VW, T>(zr[u]);
+            FVec<VW> before = to_float<VW, T>(hr[u]), og, ox;
+            // only a tile's last thread can hold step 0, as its last step
+            if (!FULL || u == N - 1) before = ta == uint64_t(u) ? h0 : before;
+            if (SIG) before -= to_float<VW, T>(ur[u]);
 #pragma unroll
             for (int v = 0; v < VW; ++v) {
                 float f, m;
@@ -309,16 +291,79 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
                 og[v] = SIG ? l * before[v] * f * m : l * before[v];
                 ox[v] = l * m;
             }
-            store_any<VW>(dg - u * int64_t(a.dgate.ts), from_float<T, VW>(og));
-            store_any<VW>(dx - u * int64_t(a.dx.ts), from_float<T, VW>(ox));
+            if (FULL || u < left) {
+                store_hint<VW, NT>(dg, from_float<T, VW>(og));
+                store_hint<VW, NT>(dx, from_float<T, VW>(ox));
+            }
+            dg -= a.dgate.ts;
+            dx -= a.dx.ts;
         }
     }
 }
 
-// Clears the tickets and words of kScanChain.
+template <typename T, int VW, bool SIG, bool BACK, int MODE, bool NT>
+__global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
+    __shared__ float sa[kScanThreads * VW], ss[kScanThreads * VW];   // [sub-chunk][slot]
+    __shared__ uint32_t ticket;
+    const uint32_t tid = threadIdx.x, slots = a.lanes * VW;
+    ScanTile tile;
+    uint32_t k;   // along the direction of travel
+    if (MODE == kScanChain) {
+        const uint32_t q = blockIdx.x % kScanQueues;
+        const uint32_t chains = a.batch * a.groups, mine = (chains - chiplet_order(q) + kScanQueues - 1) / kScanQueues;
+        if (tid == 0)
+            ticket = __hip_atomic_fetch_add(a.tickets + q * 16, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        const uint32_t n = __builtin_amdgcn_readfirstlane(ticket);
+        if (n >= mine * a.tiles) return;
+        tile.chain = chiplet_order(q) + kScanQueues * (n % mine);
+        k = n / mine;
+    } else {
+        const uint32_t chains = a.batch * a.groups, i = blockIdx.x % chains;
+        tile.chain = i < (chains & ~63u) ? chiplet_order(i) : i;
+        k = blockIdx.x / chains;
+    }
+    tile.b = tile.chain / a.groups;
+    tile.slot0 = tile.chain % a.groups * slots;
+    tile.k = BACK ? a.tiles - 1 - k : k;
+    const uint64_t n = scan_steps(a, tile.b);
+    const uint64_t t0 = uint64_t(tile.k) * a.steps;
+    const uint64_t t1 = t0 + a.steps < a.length ? t0 + a.steps : a.length;
+    tile.tend = t1 < n ? t1 : (t0 < n ? n : t0);
+    tile.count = uint32_t(tile.tend - t0);
+    tile.first = BACK ? tile.tend == n : tile.k == 0;
+    tile.last = BACK ? tile.k == 0 : tile.tend == n;
+
+    // zeros past the sequence's end
+    if (MODE != kScanSum && tile.tend < t1) {
+        const uint32_t r = tid % a.lanes, c = min(tile.slot0 + r * VW, a.channels - VW);
+        const typename Packed<T, VW>::V zero = {};
+        for (uint64_t t = tile.tend + tid / a.lanes; t < t1; t += blockDim.x / a.lanes) {
+            if (BACK) {
+                store_hint<VW, NT>(view_at<T>(a.dgate, tile.b, t, c), zero);
+                store_hint<VW, NT>(view_at<T>(a.dx, tile.b, t, c), zero);
+            } else {
+                store_hint<VW, NT>(view_at<T>(a.h, tile.b, t, c), zero);
+            }
+        }
+    }
+    if (tile.count == a.steps) {
+        scan_tile<T, VW, SIG, BACK, MODE, NT, true>(a, tile, sa, ss);
+    } else if (tile.count > 0) {
+        scan_tile<T, VW, SIG, BACK, MODE, NT, false>(a, tile, sa, ss);
+    } else if (n == 0 && tile.k == 0 && a.last && MODE != kScanSum && tid < slots) {   // an empty sequence
+        const uint32_t c = min(tile.slot0 + tid / VW * VW, a.channels - VW) + tid % VW;
+        const uint64_t state = uint64_t(tile.b) * a.channels + c;
+        const float* start = BACK ? a.dh_last : a.h0;
+        a.last[state] = start ? start[state] : 0.f;
+    }
+}
+
+// Makes the tickets (the first kScanCountBytes) 0 and the words of kScanChain empty.
 __global__ __launch_bounds__(256) void k_scan_clear(uint4* p, uint64_t n) {
-    for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += uint64_t(gridDim.x) * 256)
-        p[i] = uint4{0, 0, 0, 0};
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t v = i < kScanCountBytes / 16 ? 0u : kScanEmpty;
+    if (i < n) p[i] = uint4{v, v, v, v};
 }
 
 // agg_s becomes the state carried into each tile: a workgroup takes one chain,

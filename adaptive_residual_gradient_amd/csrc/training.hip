@@ -463,7 +463,7 @@ ScanLayout scan_layout(const adacomp_scan_shape& s, uint32_t vw, bool back) {
         return l;
     }
     l.lanes = 4;
-    while (l.lanes < 32 && l.lanes * vw < s.channels) l.lanes *= 2;
+    while (l.lanes < 64 && l.lanes * vw < s.channels) l.lanes *= 2;
     l.groups = (s.channels + l.lanes * vw - 1) / (l.lanes * vw);
     uint32_t subs = std::max(64 / l.lanes, 2u);
     while (subs * l.lanes < kScanThreads && uint64_t(subs) * per < s.length) subs *= 2;
@@ -471,8 +471,8 @@ ScanLayout scan_layout(const adacomp_scan_shape& s, uint32_t vw, bool back) {
     l.steps = subs * per;
     l.tiles = static_cast<uint32_t>((s.length + l.steps - 1) / l.steps);
     const uint64_t chains = uint64_t(s.batch) * l.groups;
-    l.chain = chains >= kScanQueues;
-    // a word of 8 bytes, or two floats, of every slot
+    l.chain = l.tiles > 1 && chains >= kScanQueues;
+    // two floats, or one word, of every slot
     if (l.tiles > 1) l.ws = kScanCountBytes + chains * l.tiles * l.lanes * vw * 8;
     return l;
 }
@@ -569,6 +569,43 @@ int check_scan(const ScanCall& c) {
     return ADACOMP_OK;
 }
 
+// Whether every step of every view the call touches starts on a cache line.
+bool scan_lines(const adacomp::ScanArgs& a, uint64_t size) {
+    for (const adacomp::ScanView* v : {&a.gate, &a.x, &a.h, &a.dh, &a.dgate, &a.dx})
+        if (v->p && (!aligned_to(v->p, 128) || v->ts * size % 128 != 0 || v->bs * size % 128 != 0)) return false;
+    return true;
+}
+
+template <typename T, int VW, bool SIG, bool BACK, bool NT>
+int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t s) {
+    using namespace adacomp;
+    const uint64_t chains = uint64_t(a.batch) * l.groups, n = chains * l.tiles;
+    // work-items of one launch must fit in 32 bits (the queues round the chains up)
+    if ((chains + kScanQueues) * l.tiles * l.threads >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;
+    const dim3 block(l.threads);
+    if (l.chain) {
+        const uint64_t vecs = (kScanCountBytes + n * l.lanes * VW * 4 + 15) / 16;
+        a.tickets = static_cast<uint32_t*>(ws);
+        a.words = a.tickets + kScanCountBytes / 4;
+        hipLaunchKernelGGL(k_scan_clear, dim3(uint32_t((vecs + 255) / 256)), dim3(256), 0, s, static_cast<uint4*>(ws),
+                           vecs);
+        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+        const uint64_t grid = (chains + kScanQueues - 1) / kScanQueues * kScanQueues * l.tiles;
+        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain, NT>), dim3(uint32_t(grid)), block, 0, s, a);
+        return launch_status();
+    }
+    if (l.tiles > 1) {
+        a.agg_a = static_cast<float*>(ws);
+        a.agg_s = a.agg_a + n * l.lanes * VW;
+        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanSum, false>), dim3(uint32_t(n)), block, 0, s, a);
+        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+        hipLaunchKernelGGL(k_scan_carry<BACK>, dim3(uint32_t(chains)), dim3(1024), 0, s, a, uint32_t(VW));
+        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    }
+    hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanCarry, NT>), dim3(uint32_t(n)), block, 0, s, a);
+    return launch_status();
+}
+
 template <typename T, int VW, bool SIG, bool BACK>
 int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t s) {
     using namespace adacomp;
@@ -577,33 +614,8 @@ int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t
         hipLaunchKernelGGL((k_scan_short<T, VW, SIG, BACK>), dim3(uint32_t(blocks)), dim3(256), 0, s, a);
         return launch_status();
     }
-    const uint64_t chains = uint64_t(a.batch) * l.groups, n = chains * l.tiles;
-    // work-items of one launch must fit in 32 bits (the queues round the chains up)
-    if ((chains + kScanQueues) * l.tiles * l.threads >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;
-    const dim3 block(l.threads);
-    if (l.tiles == 1) {
-        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanWhole>), dim3(uint32_t(n)), block, 0, s, a);
-        return launch_status();
-    }
-    if (l.chain) {
-        const uint64_t vecs = l.ws / 16;
-        a.tickets = static_cast<uint32_t*>(ws);
-        a.words = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(ws) + kScanCountBytes);
-        hipLaunchKernelGGL(k_scan_clear, dim3(uint32_t(std::min<uint64_t>((vecs + 255) / 256, 2048))), dim3(256), 0, s,
-                           static_cast<uint4*>(ws), vecs);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        const uint64_t grid = (chains + kScanQueues - 1) / kScanQueues * kScanQueues * l.tiles;
-        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain>), dim3(uint32_t(grid)), block, 0, s, a);
-        return launch_status();
-    }
-    a.agg_a = static_cast<float*>(ws);
-    a.agg_s = a.agg_a + n * l.lanes * VW;
-    hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanSum>), dim3(uint32_t(n)), block, 0, s, a);
-    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-    hipLaunchKernelGGL(k_scan_carry<BACK>, dim3(uint32_t(chains)), dim3(1024), 0, s, a, uint32_t(VW));
-    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-    hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanCarry>), dim3(uint32_t(n)), block, 0, s, a);
-    return launch_status();
+    return scan_lines(a, sizeof(T)) ? launch_scan<T, VW, SIG, BACK, true>(a, l, ws, s)
+                                    : launch_scan<T, VW, SIG, BACK, false>(a, l, ws, s);
 }
 
 template <typename T, int VW>
