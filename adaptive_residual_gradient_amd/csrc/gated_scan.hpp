@@ -11,13 +11,12 @@
 // state and gate product stay in registers between the two halves, so inputs
 // are read once and results written once.  The tile's threads join their
 // steps through LDS.  The state travels from tile to tile
-//   - not at all, where one tile holds the whole sequence (kScanCarry alone);
-//   - through one 8-byte word a channel that each tile leaves for its
-//     successor (kScanChain), where there are enough independent chains of
-//     tiles to hide that hop;
-//   - through a pass of its own over the tiles' compositions (kScanSum,
-//     k_scan_carry, kScanCarry), which reads the gates twice, for a few long
-//     sequences.
+//   - not at all, where one tile holds the whole sequence (kScanAlone);
+//   - through one word a channel that each tile leaves for its successor
+//     (kScanChain), where there are enough independent chains of tiles to hide
+//     that hop of about 1.3 us;
+//   - of few long chains, through the compositions of all tiles on the way to
+//     the last one whose state is known, many at a time (kScanBack).
 // Sequences of at most kScanShort steps take one thread per 4 bytes of
 // channels (k_scan_short).
 #pragma once
@@ -32,9 +31,10 @@ namespace adacomp {
 constexpr int scan_thread_steps(bool back) { return back ? 8 : 16; }
 constexpr uint32_t kScanShort = 16;     // longest sequence of the short kernels
 constexpr uint32_t kScanThreads = 512;  // most threads of a tile
-constexpr uint32_t kScanQueues = 64;    // tickets of kScanChain
+constexpr uint32_t kScanQueues = 64;    // most ticket counters
 constexpr uint32_t kScanCountBytes = kScanQueues * 64;   // each on a line of its own
-constexpr int kScanSum = 0, kScanCarry = 1, kScanChain = 2;
+constexpr int kScanAlone = 0, kScanChain = 1, kScanBack = 2;
+constexpr uint32_t kScanWindow = 8;     // tiles a thread of kScanBack looks at together
 
 struct ScanView {
     void* p;
@@ -47,13 +47,11 @@ struct ScanArgs {
     const float* dh_last;    // nullable
     float* last;             // h_last or dh0; nullable
     const int32_t* lengths;  // nullable
-    uint32_t* tickets;       // kScanChain
-    uint32_t* words;         // kScanChain: [chain][tile][slot] the state, kScanEmpty until it is there
-    float* agg_a;            // kScanSum, kScanCarry: [chain][tile][slot]
-    float* agg_s;            // the same; then the carried states
+    uint32_t* tickets;       // one counter a queue, 64 bytes apart
+    void* words;             // [chain][tile][slot]: uint32_t (kScanChain) or uint64_t (kScanBack)
     uint64_t length;
     uint32_t batch, channels;
-    uint32_t lanes, groups, tiles, steps;   // lanes a step, channel groups, tiles a chain, steps a tile
+    uint32_t lanes, groups, tiles, steps, queues;   // lanes a step, channel groups, tiles a chain, steps a tile
 };
 
 // Factors on the state and on the input.  With e = exp(-z), a = 1 / (1 + e)
@@ -129,6 +127,67 @@ __device__ __forceinline__ float wait_for_state(const uint32_t* word) {
     return __builtin_nanf("");
 }
 
+// What a tile of kScanBack leaves: the state's bits below kScanKnown once its
+// carried-out state is known; before, the two floats of its composition.
+constexpr uint32_t kScanKnown = 0xFFFFFFFEu;
+__device__ __forceinline__ void leave_pair(uint64_t* word, uint32_t high, float s) {
+    __hip_atomic_store(word, uint64_t(high) << 32 | __float_as_uint(s), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t composed(float a) {
+    const uint32_t bits = __float_as_uint(a);
+    return bits >= kScanKnown ? 0x7FC00000u : bits;
+}
+
+// The state carried into a tile with `before` tiles before it, word `d` of
+// which (1 the nearest) is at base + d * stride.  All threads look: the subs of
+// a slot take kScanWindow tiles each, nearest first, and join their maps
+// through LDS; if no known state is among them, the next window follows.  The
+// result is there for the first `slots` threads.  Every tile leaves its
+// composition before it looks itself, so no wait here hangs on another wait.
+__device__ __forceinline__ float look_back(const uint64_t* base, int64_t stride, uint32_t before, uint32_t slots) {
+    __shared__ float la[kScanThreads], ls[kScanThreads];
+    __shared__ uint32_t known[kScanThreads];
+    const uint32_t tid = threadIdx.x, sub = tid / slots, slot = tid % slots, subs = blockDim.x / slots;
+    bool done = false;
+    float A = 1.f, S = 0.f;
+    for (uint32_t near = 0;; near += subs * kScanWindow) {
+        const uint32_t d0 = near + sub * kScanWindow + 1;
+        uint64_t w[kScanWindow];
+#pragma unroll
+        for (uint32_t u = 0; u < kScanWindow; ++u)
+            w[u] = __hip_atomic_load(base + int64_t(min(d0 + u, before)) * stride + slot, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+        float a = 1.f, s = 0.f;
+        bool found = false;
+#pragma unroll
+        for (uint32_t u = 0; u < kScanWindow; ++u) {
+            if (found || d0 + u > before) continue;
+            uint32_t i = 0;
+            while (uint32_t(w[u] >> 32) == kScanEmpty && ++i < (1u << 22)) {
+                __builtin_amdgcn_s_sleep(1);
+                w[u] = __hip_atomic_load(base + int64_t(d0 + u) * stride + slot, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+            }
+            const uint32_t high = uint32_t(w[u] >> 32);
+            s = __builtin_fmaf(a, __uint_as_float(uint32_t(w[u])), s);
+            found = high >= kScanKnown;   // past the bound of the wait the state is a NaN's bits
+            a *= __uint_as_float(high);
+        }
+        la[tid] = a;
+        ls[tid] = s;
+        known[tid] = found;
+        __syncthreads();
+        if (tid < slots && !done) {
+            for (uint32_t j = 0; j < subs && !done; ++j) {
+                S = __builtin_fmaf(A, ls[j * slots + tid], S);
+                A *= la[j * slots + tid];
+                done = known[j * slots + tid];
+            }
+        }
+        if (!__syncthreads_or(tid < slots && !done)) return S;
+    }
+}
+
 // Workgroups go to the 8 chiplets in turn.  Of 64 consecutive ones each
 // chiplet's eight take eight neighbouring chains: neighbouring channels of the
 // same rows.
@@ -139,6 +198,7 @@ struct ScanTile {
     uint32_t chain, b, k, slot0;      // slot0: the channel of the group's first slot
     uint64_t tend;                    // the tile's steps of the sequence end here
     uint32_t count;                   // and are so many
+    uint32_t before;                  // tiles with steps before it in the direction of travel
     bool first, last;                 // first: nothing is carried in but the given state;
                                       // last: the state carried out is the call's
 };
@@ -152,7 +212,6 @@ template <typename T, int VW, bool SIG, bool BACK, int MODE, bool NT, bool FULL>
 __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& tile, float* sa, float* ss) {
     typedef typename Packed<T, VW>::V V;
     constexpr int N = scan_thread_steps(BACK);
-    constexpr bool kGrad = BACK && MODE != kScanSum;
     const uint32_t tid = threadIdx.x, R = a.lanes, slots = R * VW;
     const uint32_t r = tid % R, g = tid / R, G = blockDim.x / R, b = tile.b;
     const uint32_t c = min(tile.slot0 + r * VW, a.channels - VW);
@@ -174,7 +233,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
     walk(a.gate, ta, zr);
     walk(BACK ? a.dh : a.x, ta, xr);
     FVec<VW> h0 = 0.f;
-    if (kGrad) {   // requested before the wait
+    if (BACK) {   // requested before the wait
         if (SIG) walk(a.x, ta, ur);
         // the earlier states, the given one before step 0 (whose place reads step 0's)
         const T* p = view_at<T>(a.h, b, ta, c);
@@ -222,43 +281,42 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
         ss[g * slots + r * VW + v] = S[v];
     }
     __syncthreads();
+    float A = 1.f, C = 0.f, s0 = 0.f;
+    const uint64_t word = (uint64_t(tile.chain) * a.tiles + tile.k) * slots;
     if (tid < slots) {
-        float A = 1.f, C = 0.f;
 #pragma unroll 8
         for (uint32_t i = 0; i < G; ++i) {
             const float f = sa[i * slots + tid];
             C = __builtin_fmaf(f, C, ss[i * slots + tid]);
             A *= f;
         }
-        const uint64_t word = (uint64_t(tile.chain) * a.tiles + tile.k) * slots + tid;
-        if (MODE == kScanSum) {
-            a.agg_a[word] = A;
-            a.agg_s[word] = C;
-            return;
-        }
+        if (MODE == kScanBack && !tile.first && !tile.last)
+            leave_pair(static_cast<uint64_t*>(a.words) + word + tid, composed(A), C);
+    }
+    if (MODE == kScanBack && !tile.first)
+        s0 = look_back(static_cast<const uint64_t*>(a.words) + word, BACK ? int64_t(slots) : -int64_t(slots),
+                       tile.before, slots);
+    if (tid < slots) {
         const uint32_t sc = min(tile.slot0 + tid / VW * VW, a.channels - VW) + tid % VW;   // the slot's channel
         const uint64_t state = uint64_t(b) * a.channels + sc;
-        float s = 0.f;
         if (tile.first) {
             const float* start = BACK ? a.dh_last : a.h0;
-            if (start) s = start[state];
-        } else if (MODE == kScanCarry) {
-            s = a.agg_s[word];
+            if (start) s0 = start[state];
         } else if (MODE == kScanChain) {
-            s = wait_for_state(a.words + (BACK ? word + slots : word - slots));
+            s0 = wait_for_state(static_cast<const uint32_t*>(a.words) + (BACK ? word + slots : word - slots) + tid);
         }
-        const float out = __builtin_fmaf(A, s, C);
-        if (MODE == kScanChain && !tile.last) leave_state(a.words + word, out);
+        const float out = __builtin_fmaf(A, s0, C);
+        if (MODE == kScanChain && !tile.last) leave_state(static_cast<uint32_t*>(a.words) + word + tid, out);
+        if (MODE == kScanBack && !tile.last) leave_pair(static_cast<uint64_t*>(a.words) + word + tid, kScanKnown, out);
         if (tile.last && a.last) a.last[state] = out;
         // the state each sub-chunk starts from takes the place of its product
 #pragma unroll 8
         for (uint32_t i = 0; i < G; ++i) {
             const float f = sa[i * slots + tid];
-            sa[i * slots + tid] = s;
-            s = __builtin_fmaf(f, s, ss[i * slots + tid]);
+            sa[i * slots + tid] = s0;
+            s0 = __builtin_fmaf(f, s0, ss[i * slots + tid]);
         }
     }
-    if (MODE == kScanSum) return;
     __syncthreads();
     FVec<VW> s;
 #pragma unroll
@@ -308,20 +366,22 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
     const uint32_t tid = threadIdx.x, slots = a.lanes * VW;
     ScanTile tile;
     uint32_t k;   // along the direction of travel
-    if (MODE == kScanChain) {
-        const uint32_t q = blockIdx.x % kScanQueues;
-        const uint32_t chains = a.batch * a.groups, mine = (chains - chiplet_order(q) + kScanQueues - 1) / kScanQueues;
+    const uint32_t chains = a.batch * a.groups;
+    if (MODE != kScanAlone) {
+        // tickets of a queue go through its chains tile by tile
+        const uint32_t q = blockIdx.x % a.queues, at = a.queues == kScanQueues ? chiplet_order(q) : q;
+        const uint32_t mine = (chains - at + a.queues - 1) / a.queues;
         if (tid == 0)
             ticket = __hip_atomic_fetch_add(a.tickets + q * 16, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         const uint32_t n = __builtin_amdgcn_readfirstlane(ticket);
         if (n >= mine * a.tiles) return;
-        tile.chain = chiplet_order(q) + kScanQueues * (n % mine);
+        tile.chain = at + a.queues * (n % mine);
         k = n / mine;
     } else {
-        const uint32_t chains = a.batch * a.groups, i = blockIdx.x % chains;
+        const uint32_t i = blockIdx.x;
         tile.chain = i < (chains & ~63u) ? chiplet_order(i) : i;
-        k = blockIdx.x / chains;
+        k = 0;
     }
     tile.b = tile.chain / a.groups;
     tile.slot0 = tile.chain % a.groups * slots;
@@ -332,10 +392,11 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
     tile.tend = t1 < n ? t1 : (t0 < n ? n : t0);
     tile.count = uint32_t(tile.tend - t0);
     tile.first = BACK ? tile.tend == n : tile.k == 0;
+    tile.before = BACK ? uint32_t((n + a.steps - 1) / a.steps) - 1 - tile.k : tile.k;
     tile.last = BACK ? tile.k == 0 : tile.tend == n;
 
     // zeros past the sequence's end
-    if (MODE != kScanSum && tile.tend < t1) {
+    if (tile.tend < t1) {
         const uint32_t r = tid % a.lanes, c = min(tile.slot0 + r * VW, a.channels - VW);
         const typename Packed<T, VW>::V zero = {};
         for (uint64_t t = tile.tend + tid / a.lanes; t < t1; t += blockDim.x / a.lanes) {
@@ -351,7 +412,7 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
         scan_tile<T, VW, SIG, BACK, MODE, NT, true>(a, tile, sa, ss);
     } else if (tile.count > 0) {
         scan_tile<T, VW, SIG, BACK, MODE, NT, false>(a, tile, sa, ss);
-    } else if (n == 0 && tile.k == 0 && a.last && MODE != kScanSum && tid < slots) {   // an empty sequence
+    } else if (n == 0 && tile.k == 0 && a.last && tid < slots) {   // an empty sequence
         const uint32_t c = min(tile.slot0 + tid / VW * VW, a.channels - VW) + tid % VW;
         const uint64_t state = uint64_t(tile.b) * a.channels + c;
         const float* start = BACK ? a.dh_last : a.h0;
@@ -359,45 +420,11 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
     }
 }
 
-// Makes the tickets (the first kScanCountBytes) 0 and the words of kScanChain empty.
+// Makes the tickets (the first kScanCountBytes) 0 and the words empty.
 __global__ __launch_bounds__(256) void k_scan_clear(uint4* p, uint64_t n) {
     const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
     const uint32_t v = i < kScanCountBytes / 16 ? 0u : kScanEmpty;
     if (i < n) p[i] = uint4{v, v, v, v};
-}
-
-// agg_s becomes the state carried into each tile: a workgroup takes one chain,
-// 1024 / slots sections of its tiles at once, joined through LDS.
-template <bool BACK>
-__global__ __launch_bounds__(1024) void k_scan_carry(ScanArgs a, uint32_t vw) {
-    __shared__ float sa[1024], ss[1024];
-    const uint32_t slots = a.lanes * vw, slot = threadIdx.x % slots, part = threadIdx.x / slots;
-    const uint32_t parts = blockDim.x / slots, chain = blockIdx.x, b = chain / a.groups;
-    const uint32_t tiles = uint32_t((scan_steps(a, b) + a.steps - 1) / a.steps);   // those with steps
-    const uint32_t per = (tiles + parts - 1) / parts;
-    const uint32_t n0 = min(part * per, tiles), n1 = min(n0 + per, tiles);
-    const uint64_t base = uint64_t(chain) * a.tiles * slots + slot;
-    auto at = [&](uint32_t n) { return base + uint64_t(BACK ? tiles - 1 - n : n) * slots; };
-    float A = 1.f, S = 0.f;
-#pragma unroll 8
-    for (uint32_t n = n0; n < n1; ++n) {
-        const float f = a.agg_a[at(n)];
-        S = __builtin_fmaf(f, S, a.agg_s[at(n)]);
-        A *= f;
-    }
-    sa[threadIdx.x] = A;
-    ss[threadIdx.x] = S;
-    __syncthreads();
-    const uint32_t c = min((chain % a.groups) * slots + slot / vw * vw, a.channels - vw) + slot % vw;
-    const float* start = BACK ? a.dh_last : a.h0;
-    float s = start ? start[uint64_t(b) * a.channels + c] : 0.f;
-    for (uint32_t i = 0; i < part; ++i) s = __builtin_fmaf(sa[i * slots + slot], s, ss[i * slots + slot]);
-#pragma unroll 8
-    for (uint32_t n = n0; n < n1; ++n) {
-        const float f = a.agg_a[at(n)], d = a.agg_s[at(n)];
-        a.agg_s[at(n)] = s;
-        s = __builtin_fmaf(f, s, d);
-    }
 }
 
 // ---- short sequences ----

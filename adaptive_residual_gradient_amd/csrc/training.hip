@@ -471,8 +471,10 @@ ScanLayout scan_layout(const adacomp_scan_shape& s, uint32_t vw, bool back) {
     l.steps = subs * per;
     l.tiles = static_cast<uint32_t>((s.length + l.steps - 1) / l.steps);
     const uint64_t chains = uint64_t(s.batch) * l.groups;
-    l.chain = l.tiles > 1 && chains >= kScanQueues;
-    // two floats, or one word, of every slot
+    // At 64 chains and more the hop from tile to tile hides behind the other chains' tiles, and looking
+    // further back only adds to the traffic.
+    l.chain = chains >= 64;
+    // a word of every slot
     if (l.tiles > 1) l.ws = kScanCountBytes + chains * l.tiles * l.lanes * vw * 8;
     return l;
 }
@@ -583,26 +585,20 @@ int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t
     // work-items of one launch must fit in 32 bits (the queues round the chains up)
     if ((chains + kScanQueues) * l.tiles * l.threads >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;
     const dim3 block(l.threads);
-    if (l.chain) {
-        const uint64_t vecs = (kScanCountBytes + n * l.lanes * VW * 4 + 15) / 16;
-        a.tickets = static_cast<uint32_t*>(ws);
-        a.words = a.tickets + kScanCountBytes / 4;
-        hipLaunchKernelGGL(k_scan_clear, dim3(uint32_t((vecs + 255) / 256)), dim3(256), 0, s, static_cast<uint4*>(ws),
-                           vecs);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        const uint64_t grid = (chains + kScanQueues - 1) / kScanQueues * kScanQueues * l.tiles;
-        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain, NT>), dim3(uint32_t(grid)), block, 0, s, a);
+    if (l.tiles == 1) {
+        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanAlone, NT>), dim3(uint32_t(n)), block, 0, s, a);
         return launch_status();
     }
-    if (l.tiles > 1) {
-        a.agg_a = static_cast<float*>(ws);
-        a.agg_s = a.agg_a + n * l.lanes * VW;
-        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanSum, false>), dim3(uint32_t(n)), block, 0, s, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        hipLaunchKernelGGL(k_scan_carry<BACK>, dim3(uint32_t(chains)), dim3(1024), 0, s, a, uint32_t(VW));
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-    }
-    hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanCarry, NT>), dim3(uint32_t(n)), block, 0, s, a);
+    const uint64_t vecs = (kScanCountBytes + n * l.lanes * VW * (l.chain ? 4 : 8) + 15) / 16;
+    a.tickets = static_cast<uint32_t*>(ws);
+    a.words = a.tickets + kScanCountBytes / 4;
+    a.queues = static_cast<uint32_t>(std::min<uint64_t>(chains, kScanQueues));
+    hipLaunchKernelGGL(k_scan_clear, dim3(uint32_t((vecs + 255) / 256)), dim3(256), 0, s, static_cast<uint4*>(ws),
+                       vecs);
+    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    const dim3 grid(uint32_t((chains + a.queues - 1) / a.queues * a.queues * l.tiles));
+    if (l.chain) hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain, NT>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanBack, NT>), grid, block, 0, s, a);
     return launch_status();
 }
 
