@@ -1,8 +1,9 @@
 """AdaComp for AMD Instinct MI355X: Python binding of ``libadacomp.so``.
 
-A thin ctypes layer over the C ABI declared in ``include/adacomp.h``: it
-marshals torch tensors (device memory) and the current HIP stream into plain
-pointers and sizes.  Every step of compression and decoding runs in the HIP
+A thin layer over the C ABI declared in ``include/adacomp.h`` (ctypes; for the
+training-step operators the extension module ``_binding.so``): it marshals
+torch tensors (device memory) and the current HIP stream into plain pointers
+and sizes.  Every step of compression and decoding runs in the HIP
 kernels of the library; nothing here computes.  If the library is not built,
 every call raises ``HipLibraryMissing``; there is no fallback.
 
@@ -402,46 +403,28 @@ MOMENT_BLOCK = 32        # elements of one tensor that share the scales of their
 NORM_MAX_COLS = 65536    # longest row of layer_norm
 
 
-# Operand types, filled in at the first call: importing this module does not import torch.
-_TYPES: dict = {}
-_F32 = _I32 = _U8 = _BF16 = _CODES = None
+_ops = None
 
 
-def _load_types() -> None:
-    global _F32, _I32, _U8, _BF16, _CODES
-    import torch
-    _F32, _I32, _U8, _BF16 = torch.float32, torch.int32, torch.uint8, torch.bfloat16
-    _CODES = (torch.float8_e4m3fn, torch.uint8)
-    _TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+def _operators():
+    """The operators' native entry points (csrc/binding.cpp), which check the tensors and make the calls;
+    raises HipLibraryMissing if they are not built."""
+    global _ops
+    if _ops is None:
+        lib()
+        import torch  # noqa: F401  the module is linked against torch's libraries
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise HipLibraryMissing(f"the operators' entry points are not built ({e}); build them with "
+                                    "__graft_entry__.build()") from e
+        _ops = _binding
+    return _ops
 
 
-def _type_of(t, name: str) -> int:
-    if not _TYPES:
-        _load_types()
-    code = _TYPES.get(t.dtype)
-    if code is None or not t.is_cuda:
-        raise TypeError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
-    return code
-
-
-def _ptr(t, dtype, name: str) -> int:
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous CUDA tensor of {dtype}")
-    return t.data_ptr()
-
-
-def _f32_opt(t, n: int, name: str):
-    """Pointer of a nullable float32 tensor of n elements."""
-    if t is None:
-        return None
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements")
-    return _ptr(t, _F32, name)
-
-
-def _ws(t):
-    """(pointer, bytes) of a nullable workspace."""
-    return (None, 0) if t is None else (_ptr(t, _U8, "ws"), t.numel())
+def _grad(grad):
+    """(type code, address) of a gradient."""
+    return _operators().gradient(grad)
 
 
 class Optimizer:
@@ -460,12 +443,12 @@ class Optimizer:
         info = OptimizerInfo()
         _check("adacomp_optimizer_get_info", lib().adacomp_optimizer_get_info(h, ctypes.byref(info)))
         self.info = info
-        self.span, self.nblocks = int(info.span), int(info.nblocks)
+        self.span, self.nblocks, self.address = int(info.span), int(info.nblocks), h.value
 
     def close(self):
         if getattr(self, "handle", None):
             lib().adacomp_optimizer_destroy(self.handle)
-            self.handle = None
+            self.handle, self.address = None, 0
 
     def __del__(self):
         try:
@@ -498,34 +481,12 @@ def optimizer_query(tensors) -> OptimizerInfo:
     return info
 
 
-def _grad(grad):
-    code = _type_of(grad, "grad")
-    if not grad.is_contiguous():
-        raise TypeError("grad must be contiguous")
-    return code, grad.data_ptr()
-
-
-def _bf16_opt(t, n: int):
-    if t is None:
-        return None
-    if t.numel() < n:
-        raise ValueError("weights_bf16 shorter than the other buffers")
-    return _ptr(t, _BF16, "weights_bf16")
-
-
-def _codes(t, name: str) -> int:
-    if t.dtype not in _CODES or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous float8_e4m3fn or uint8 CUDA tensor")
-    return t.data_ptr()
-
-
 def grad_norm(opt: Optimizer, grad, clip, ws, max_norm: float, scale: float = 1.0, stream=None) -> None:
     """clip[0] = norm of scale * grad over the table's tensors, clip[1] = the factor that brings it
     down to max_norm."""
-    code, ptr = _grad(grad)
-    st = lib().adacomp_grad_norm(opt.handle, ptr, code, grad.numel(), max_norm, scale,
-                                 _f32_opt(clip, 2, "clip"), *_ws(ws), _stream_handle(stream))
-    _check("adacomp_grad_norm", st)
+    st = _operators().grad_norm(opt.address, grad, clip, ws, max_norm, scale, stream)
+    if st:
+        raise AdaCompError("adacomp_grad_norm", st)
 
 
 def adamw(opt: Optimizer, weights, grad, m, v, lr: float, beta1: float = 0.9, beta2: float = 0.999,
@@ -533,13 +494,10 @@ def adamw(opt: Optimizer, weights, grad, m, v, lr: float, beta1: float = 0.9, be
           stream=None) -> None:
     """AdamW step number ``step`` (>= 1) on weights, m and v (float32, in place) with the gradient
     scale * clip[1] * grad; weights_bf16 receives the new weights rounded."""
-    code, ptr = _grad(grad)
-    n = min(weights.numel(), grad.numel(), m.numel(), v.numel())
-    p = AdamW(lr, beta1, beta2, eps, scale, int(step))
-    st = lib().adacomp_adamw_step(
-        opt.handle, _ptr(weights, _F32, "weights"), ptr, code, _ptr(m, _F32, "m"), _ptr(v, _F32, "v"),
-        _bf16_opt(weights_bf16, opt.span), n, p, _f32_opt(clip, 2, "clip"), _stream_handle(stream))
-    _check("adacomp_adamw_step", st)
+    st = _operators().adamw(opt.address, opt.span, opt.nblocks, weights, grad, m, v, None, lr, beta1, beta2, eps, step,
+                            scale, 0, clip, weights_bf16, stream)
+    if st:
+        raise AdaCompError("adacomp_adamw_step", st)
 
 
 def adamw_packed(opt: Optimizer, weights, grad, m, v, scales, lr: float, beta1: float = 0.9,
@@ -547,46 +505,20 @@ def adamw_packed(opt: Optimizer, weights, grad, m, v, scales, lr: float, beta1: 
                  clip=None, weights_bf16=None, stream=None) -> None:
     """As adamw with moments in 8 bits: m and v e4m3 codes (float8_e4m3fn or uint8), scales as
     Optimizer.moment_scales gives them, updated in place; ``seed`` chooses the rounding's random bits."""
-    if scales.numel() < 2 * opt.nblocks:
-        raise ValueError("scales shorter than the optimizer's blocks")
-    code, ptr = _grad(grad)
-    n = min(weights.numel(), grad.numel(), m.numel(), v.numel())
-    p = AdamW(lr, beta1, beta2, eps, scale, int(step))
-    st = lib().adacomp_adamw_packed_step(
-        opt.handle, _ptr(weights, _F32, "weights"), ptr, code, _codes(m, "m"), _codes(v, "v"),
-        _ptr(scales, _U8, "scales"), _bf16_opt(weights_bf16, opt.span), n, p, int(seed) & 0xFFFFFFFF,
-        _f32_opt(clip, 2, "clip"), _stream_handle(stream))
-    _check("adacomp_adamw_packed_step", st)
-
-
-def _rows(t, name: str, like=None):
-    """(pointer, row stride, rows, cols, type) of a tensor whose last axis is adjacent and whose
-    other axes have one stride between them."""
-    code = _type_of(t, name)
-    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype):
-        raise ValueError(f"{name} must have the shape and type of the input")
-    if t.dim() == 0:
-        raise ValueError(f"{name} must have at least one axis")
-    cols = t.shape[-1]
-    rows = t.numel() // cols if cols else 0
-    if t.is_contiguous() or rows <= 1 and (t.stride(-1) == 1 or cols == 1):
-        stride = cols
-    elif t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
-        stride = t.stride(0)
-    else:
-        raise TypeError(f"{name} must be contiguous, or a matrix with adjacent columns")
-    return t.data_ptr(), stride, rows, cols, code
+    if scales is None:
+        raise TypeError("scales must be a tensor")
+    st = _operators().adamw(opt.address, opt.span, opt.nblocks, weights, grad, m, v, scales, lr, beta1, beta2, eps, step,
+                            scale, int(seed) & 0xFFFFFFFF, clip, weights_bf16, stream)
+    if st:
+        raise AdaCompError("adacomp_adamw_packed_step", st)
 
 
 def layer_norm(x, weight, bias, out, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
     """Layer norm of x over its last axis into out; weight and bias float32 or None; mean and rstd
     (float32, one a row) are what layer_norm_backward needs."""
-    px, sx, rows, cols, code = _rows(x, "x")
-    po, so, _, _, _ = _rows(out, "out", x)
-    st = lib().adacomp_layer_norm(px, sx, _f32_opt(weight, cols, "weight"), _f32_opt(bias, cols, "bias"),
-                                  po, so, _f32_opt(mean, rows, "mean"), _f32_opt(rstd, rows, "rstd"), rows,
-                                  cols, code, eps, _stream_handle(stream))
-    _check("adacomp_layer_norm", st)
+    st = _operators().layer_norm(x, weight, bias, out, mean, rstd, eps, stream)
+    if st:
+        raise AdaCompError("adacomp_layer_norm", st)
 
 
 def layer_norm_workspace(rows: int, cols: int, device="cuda"):
@@ -600,42 +532,9 @@ def layer_norm_workspace(rows: int, cols: int, device="cuda"):
 def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, ws=None,
                         stream=None) -> None:
     """Gradients of layer_norm: dx, and dweight and dbias (float32, both or neither)."""
-    pd, sd, rows, cols, code = _rows(dy, "dy")
-    px, sx, _, _, _ = _rows(x, "x", dy)
-    po, so, _, _, _ = _rows(dx, "dx", dy)
-    st = lib().adacomp_layer_norm_backward(
-        pd, sd, px, sx, _f32_opt(weight, cols, "weight"), _f32_opt(mean, rows, "mean"),
-        _f32_opt(rstd, rows, "rstd"), po, so, _f32_opt(dweight, cols, "dweight"),
-        _f32_opt(dbias, cols, "dbias"), rows, cols, code, *_ws(ws), _stream_handle(stream))
-    _check("adacomp_layer_norm_backward", st)
-
-
-def _scan_view(t, shape, dtype, name: str):
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of the gate's shape and type")
-    if t.is_contiguous():
-        return _View(t.data_ptr(), shape[1] * shape[2], shape[2])
-    B, T, D = shape
-    sb, st, sd = t.stride()
-    if D > 1 and sd != 1:
-        raise TypeError(f"{name} must have adjacent channels")
-    return _View(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else D)
-
-
-def _scan_shape(gate, sigmoid: bool):
-    code = _type_of(gate, "gate")
-    s = gate.shape
-    if len(s) != 3:
-        raise ValueError("gate must be [batch, length, channels]")
-    return s, s[0] * s[2], _ScanShape(s[1], s[0], s[2], code, 1 if sigmoid else 0)
-
-
-def _lengths_opt(lengths, batch: int):
-    if lengths is None:
-        return None
-    if lengths.numel() != batch:
-        raise ValueError("lengths must have one element a sequence")
-    return _ptr(lengths, _I32, "lengths")
+    st = _operators().layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream)
+    if st:
+        raise AdaCompError("adacomp_layer_norm_backward", st)
 
 
 def gated_scan_workspace(batch: int, length: int, channels: int, device="cuda"):
@@ -652,24 +551,15 @@ def gated_scan(gate, x, h, h0=None, h_last=None, lengths=None, sigmoid: bool = T
                stream=None) -> None:
     """h_t = a_t h_(t-1) + k_t x_t along axis 1 of [batch, length, channels] tensors, with
     (a, k) = (sigmoid(gate), sigmoid(-gate)) or (gate, 1); h0 and h_last float32 [batch, channels]."""
-    s, n, shape = _scan_shape(gate, sigmoid)
-    dt = gate.dtype
-    st = lib().adacomp_gated_scan(
-        shape, _scan_view(gate, s, dt, "gate"), _scan_view(x, s, dt, "x"), _scan_view(h, s, dt, "h"),
-        _f32_opt(h0, n, "h0"), _f32_opt(h_last, n, "h_last"), _lengths_opt(lengths, s[0]), *_ws(ws),
-        _stream_handle(stream))
-    _check("adacomp_gated_scan", st)
+    st = _operators().gated_scan(gate, x, h, h0, h_last, lengths, sigmoid, ws, stream)
+    if st:
+        raise AdaCompError("adacomp_gated_scan", st)
 
 
 def gated_scan_backward(gate, x, h, dh, dgate, dx, h0=None, dh_last=None, dh0=None, lengths=None,
                         sigmoid: bool = True, ws=None, stream=None) -> None:
     """Gradients of gated_scan from the states h it wrote (x is not needed, and may be None, without
     the sigmoid)."""
-    s, n, shape = _scan_shape(gate, sigmoid)
-    dt = gate.dtype
-    st = lib().adacomp_gated_scan_backward(
-        shape, _scan_view(gate, s, dt, "gate"), None if x is None else _scan_view(x, s, dt, "x"),
-        _scan_view(h, s, dt, "h"), _scan_view(dh, s, dt, "dh"), _scan_view(dgate, s, dt, "dgate"),
-        _scan_view(dx, s, dt, "dx"), _f32_opt(h0, n, "h0"), _f32_opt(dh_last, n, "dh_last"),
-        _f32_opt(dh0, n, "dh0"), _lengths_opt(lengths, s[0]), *_ws(ws), _stream_handle(stream))
-    _check("adacomp_gated_scan_backward", st)
+    st = _operators().gated_scan_backward(gate, x, h, dh, dgate, dx, h0, dh_last, dh0, lengths, sigmoid, ws, stream)
+    if st:
+        raise AdaCompError("adacomp_gated_scan_backward", st)
