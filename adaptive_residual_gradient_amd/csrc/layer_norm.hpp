@@ -22,8 +22,9 @@ constexpr uint32_t kNormWaveCols = 64 * kNormElems;       // one wavefront's col
 constexpr uint32_t kNormRegCols = 16 * kNormWaveCols;     // a workgroup's
 constexpr uint32_t kNormMaxWaves = 4096;                  // wavefronts of a forward launch
 constexpr uint32_t kNormBackRegCols = 8 * kNormWaveCols;
-constexpr uint32_t kNormMaxPartials = 512;                // workgroups of the weight gradients
+constexpr uint32_t kNormMaxPartials = 256;                // workgroups of the weight gradients
 constexpr uint32_t kNormWideThreads = 1024;
+constexpr uint32_t kNormBackThreads = 512;                // most threads of a workgroup there
 
 struct NormArgs {
     const void* x;
@@ -107,12 +108,11 @@ __device__ __forceinline__ FVec<VEC> load_param(const float* p, uint32_t c, floa
     return v;
 }
 
-// The thread's team.  A whole wavefront's is told to be the same in every
-// lane, so that its rows' addresses and statistics take scalar registers.
-template <int LANES, bool BLOCK>
-__device__ __forceinline__ uint32_t team_index() {
-    if (BLOCK) return 0;
-    const uint32_t i = threadIdx.x / LANES;
+// The thread's team of `team` lanes.  Whole wavefronts' is told to be the same in
+// every lane, so that its rows' addresses and statistics take scalar registers.
+template <int LANES>
+__device__ __forceinline__ uint32_t team_index(uint32_t team) {
+    const uint32_t i = threadIdx.x / team;
     return LANES == 64 ? uint32_t(__builtin_amdgcn_readfirstlane(int(i))) : i;
 }
 
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 256) void k_layer_norm(NormArgs a) {
     typedef typename Packed<T, VEC>::V V;
     constexpr uint32_t TEAMS = BLOCK ? 1 : 256 / LANES;
     const uint32_t team = BLOCK ? blockDim.x : LANES, lane = threadIdx.x % team;
-    const uint32_t mine = team_index<LANES, BLOCK>();
+    const uint32_t mine = BLOCK ? 0 : team_index<LANES>(LANES);
     const NormCols<VEC, NV> cols(a.cols, lane, team);
     __shared__ float slots[2][16];
     FVec<VEC> w[NV], b[NV];
@@ -234,46 +234,50 @@ __global__ __launch_bounds__(kNormWideThreads) void k_layer_norm_wide(NormArgs a
 
 // Each team steps over rows and adds its columns' share of dweight and dbias
 // in registers; the workgroup's teams are joined in LDS in team order and
-// written as one partial row pair, which k_norm_weight_grad adds up.  The next
-// row is requested before the present one is joined, and the weight waits in
-// LDS, for registers decide how many wavefronts keep a row in flight; it is 0
+// written as one partial row pair, which k_norm_weight_grad adds up.  The
+// next row is requested before the present one is joined (two rows ahead
+// measured the same), and the weight waits in LDS; it is 0
 // there in columns that another lane holds, which takes them out of the row's
-// sums.  A team is LANES lanes of a wavefront or, BLOCK, a workgroup.
+// sums.  A team is LANES lanes of a wavefront or, BLOCK, one wavefront per 1024
+// columns; a workgroup holds as many teams as kNormBackThreads lets it, for every
+// workgroup costs a partial row pair.
 template <typename T, int VEC, int NV, int LANES, bool BLOCK>
-__global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormArgs a) {
+__global__ __launch_bounds__(kNormBackThreads) void k_layer_norm_backward(NormArgs a) {
     typedef typename Packed<T, VEC>::V V;
-    constexpr uint32_t TEAMS = BLOCK ? 1 : 256 / LANES;
-    const uint32_t team = BLOCK ? blockDim.x : LANES, lane = threadIdx.x % team;
-    const uint32_t mine = team_index<LANES, BLOCK>();
+    const uint32_t waves = (a.cols + kNormWaveCols - 1) / kNormWaveCols;   // a team's, with BLOCK
+    const uint32_t team = BLOCK ? waves * 64 : LANES, teams = blockDim.x / team;
+    const uint32_t mine = team_index<LANES>(team), lane = threadIdx.x - mine * team;
     const NormCols<VEC, NV> cols(a.cols, lane, team);
-    __shared__ float slots[2][16];
-    extern __shared__ float dynamic[];   // the weight, then the teams' sums
+    extern __shared__ float dynamic[];   // the weight and two sets of row sums, then the teams' sums
+    const uint32_t span = team * NV * VEC;
     FVec<VEC> dw[NV], db[NV];
-    V nx[NV], ng[NV];
-    float nmean, nrstd;
+    struct Row {
+        V x[NV], g[NV];
+        float mean, rstd;
+    } next;
     // The statistics take vector loads, in order with the row's: scalar ones would be waited for with
     // the weight's LDS reads, a row too early.
     uint32_t zero;
     asm("v_mov_b32 %0, 0" : "=v"(zero));
     auto request = [&](uint64_t row) {   // past the last row: the last row again
         const uint64_t r = min(row, a.rows - 1);
-        nmean = a.mean[r + zero];
-        nrstd = a.rstd[r + zero];
+        next.mean = a.mean[r + zero];
+        next.rstd = a.rstd[r + zero];
         const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
         const T* dy = static_cast<const T*>(a.dy) + r * a.dy_stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            nx[j] = stream_load<VEC>(x + cols.at[j]);
-            ng[j] = stream_load<VEC>(dy + cols.at[j]);
+            next.x[j] = stream_load<VEC>(x + cols.at[j]);
+            next.g[j] = stream_load<VEC>(dy + cols.at[j]);
         }
-        if (LANES < 64 && row >= a.rows) {   // a team without a row beside teams that have one
-            nmean = nrstd = 0.f;
+        if ((LANES < 64 || BLOCK) && row >= a.rows) {   // a team without a row beside teams that have one
+            next.mean = next.rstd = 0.f;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) nx[j] = ng[j] = V{};
+            for (int j = 0; j < NV; ++j) next.x[j] = next.g[j] = V{};
         }
     };
-    const uint64_t step = uint64_t(gridDim.x) * TEAMS;
-    request(uint64_t(blockIdx.x) * TEAMS + mine);
+    const uint64_t step = uint64_t(gridDim.x) * teams, first = uint64_t(blockIdx.x) * teams;
+    request(first + mine);
     FVec<VEC>* wl = reinterpret_cast<FVec<VEC>*>(dynamic) + lane;   // vector j at wl[j * team]
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -281,21 +285,21 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
         FVec<VEC> w = load_param<VEC>(a.weight, cols.at[j], 1.f);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) w[k] = k < cols.skip[j] ? 0.f : w[k];
-        if (BLOCK || threadIdx.x < LANES) wl[j * team] = w;
+        if (threadIdx.x < team) wl[j * team] = w;
     }
     __syncthreads();
     uint32_t turn = 0;
-    for (uint64_t r0 = uint64_t(blockIdx.x) * TEAMS; r0 < a.rows; r0 += step) {
+    for (uint64_t r0 = first; r0 < a.rows; r0 += step) {
         const uint64_t row = r0 + mine;
         if (LANES == 64 && !BLOCK && row >= a.rows) break;
-        const float mean = nmean, rstd = nrstd;
+        const float mean = next.mean, rstd = next.rstd;
         FVec<VEC> h[NV], g[NV];
         float sum = 0.f, along = 0.f;
         asm volatile("" ::: "memory");   // the weight stays in LDS, not in registers across rows
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            h[j] = to_float<VEC, T>(nx[j]);
-            g[j] = to_float<VEC, T>(ng[j]);
+            h[j] = to_float<VEC, T>(next.x[j]);
+            g[j] = to_float<VEC, T>(next.g[j]);
         }
         if (r0 + step < a.rows) request(row + step);
 #pragma unroll
@@ -314,17 +318,17 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
         sum = team_sum<LANES>(sum);
         along = team_sum<LANES>(along);
         if (BLOCK) {
-            float* slot = slots[turn];
-            turn ^= 1;   // a slot is written again a barrier after its last reader
+            float* slot = dynamic + span + turn;
+            turn ^= 2 * kNormBackThreads / 64;   // a set is written again a barrier after its last reader
             if ((threadIdx.x & 63) == 0) {
                 slot[threadIdx.x >> 6] = sum;
-                slot[8 + (threadIdx.x >> 6)] = along;
+                slot[kNormBackThreads / 64 + (threadIdx.x >> 6)] = along;
             }
             __syncthreads();
             sum = along = 0.f;
-            for (uint32_t i = 0; i < blockDim.x / 64; ++i) {
+            for (uint32_t i = mine * waves; i < (mine + 1) * waves; ++i) {
                 sum += slot[i];
-                along += slot[8 + i];
+                along += slot[kNormBackThreads / 64 + i];
             }
         }
         if (row >= a.rows) continue;
@@ -347,23 +351,21 @@ __global__ __launch_bounds__(BLOCK ? 512 : 256) void k_layer_norm_backward(NormA
     }
     if (a.partial == nullptr) return;
     float* out = a.partial + uint64_t(blockIdx.x) * 2 * a.cols;
-    float* sums = BLOCK ? out : dynamic;
-    const uint32_t span = BLOCK ? a.cols : LANES * NV * VEC;   // from one row of sums to the next
     __syncthreads();   // the weight has been read
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             if (k < cols.skip[j]) continue;
-            sums[mine * span + cols.at[j] + k] = dw[j][k];
-            sums[(TEAMS + mine) * span + cols.at[j] + k] = db[j][k];
+            dynamic[mine * span + cols.at[j] + k] = dw[j][k];
+            dynamic[(teams + mine) * span + cols.at[j] + k] = db[j][k];
         }
-    if (BLOCK) return;
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < 2 * a.cols; i += 256) {
+    for (uint32_t i = threadIdx.x; i < 2 * a.cols; i += blockDim.x) {
         const uint32_t which = i >= a.cols, c = i - which * a.cols;
         float s = 0.f;
-        for (uint32_t t = 0; t < TEAMS; ++t) s += sums[(which * TEAMS + t) * span + c];
+#pragma unroll 4
+        for (uint32_t t = 0; t < teams; ++t) s += dynamic[(which * teams + t) * span + c];
         out[i] = s;
     }
 }
