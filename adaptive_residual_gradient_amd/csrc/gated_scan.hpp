@@ -4,13 +4,13 @@
 //   c_t = a_t (dh_t + c_(t+1))             (backward, t descending; l_t = dh_t + c_(t+1))
 //
 // Each step is a map s -> a s + b of the carried state, and maps compose: the
-// steps of a tile are composed without knowing the state carried into it, and
-// every result is then one multiply-add of that state.  A tile is up to 256
-// steps (more where a sequence has few channels) of 32 or 64 channels: 512
-// threads, each with 4 bytes of channels and 16 (backward 8) consecutive steps whose local
-// state and gate product stay in registers between the two halves, so inputs
-// are read once and results written once.  The tile's threads join their
-// steps through LDS.  The state travels from tile to tile
+// steps of a tile are composed without knowing the state carried into it.  Once
+// it is known every forward result is one multiply-add of it, and the backward
+// recurrence runs again.  A tile is up to 256 steps (more where a sequence has
+// few channels) of 64 or 128 channels: 512 threads, each with 4 bytes of
+// channels and up to 16 consecutive steps that stay in registers between the two
+// halves, so inputs are read once and results written once.  The tile's threads
+// join their steps through LDS.  The state travels from tile to tile
 //   - not at all, where one tile holds the whole sequence (kScanAlone);
 //   - through one word a channel that each tile leaves for its successor
 //     (kScanChain), where there are enough independent chains of tiles to hide
@@ -26,15 +26,18 @@
 
 namespace adacomp {
 
-// Steps a thread holds: backward, their gates, states and gradients are held as
-// well, and 16 steps would take more than the 128 registers of four wavefronts a SIMD.
-constexpr int scan_thread_steps(bool back) { return back ? 8 : 16; }
+// Steps a thread holds.  Backward with the sigmoid 8: 16 of them take 110 registers, two workgroups
+// a CU (8 x 4096 x 2048 bf16 171 us against 142).  The others 16, for fewer tiles on the way of the state
+// (backward without the sigmoid, 1 x 65536 x 256 f32: 73 us against 85 with 8).
+constexpr int scan_thread_steps(bool sigmoid, bool back) { return sigmoid && back ? 8 : 16; }
 constexpr uint32_t kScanShort = 16;     // longest sequence of the short kernels
 constexpr uint32_t kScanThreads = 512;  // most threads of a tile
 constexpr uint32_t kScanQueues = 64;    // most ticket counters
 constexpr uint32_t kScanCountBytes = kScanQueues * 64;   // each on a line of its own
 constexpr int kScanAlone = 0, kScanChain = 1, kScanBack = 2;
-constexpr uint32_t kScanWindow = 8;     // tiles a thread of kScanBack looks at together
+// Tiles a thread of kScanBack looks at together: backward fewer, for its registers hold the inputs
+// meanwhile (1 x 65536 x 256 f32: backward 72.7 us with 4, 74.8 with 8; forward 50.5 and 49.4).
+constexpr uint32_t scan_window(bool back) { return back ? 4 : 8; }
 
 struct ScanView {
     void* p;
@@ -140,27 +143,28 @@ __device__ __forceinline__ uint32_t composed(float a) {
 
 // The state carried into a tile with `before` tiles before it, word `d` of
 // which (1 the nearest) is at base + d * stride.  All threads look: the subs of
-// a slot take kScanWindow tiles each, nearest first, and join their maps
+// a slot take WINDOW tiles each, nearest first, and join their maps
 // through LDS; if no known state is among them, the next window follows.  The
 // result is there for the first `slots` threads.  Every tile leaves its
 // composition before it looks itself, so no wait here hangs on another wait.
+template <uint32_t WINDOW>
 __device__ __forceinline__ float look_back(const uint64_t* base, int64_t stride, uint32_t before, uint32_t slots) {
     __shared__ float la[kScanThreads], ls[kScanThreads];
     __shared__ uint32_t known[kScanThreads];
     const uint32_t tid = threadIdx.x, sub = tid / slots, slot = tid % slots, subs = blockDim.x / slots;
     bool done = false;
     float A = 1.f, S = 0.f;
-    for (uint32_t near = 0;; near += subs * kScanWindow) {
-        const uint32_t d0 = near + sub * kScanWindow + 1;
-        uint64_t w[kScanWindow];
+    for (uint32_t near = 0;; near += subs * WINDOW) {
+        const uint32_t d0 = near + sub * WINDOW + 1;
+        uint64_t w[WINDOW];
 #pragma unroll
-        for (uint32_t u = 0; u < kScanWindow; ++u)
+        for (uint32_t u = 0; u < WINDOW; ++u)
             w[u] = __hip_atomic_load(base + int64_t(min(d0 + u, before)) * stride + slot, __ATOMIC_RELAXED,
                                      __HIP_MEMORY_SCOPE_AGENT);
         float a = 1.f, s = 0.f;
         bool found = false;
 #pragma unroll
-        for (uint32_t u = 0; u < kScanWindow; ++u) {
+        for (uint32_t u = 0; u < WINDOW; ++u) {
             if (found || d0 + u > before) continue;
             uint32_t i = 0;
             while (uint32_t(w[u] >> 32) == kScanEmpty && ++i < (1u << 22)) {
@@ -211,7 +215,7 @@ struct ScanTile {
 template <typename T, int VW, bool SIG, bool BACK, int MODE, bool NT, bool FULL>
 __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& tile, float* sa, float* ss) {
     typedef typename Packed<T, VW>::V V;
-    constexpr int N = scan_thread_steps(BACK);
+    constexpr int N = scan_thread_steps(SIG, BACK);
     const uint32_t tid = threadIdx.x, R = a.lanes, slots = R * VW;
     const uint32_t r = tid % R, g = tid / R, G = blockDim.x / R, b = tile.b;
     const uint32_t c = min(tile.slot0 + r * VW, a.channels - VW);
@@ -249,30 +253,24 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
         if (tile.k == 0 && a.h0) h0 = load_any<VW>(a.h0 + uint64_t(b) * a.channels + c);
     }
 
-    // the thread's steps composed: s the state from 0, p the product of gates.  Backward keeps
-    // what reaches step t: dh + s before it, and p before it.
-    FVec<VW> S = 0.f, P = 1.f, sv[N], pv[N];
+    // the thread's steps composed: S the state from 0, P the product of gates.  Forward keeps both
+    // after every step.
+    FVec<VW> S = 0.f, P = 1.f, sv[BACK ? 1 : N], pv[BACK ? 1 : N];
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         const FVec<VW> z = to_float<VW, T>(zr[u]), x = to_float<VW, T>(xr[u]);
+        const bool on = FULL || u < left;
 #pragma unroll
         for (int v = 0; v < VW; ++v) {
             float f, m;
             gates<T, SIG>(z[v], f, m);
-            const bool on = FULL || u < left;
             f = on ? f : 1.f;
-            if (BACK) {
-                const float l = (on ? x[v] : 0.f) + S[v];
-                sv[u][v] = l;
-                pv[u][v] = P[v];
-                S[v] = f * l;
-                P[v] *= f;
-            } else {
-                S[v] = __builtin_fmaf(f, S[v], on ? m * x[v] : 0.f);
-                P[v] *= f;
-                sv[u][v] = S[v];
-                pv[u][v] = P[v];
-            }
+            S[v] = BACK ? f * ((on ? x[v] : 0.f) + S[v]) : __builtin_fmaf(f, S[v], on ? m * x[v] : 0.f);
+            P[v] *= f;
+        }
+        if (!BACK) {
+            sv[u] = S;
+            pv[u] = P;
         }
     }
 #pragma unroll
@@ -294,8 +292,8 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
             leave_pair(static_cast<uint64_t*>(a.words) + word + tid, composed(A), C);
     }
     if (MODE == kScanBack && !tile.first)
-        s0 = look_back(static_cast<const uint64_t*>(a.words) + word, BACK ? int64_t(slots) : -int64_t(slots),
-                       tile.before, slots);
+        s0 = look_back<scan_window(BACK)>(static_cast<const uint64_t*>(a.words) + word,
+                                          BACK ? int64_t(slots) : -int64_t(slots), tile.before, slots);
     if (tid < slots) {
         const uint32_t sc = min(tile.slot0 + tid / VW * VW, a.channels - VW) + tid % VW;   // the slot's channel
         const uint64_t state = uint64_t(b) * a.channels + sc;
@@ -332,11 +330,13 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
             h += a.h.ts;
         }
     } else {
+        // the recurrence again, now from the state that is carried in: the gates are needed here in any
+        // case, and no step's composition has to wait in registers
         T* dg = view_at<T>(a.dgate, b, ta, c);
         T* dx = view_at<T>(a.dx, b, ta, c);
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-            const FVec<VW> z = to_float<VW, T>(zr[u]);
+            const FVec<VW> z = to_float<VW, T>(zr[u]), d = to_float<VW, T>(xr[u]);
             FVec<VW> before = to_float<VW, T>(hr[u]), og, ox;
             // only a tile's last thread can hold step 0, as its last step
             if (!FULL || u == N - 1) before = ta == uint64_t(u) ? h0 : before;
@@ -345,8 +345,9 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
             for (int v = 0; v < VW; ++v) {
                 float f, m;
                 gates<T, SIG>(z[v], f, m);
-                const float l = __builtin_fmaf(pv[u][v], s[v], sv[u][v]);
-                og[v] = SIG ? l * before[v] * f * m : l * before[v];
+                const float l = d[v] + s[v];
+                s[v] = f * l;
+                og[v] = SIG ? s[v] * before[v] * m : l * before[v];
                 ox[v] = l * m;
             }
             if (FULL || u < left) {

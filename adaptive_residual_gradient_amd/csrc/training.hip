@@ -460,9 +460,9 @@ int check_shape(const adacomp_scan_shape* s) {
 
 // Tiles of one shape for vectors of vw channels.
 ScanLayout scan_layout(const adacomp_scan_shape& s, uint32_t vw, bool back) {
+    const uint32_t per = adacomp::scan_thread_steps(s.sigmoid != 0, back);
     using namespace adacomp;
     ScanLayout l{};
-    const uint32_t per = scan_thread_steps(back);
     if (s.length <= kScanShort) {   // one thread per vector
         l.lanes = (s.channels + vw - 1) / vw;
         return l;
@@ -486,10 +486,12 @@ ScanLayout scan_layout(const adacomp_scan_shape& s, uint32_t vw, bool back) {
 // Channels of one thread: 4 bytes.
 uint32_t scan_vector(const adacomp_scan_shape& s) { return s.type == ADACOMP_FLOAT || s.channels < 2 ? 1 : 2; }
 // What either direction and any type of this shape needs.
-uint64_t scan_workspace(const adacomp_scan_shape& s) {
+uint64_t scan_workspace(adacomp_scan_shape s) {
     uint64_t most = 0;
-    for (const bool back : {false, true})
-        for (uint32_t vw = 1; vw <= std::min(s.channels, 2u); ++vw) most = std::max(most, scan_layout(s, vw, back).ws);
+    for (s.sigmoid = 0; s.sigmoid < 2; ++s.sigmoid)
+        for (const bool back : {false, true})
+            for (uint32_t vw = 1; vw <= std::min(s.channels, 2u); ++vw)
+                most = std::max(most, scan_layout(s, vw, back).ws);
     return most;
 }
 

@@ -473,9 +473,9 @@ int adacomp_layer_norm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t* b
  *   h_t = a_t * h_(t-1) + k_t * x_t,   t = 0 .. n_b - 1
  *   sigmoid = 1:  a = 1 / (1 + exp(-gate)),  k = 1 / (1 + exp(gate))  (= 1 - a)
  *   sigmoid = 0:  a = gate,  k = 1
- * states in float32.  The sequence is cut into chunks whose gate products are
- * formed, so with sigmoid = 0 products of up to 512 consecutive gates have to
- * stay within float32's range (gates in [-1, 1] always do). */
+ * states in float32.  The sequence is cut into tiles whose gate products are
+ * formed and joined, so with sigmoid = 0 the products of consecutive gates,
+ * however many, have to stay within float32's range (gates in [-1, 1] always do). */
 typedef struct adacomp_scan_shape {
     uint64_t length;      /* steps, n_b <= length; may be 0 */
     uint32_t batch;       /* sequences; may be 0 */
