@@ -353,21 +353,23 @@ __global__ __launch_bounds__(kNormBackThreads) void k_layer_norm_backward(NormAr
     }
     if (a.partial == nullptr) return;
     float* out = a.partial + uint64_t(blockIdx.x) * 2 * a.cols;
+    // Whole vectors at their places of a row without moved-back ones, 16 bytes a lane; those that were
+    // moved back are found there again.
     __syncthreads();   // the weight has been read
+    FVec<VEC>* sums = reinterpret_cast<FVec<VEC>*>(dynamic) + lane;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            if (k < cols.skip[j]) continue;
-            dynamic[mine * span + cols.at[j] + k] = dw[j][k];
-            dynamic[(teams + mine) * span + cols.at[j] + k] = db[j][k];
-        }
+    for (int j = 0; j < NV; ++j) {
+        sums[mine * (span / VEC) + j * team] = dw[j];
+        sums[(teams + mine) * (span / VEC) + j * team] = db[j];
+    }
     __syncthreads();
+    const uint32_t whole = a.cols / VEC * VEC;   // columns of vectors in their own place
     for (uint32_t i = threadIdx.x; i < 2 * a.cols; i += blockDim.x) {
         const uint32_t which = i >= a.cols, c = i - which * a.cols;
+        const uint32_t at = c < whole ? c : whole + VEC - (a.cols - c);
         float s = 0.f;
 #pragma unroll 4
-        for (uint32_t t = 0; t < teams; ++t) s += dynamic[(which * teams + t) * span + c];
+        for (uint32_t t = 0; t < teams; ++t) s += dynamic[(which * teams + t) * span + at];
         out[i] = s;
     }
 }
