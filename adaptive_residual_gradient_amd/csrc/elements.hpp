@@ -40,6 +40,16 @@ template <int N, typename T>
 __device__ __forceinline__ void stream_store(T* p, typename Packed<T, N>::V v) {
     __builtin_nontemporal_store(v, reinterpret_cast<typename Packed<T, N>::Any*>(p));
 }
+// Either, by NT (non-temporal).
+template <int N, bool NT, typename T>
+__device__ __forceinline__ typename Packed<T, N>::V load_hint(const T* p) {
+    return NT ? stream_load<N>(p) : load_any<N>(p);
+}
+template <int N, bool NT, typename T>
+__device__ __forceinline__ void store_hint(T* p, typename Packed<T, N>::V v) {
+    if (NT) stream_store<N>(p, v);
+    else store_any<N>(p, v);
+}
 template <int N, typename T>
 __device__ __forceinline__ FVec<N> to_float(typename Packed<T, N>::V v) {
     return __builtin_convertvector(v, FVec<N>);

@@ -101,19 +101,6 @@ __device__ __forceinline__ T* view_at(const ScanView& v, uint32_t b, uint64_t t,
 
 // ---- tiles ----
 
-// Non-temporal accesses where every row starts on a cache line; elsewhere the
-// lines at a tile's edges serve the neighbouring channels' tiles as well, which
-// run on the same chiplet, and have to stay in its cache.
-template <int N, bool NT, typename T>
-__device__ __forceinline__ typename Packed<T, N>::V load_hint(const T* p) {
-    return NT ? stream_load<N>(p) : load_any<N>(p);
-}
-template <int N, bool NT, typename T>
-__device__ __forceinline__ void store_hint(T* p, typename Packed<T, N>::V v) {
-    if (NT) stream_store<N>(p, v);
-    else store_any<N>(p, v);
-}
-
 // A state on its way to the next tile: its bits, of which this NaN's stand for
 // "not there yet".
 constexpr uint32_t kScanEmpty = 0xFFFFFFFFu;

@@ -266,7 +266,7 @@ uint32_t norm_blocks(uint64_t need, uint32_t most) {
         }                                                            \
     } while (0)
 
-template <typename T>
+template <typename T, int KEEP>
 void launch_norm(const adacomp::NormArgs& a, hipStream_t s) {
     using namespace adacomp;
     constexpr int VEC = norm_vec<T>(), NVMAX = kNormElems / VEC;
@@ -275,11 +275,11 @@ void launch_norm(const adacomp::NormArgs& a, hipStream_t s) {
         hipLaunchKernelGGL(k_layer_norm_wide<T>, dim3(rows), dim3(kNormWideThreads), 0, s, a);
     } else if (a.cols > kNormWaveCols) {
         const uint32_t waves = (a.cols + kNormWaveCols - 1) / kNormWaveCols;
-        hipLaunchKernelGGL((k_layer_norm<T, VEC, NVMAX, 64, true>), dim3(norm_blocks(rows, kNormMaxWaves / waves)),
+        hipLaunchKernelGGL((k_layer_norm<T, VEC, NVMAX, 64, true, KEEP>), dim3(norm_blocks(rows, kNormMaxWaves / waves)),
                            dim3(64 * waves), 0, s, a);
     } else {
 #define ADACOMP_LN(V, NV, LANES)                                                              \
-    hipLaunchKernelGGL((k_layer_norm<T, V, NV, LANES, false>),                                \
+    hipLaunchKernelGGL((k_layer_norm<T, V, NV, LANES, false, KEEP>),                                \
                        dim3(norm_blocks((rows + 256 / LANES - 1) / (256 / LANES), kNormMaxWaves / 4)), dim3(256), 0, \
                        s, a)
         ADACOMP_NORM_TEAMS(ADACOMP_LN);
@@ -288,7 +288,7 @@ void launch_norm(const adacomp::NormArgs& a, hipStream_t s) {
 }
 
 // Returns the number of partial rows written.
-template <typename T>
+template <typename T, int KEEP>
 uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
     using namespace adacomp;
     constexpr int VEC = norm_vec<T>(), NVMAX = kNormElems / VEC;
@@ -307,7 +307,7 @@ uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
         const uint32_t waves = (a.cols + kNormWaveCols - 1) / kNormWaveCols;
         const uint32_t teams = teams_of(kNormBackThreads / 64 / waves);
         const uint32_t n = norm_blocks((rows + teams - 1) / teams, most);
-        hipLaunchKernelGGL((k_layer_norm_backward<T, VEC, NVMAX, 64, true>), dim3(n), dim3(64 * waves * teams),
+        hipLaunchKernelGGL((k_layer_norm_backward<T, VEC, NVMAX, 64, true, KEEP>), dim3(n), dim3(64 * waves * teams),
                            2 * 4 * kNormWaveCols * waves * teams, s, a);
         return n;
     }
@@ -316,7 +316,7 @@ uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
     do {                                                                                        \
         const uint32_t teams = teams_of(kNormBackThreads / LANES);                              \
         n = norm_blocks((rows + teams - 1) / teams, most);                                      \
-        hipLaunchKernelGGL((k_layer_norm_backward<T, V, NV, LANES, false>), dim3(n),            \
+        hipLaunchKernelGGL((k_layer_norm_backward<T, V, NV, LANES, false, KEEP>), dim3(n),            \
                            dim3(teams * LANES), 2 * 4 * teams * LANES * NV * V, s, a);          \
     } while (0)
     ADACOMP_NORM_TEAMS(ADACOMP_LNB);
@@ -324,6 +324,29 @@ uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
     return n;
 }
 #undef ADACOMP_NORM_TEAMS
+
+int norm_keep(uint64_t read, uint64_t written) {
+    return read <= adacomp::kNormKeepBytes ? adacomp::kNormKeepIn
+                                           : written <= adacomp::kNormKeepBytes ? adacomp::kNormKeepOut
+                                                                                : adacomp::kNormKeepNone;
+}
+template <typename T>
+void launch_norm(const adacomp::NormArgs& a, hipStream_t s) {
+    const uint64_t bytes = a.rows * a.cols * sizeof(T);
+    switch (norm_keep(bytes, bytes)) {
+        case adacomp::kNormKeepIn: return launch_norm<T, adacomp::kNormKeepIn>(a, s);
+        default: return launch_norm<T, adacomp::kNormKeepNone>(a, s);   // the output is as large as the input
+    }
+}
+template <typename T>
+uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
+    const uint64_t bytes = a.rows * a.cols * sizeof(T);
+    switch (norm_keep(2 * bytes, bytes)) {
+        case adacomp::kNormKeepIn: return launch_norm_backward<T, adacomp::kNormKeepIn>(a, s);
+        case adacomp::kNormKeepOut: return launch_norm_backward<T, adacomp::kNormKeepOut>(a, s);
+        default: return launch_norm_backward<T, adacomp::kNormKeepNone>(a, s);
+    }
+}
 
 }  // namespace
 
@@ -578,7 +601,9 @@ int check_scan(const ScanCall& c) {
     return ADACOMP_OK;
 }
 
-// Whether every step of every view the call touches starts on a cache line.
+// Non-temporal accesses where every step of every view the call touches starts on a cache line; elsewhere
+// the lines at a tile's edges serve the neighbouring channels' tiles as well, which run on the same
+// chiplet, and have to stay in its cache.
 bool scan_lines(const adacomp::ScanArgs& a, uint64_t size) {
     for (const adacomp::ScanView* v : {&a.gate, &a.x, &a.h, &a.dh, &a.dgate, &a.dx})
         if (v->p && (!aligned_to(v->p, 128) || v->ts * size % 128 != 0 || v->bs * size % 128 != 0)) return false;
