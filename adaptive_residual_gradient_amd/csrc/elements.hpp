@@ -13,6 +13,10 @@ typedef _Float16 f16;
 template <int N>
 using FVec = float __attribute__((ext_vector_type(N)));
 
+// Most bytes of a call's inputs (or output) that are worth a place in the 256 MB cache in front of the
+// memory: beside them it holds what the calls around this one touch.
+constexpr uint64_t kKeepBytes = 96u << 20;
+
 // N elements at any address aligned to one element: gfx950 reads and writes
 // 16 bytes from any address, so rows of odd widths keep wide accesses (a row
 // that starts inside a 16-byte granule costs one more cache line, not a loop

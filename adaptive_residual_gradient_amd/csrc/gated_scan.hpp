@@ -43,6 +43,11 @@ constexpr int kScanAlone = 0, kScanChain = 1, kScanBack = 2;
 // meanwhile (1 x 65536 x 256 f32: backward 72.7 us with 4, 74.8 with 8; forward 50.5 and 49.4).
 constexpr uint32_t scan_window(bool back) { return back ? 4 : 8; }
 
+// Accesses: non-temporal; non-temporal results and inputs of at most kKeepBytes, which the call before
+// has just written, through the cache (8 x 2048 x 1024 bf16 22.0 us and 26.8, but backward, with twice
+// the inputs, 48.8 and 44.7); all through the cache.
+constexpr int kScanStream = 0, kScanKeepIn = 1, kScanCached = 2;
+
 struct ScanView {
     void* p;
     uint64_t bs, ts;   // batch and time strides in elements
@@ -203,7 +208,7 @@ struct ScanTile {
 // no load stands under a condition (one that does is waited for at once).
 // Where the channels are no multiple of the vector the last lanes move back and
 // repeat their neighbours' channels, with the same results.
-template <typename T, int VW, bool SIG, bool BACK, int MODE, bool NT, bool FULL>
+template <typename T, int VW, bool SIG, bool BACK, int MODE, int ACCESS, bool FULL>
 __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& tile, float* sa, float* ss) {
     typedef typename Packed<T, VW>::V V;
     constexpr int N = scan_thread_steps(SIG, BACK);
@@ -220,7 +225,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
         const int64_t step = BACK ? -int64_t(view.ts) : int64_t(view.ts);
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-            v[u] = load_hint<VW, NT>(p);
+            v[u] = load_hint<VW, ACCESS == kScanStream>(p);
             if (u + 1 < N) p += FULL || u + 1 < left ? step : 0;
         }
     };
@@ -239,7 +244,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
                 p -= a.h.ts;
                 --t;
             }
-            hr[u] = load_hint<VW, NT>(p);
+            hr[u] = load_hint<VW, ACCESS == kScanStream>(p);
         }
         if (tile.k == 0 && a.h0) h0 = load_any<VW>(a.h0 + uint64_t(b) * a.channels + c);
     }
@@ -317,7 +322,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
             FVec<VW> o;
 #pragma unroll
             for (int v = 0; v < VW; ++v) o[v] = __builtin_fmaf(pv[u][v], s[v], sv[u][v]);
-            if (FULL || u < left) store_hint<VW, NT>(h, from_float<T, VW>(o));
+            if (FULL || u < left) store_hint<VW, ACCESS != kScanCached>(h, from_float<T, VW>(o));
             h += a.h.ts;
         }
     } else {
@@ -342,8 +347,8 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
                 ox[v] = l * m;
             }
             if (FULL || u < left) {
-                store_hint<VW, NT>(dg, from_float<T, VW>(og));
-                store_hint<VW, NT>(dx, from_float<T, VW>(ox));
+                store_hint<VW, ACCESS != kScanCached>(dg, from_float<T, VW>(og));
+                store_hint<VW, ACCESS != kScanCached>(dx, from_float<T, VW>(ox));
             }
             dg -= a.dgate.ts;
             dx -= a.dx.ts;
@@ -351,7 +356,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
     }
 }
 
-template <typename T, int VW, bool SIG, bool BACK, int MODE, bool NT>
+template <typename T, int VW, bool SIG, bool BACK, int MODE, int ACCESS>
 __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
     __shared__ float sa[kScanThreads * VW], ss[kScanThreads * VW];   // [sub-chunk][slot]
     __shared__ uint32_t ticket;
@@ -393,17 +398,17 @@ __global__ __launch_bounds__(kScanThreads, 4) void k_scan_tile(ScanArgs a) {
         const typename Packed<T, VW>::V zero = {};
         for (uint64_t t = tile.tend + tid / a.lanes; t < t1; t += blockDim.x / a.lanes) {
             if (BACK) {
-                store_hint<VW, NT>(view_at<T>(a.dgate, tile.b, t, c), zero);
-                store_hint<VW, NT>(view_at<T>(a.dx, tile.b, t, c), zero);
+                store_hint<VW, ACCESS != kScanCached>(view_at<T>(a.dgate, tile.b, t, c), zero);
+                store_hint<VW, ACCESS != kScanCached>(view_at<T>(a.dx, tile.b, t, c), zero);
             } else {
-                store_hint<VW, NT>(view_at<T>(a.h, tile.b, t, c), zero);
+                store_hint<VW, ACCESS != kScanCached>(view_at<T>(a.h, tile.b, t, c), zero);
             }
         }
     }
     if (tile.count == a.steps) {
-        scan_tile<T, VW, SIG, BACK, MODE, NT, true>(a, tile, sa, ss);
+        scan_tile<T, VW, SIG, BACK, MODE, ACCESS, true>(a, tile, sa, ss);
     } else if (tile.count > 0) {
-        scan_tile<T, VW, SIG, BACK, MODE, NT, false>(a, tile, sa, ss);
+        scan_tile<T, VW, SIG, BACK, MODE, ACCESS, false>(a, tile, sa, ss);
     } else if (n == 0 && tile.k == 0 && a.last && tid < slots) {   // an empty sequence
         const uint32_t c = min(tile.slot0 + tid / VW * VW, a.channels - VW) + tid % VW;
         const uint64_t state = uint64_t(tile.b) * a.channels + c;

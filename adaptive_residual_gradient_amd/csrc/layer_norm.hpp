@@ -30,11 +30,10 @@ constexpr uint32_t kNormBackThreads = 512;                // most threads of a w
 
 // What a call leaves to the 256 MB cache in front of the memory, the rest going past it by
 // non-temporal accesses: its inputs, which the call before has just written, where they are at most
-// kNormKeepBytes, else its output where that is.  Inputs kept against nothing kept: 4099 x 1000
+// kKeepBytes, else its output where that is.  Inputs kept against nothing kept: 4099 x 1000
 // float32 gradient 14.6 us and 17.0, 32768 x 1024 bf16 21.6 and 24.9, but 16384 x 4096 bf16 52.0 and
 // 48.3; the output kept: 32768 x 1024 bf16 gradient 38.9 us and 40.9.
 constexpr int kNormKeepNone = 0, kNormKeepIn = 1, kNormKeepOut = 2;
-constexpr uint64_t kNormKeepBytes = 96u << 20;
 
 struct NormArgs {
     const void* x;

@@ -326,8 +326,8 @@ uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
 #undef ADACOMP_NORM_TEAMS
 
 int norm_keep(uint64_t read, uint64_t written) {
-    return read <= adacomp::kNormKeepBytes ? adacomp::kNormKeepIn
-                                           : written <= adacomp::kNormKeepBytes ? adacomp::kNormKeepOut
+    return read <= adacomp::kKeepBytes ? adacomp::kNormKeepIn
+                                           : written <= adacomp::kKeepBytes ? adacomp::kNormKeepOut
                                                                                 : adacomp::kNormKeepNone;
 }
 template <typename T>
@@ -601,16 +601,18 @@ int check_scan(const ScanCall& c) {
     return ADACOMP_OK;
 }
 
-// Non-temporal accesses where every step of every view the call touches starts on a cache line; elsewhere
-// the lines at a tile's edges serve the neighbouring channels' tiles as well, which run on the same
-// chiplet, and have to stay in its cache.
-bool scan_lines(const adacomp::ScanArgs& a, uint64_t size) {
+// How a call's views are accessed.  Where a step of one does not start on a cache line, the lines at a
+// tile's edges serve the neighbouring channels' tiles as well, which run on the same chiplet, and have
+// to stay in its cache.
+int scan_access(const adacomp::ScanArgs& a, uint64_t size, uint64_t inputs) {
     for (const adacomp::ScanView* v : {&a.gate, &a.x, &a.h, &a.dh, &a.dgate, &a.dx})
-        if (v->p && (!aligned_to(v->p, 128) || v->ts * size % 128 != 0 || v->bs * size % 128 != 0)) return false;
-    return true;
+        if (v->p && (!aligned_to(v->p, 128) || v->ts * size % 128 != 0 || v->bs * size % 128 != 0))
+            return adacomp::kScanCached;
+    return inputs * size * a.batch * a.length * a.channels <= adacomp::kKeepBytes ? adacomp::kScanKeepIn
+                                                                                  : adacomp::kScanStream;
 }
 
-template <typename T, int VW, bool SIG, bool BACK, bool NT>
+template <typename T, int VW, bool SIG, bool BACK, int ACCESS>
 int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t s) {
     using namespace adacomp;
     const uint64_t chains = uint64_t(a.batch) * l.groups, n = chains * l.tiles;
@@ -618,7 +620,7 @@ int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t
     if ((chains + kScanQueues) * l.tiles * l.threads >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;
     const dim3 block(l.threads);
     if (l.tiles == 1) {
-        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanAlone, NT>), dim3(uint32_t(n)), block, 0, s, a);
+        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanAlone, ACCESS>), dim3(uint32_t(n)), block, 0, s, a);
         return launch_status();
     }
     const uint64_t vecs = (kScanCountBytes + n * l.lanes * VW * (l.chain ? 4 : 8) + 15) / 16;
@@ -629,8 +631,8 @@ int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t
                        vecs);
     if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
     const dim3 grid(uint32_t((chains + a.queues - 1) / a.queues * a.queues * l.tiles));
-    if (l.chain) hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain, NT>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanBack, NT>), grid, block, 0, s, a);
+    if (l.chain) hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain, ACCESS>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanBack, ACCESS>), grid, block, 0, s, a);
     return launch_status();
 }
 
@@ -642,8 +644,11 @@ int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t
         hipLaunchKernelGGL((k_scan_short<T, VW, SIG, BACK>), dim3(uint32_t(blocks)), dim3(256), 0, s, a);
         return launch_status();
     }
-    return scan_lines(a, sizeof(T)) ? launch_scan<T, VW, SIG, BACK, true>(a, l, ws, s)
-                                    : launch_scan<T, VW, SIG, BACK, false>(a, l, ws, s);
+    switch (scan_access(a, sizeof(T), BACK ? (SIG ? 4 : 3) : 2)) {
+        case kScanStream: return launch_scan<T, VW, SIG, BACK, kScanStream>(a, l, ws, s);
+        case kScanKeepIn: return launch_scan<T, VW, SIG, BACK, kScanKeepIn>(a, l, ws, s);
+        default: return launch_scan<T, VW, SIG, BACK, kScanCached>(a, l, ws, s);
+    }
 }
 
 template <typename T, int VW>
