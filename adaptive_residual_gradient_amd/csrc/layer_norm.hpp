@@ -10,7 +10,7 @@
 // joins its sums by lane moves alone; a wider one to a workgroup of one
 // wavefront per 1024 columns, joined through LDS; past 16384 columns a
 // workgroup reads the row once per pass.  16384 x 4096 bf16 takes 47 us (5.7
-// TB/s), the gradients of 32768 x 1024 bf16 36.9 us (5.5 TB/s) and 4.6 us for
+// TB/s), the gradients of 32768 x 1024 bf16 34.2 us (6.0 TB/s) and 4.8 us for
 // the weight's partial rows.
 #pragma once
 
