@@ -268,11 +268,28 @@ __global__ __launch_bounds__(256) void k_adamw_packed(AdamwArgs a) {
         const double g = double(g4[c]) * factor;
         m[c] = b1 * m[c] + a.omb1 * g;
         v[c] = b2 * v[c] + omb2 * (g * g);
-        // the weights' step: the hardware's root and reciprocal are off by one unit in the last
-        // place of a term that is far below the weight
-        const float denom = __builtin_fmaf(__builtin_amdgcn_sqrtf(float(v[c])), rbc2, a.eps);
-        w4[c] = __builtin_fmaf(w4[c], keep, -size * (float(m[c]) * __builtin_amdgcn_rcpf(denom)));
     }
+    // the weights' step: the hardware's root and reciprocal are off by one unit in the last place of a
+    // term that is far below the weight
+    float q[4];
+    bool far = false;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float u = float(v[c]);
+        far |= u == __builtin_inff();
+        q[c] = float(m[c]) * __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_amdgcn_sqrtf(u), rbc2, a.eps));
+    }
+    // v past 2^(128 - kUp), of gradients past 1e16 or so: root, denominator and m times 2^-65
+    if (far) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (float(v[c]) != __builtin_inff()) continue;
+            const float root = __builtin_amdgcn_sqrtf(float(v[c] * power_of_two(-130 - kUp)));
+            q[c] = float(m[c] * 0x1p-65) * __builtin_amdgcn_rcpf(__builtin_fmaf(root, a.rbc2, a.eps * 0x1p-65f));
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w4[c] = __builtin_fmaf(w4[c], keep, -size * q[c]);
     // every lane takes part: a block's lanes hold 0 past the end
     const int ms = block_scale<0>(block_top(m)), vs = block_scale<kUp>(block_top(v));
     const double m_up = power_of_two(127 - ms), v_up = power_of_two(127 - vs - kUp);
