@@ -30,7 +30,8 @@ struct AdamwArgs {
     bf16* w16;           // nullable
     const float* clip;   // nullable
     double beta1, beta2, omb1, omb2;
-    float lr, inv_bc1, rbc2, eps, scale;   // inv_bc1 = 1 / (1 - beta1^t)
+    double lr, inv_bc1;   // inv_bc1 = 1 / (1 - beta1^t)
+    float rbc2, eps, scale;
     uint32_t key;        // hash of seed and step
 };
 
@@ -126,15 +127,23 @@ __device__ __forceinline__ OptTile step_tile(const AdamwArgs& a) {
     return a.tiles[a.clip ? gridDim.x - 1 - blockIdx.x : blockIdx.x];
 }
 
+// A tile's step size and decay factor, formed in float64 and rounded once: six operations a thread,
+// beside 60 and more on its elements.
+struct Factors {
+    float size, keep;
+};
+__device__ __forceinline__ Factors tile_factors(const AdamwArgs& a, const OptTile& tile) {
+    const double lr = a.lr * double(tile.lr_scale);
+    return {float(lr * a.inv_bc1), float(1.0 - lr * double(tile.weight_decay))};
+}
+
 // ---- float32 moments ----
 
 template <typename G>
 __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
     const OptTile tile = step_tile(a);
     const int tid = threadIdx.x;
-    const float lr = a.lr * tile.lr_scale;
-    const float size = lr * a.inv_bc1;
-    const float keep = 1.0f - lr * tile.weight_decay;
+    const Factors f = tile_factors(a, tile);
     const float factor = a.clip ? a.clip[1] * a.scale : a.scale;
     const float b1 = float(a.beta1), b2 = float(a.beta2), omb1 = float(a.omb1), omb2 = float(a.omb2);
     float* m = static_cast<float*>(a.m);
@@ -150,7 +159,7 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
         m4[c] = __builtin_fmaf(b1, m4[c], omb1 * g);
         v4[c] = __builtin_fmaf(b2, v4[c], omb2 * (g * g));
         const float denom = __builtin_fmaf(sqrtf(v4[c]), a.rbc2, a.eps);
-        w4[c] = __builtin_fmaf(w4[c], keep, -size * (m4[c] / denom));
+        w4[c] = __builtin_fmaf(w4[c], f.keep, -f.size * (m4[c] / denom));
     }
     store_part(a.w + at, w4, left);
     store_part(m + at, m4, left);
@@ -220,9 +229,7 @@ template <typename G>
 __global__ __launch_bounds__(256) void k_adamw_packed(AdamwArgs a) {
     const OptTile tile = step_tile(a);
     const int tid = threadIdx.x;
-    const float lr = a.lr * tile.lr_scale;
-    const float size = lr * a.inv_bc1;
-    const float keep = 1.0f - lr * tile.weight_decay;
+    const Factors f = tile_factors(a, tile);
     const double factor = a.clip ? double(a.clip[1]) * double(a.scale) : double(a.scale);
     uint8_t* mc = static_cast<uint8_t*>(a.m);
     uint8_t* vc = static_cast<uint8_t*>(a.v);
@@ -289,7 +296,7 @@ __global__ __launch_bounds__(256) void k_adamw_packed(AdamwArgs a) {
         }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) w4[c] = __builtin_fmaf(w4[c], keep, -size * q[c]);
+    for (int c = 0; c < 4; ++c) w4[c] = __builtin_fmaf(w4[c], f.keep, -f.size * q[c]);
     // every lane takes part: a block's lanes hold 0 past the end
     const int ms = block_scale<0>(block_top(m)), vs = block_scale<kUp>(block_top(v));
     const double m_up = power_of_two(127 - ms), v_up = power_of_two(127 - vs - kUp);

@@ -84,7 +84,7 @@ int adamw_impl(const adacomp_optimizer* o, float* weights, const void* grad, int
     a.beta2 = p->beta2;
     a.omb1 = 1.0 - a.beta1;
     a.omb2 = 1.0 - a.beta2;
-    a.inv_bc1 = float(1.0 / (1.0 - std::pow(a.beta1, double(p->step))));
+    a.inv_bc1 = 1.0 / (1.0 - std::pow(a.beta1, double(p->step)));
     a.rbc2 = float(1.0 / std::sqrt(1.0 - std::pow(a.beta2, double(p->step))));
     a.eps = p->eps;
     a.scale = p->scale;

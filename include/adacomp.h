@@ -394,8 +394,10 @@ int adacomp_grad_norm(const adacomp_optimizer* optimizer, const void* grad, int 
  *   m = beta1 * m + (1 - beta1) * g;   v = beta2 * v + (1 - beta2) * (g * g)
  *   w = w * (1 - lr_i * weight_decay_i)
  *         - lr_i / (1 - beta1^step) * (m / (sqrt(v) / sqrt(1 - beta2^step) + eps))
- * 1 - beta and the bias corrections are formed in float64.  step >= 1 counts the calls made so far, this one included; it and
- * lr are values of the call, so a captured step replays with the same ones. */
+ * 1 - beta, the bias corrections, lr_i, the step size lr_i / (1 - beta1^step)
+ * and the decay factor are formed in float64, each rounded once.  step >= 1
+ * counts the calls made so far, this one included; it and lr are values of the
+ * call, so a captured step replays with the same ones. */
 typedef struct adacomp_adamw {
     float lr;
     float beta1;

@@ -32,3 +32,28 @@ def test_packed_step_of_large_gradients(size):
     m, v = R.moments(R.f64(g) * p["scale"], np.zeros(n), np.zeros(n), p)
     new, step, denom = R.adamw_weights(w0, m, v, p, 0.1, 1.0)
     R.assert_within(w, new, R.weight_bound(w0, new, m, R.U * np.abs(m), step, denom), "w")
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_decay_and_step_size_are_rounded_once(packed):
+    """Without a gradient a weight of 1 becomes the decay factor; with a denominator of 1 a weight of 0
+    becomes the step size times m.  Both factors are formed in float64."""
+    rng = np.random.default_rng(2)
+    table = [(4 * i, 4, R.f32(rng.uniform(0.01, 30.0)), R.f32(rng.uniform(0.1, 3.0))) for i in range(500)]
+    opt = A.Optimizer(table)
+    n = 4 * len(table)
+    dt = torch.uint8 if packed else torch.float32
+    p = dict(lr=R.f32(0.0123), beta1=0.9, beta2=0.999, eps=1.0, step=3)
+    step = A.adamw_packed if packed else A.adamw
+    extra = lambda: (opt.moment_scales(DEV),) if packed else ()
+    w, zero = torch.ones(n, device=DEV), torch.zeros(n, device=DEV)
+    m, v = (torch.zeros(n, dtype=dt, device=DEV) for _ in range(2))
+    step(opt, w, zero, m, v, *extra(), **p)
+    lr = np.array([p["lr"] * t[3] for t in table])
+    keep = (1.0 - lr * np.array([t[2] for t in table])).astype(np.float32)
+    assert np.array_equal(w.cpu().numpy(), np.repeat(keep, 4))
+    if not packed:
+        w, m, v = torch.zeros(n, device=DEV), torch.randn(n, device=DEV), torch.zeros(n, device=DEV)
+        step(opt, w, zero, m, v, **p)
+        size = (lr / (1.0 - R.f32(0.9) ** 3)).astype(np.float32)
+        assert np.array_equal(w.cpu().numpy(), -np.repeat(size, 4) * m.cpu().numpy())
