@@ -15,8 +15,8 @@
 //   - through one word a channel that each tile leaves for its successor
 //     (kScanChain), where there are enough independent chains of tiles to hide
 //     that hop of about 1.3 us;
-//   - of few long chains, through the compositions of all tiles on the way to
-//     the last one whose state is known, many at a time (kScanBack).
+//   - of few long chains, through the compositions of the tiles and of groups of
+//     tiles before, many at a time (kScanBack).
 // Sequences of at most kScanShort steps take one thread per 4 bytes of
 // channels (k_scan_short).
 //
@@ -39,9 +39,10 @@ constexpr uint32_t kScanThreads = 512;  // most threads of a tile
 constexpr uint32_t kScanQueues = 64;    // most ticket counters
 constexpr uint32_t kScanCountBytes = kScanQueues * 64;   // each on a line of its own
 constexpr int kScanAlone = 0, kScanChain = 1, kScanBack = 2;
-// Tiles a thread of kScanBack looks at together: backward fewer, for its registers hold the inputs
-// meanwhile (1 x 65536 x 256 f32: backward 72.7 us with 4, 74.8 with 8; forward 50.5 and 49.4).
-constexpr uint32_t scan_window(bool back) { return back ? 4 : 8; }
+// Words that a thread of kScanBack looks at together, of tiles and of groups of tiles each.  8 tiles' forward
+// takes 114 registers instead of 77 (1 x 20000 x 1000 f32 58.5 us and 53.1), or more than there are
+// (4 x 8000 x 512 bf16 36.8 and 27.5).
+constexpr uint32_t kScanWindow = 4;
 
 // Accesses: non-temporal; non-temporal results and inputs of at most kKeepBytes, which the call before
 // has just written, through the cache (8 x 2048 x 1024 bf16 22.0 us and 26.8, but backward, with twice
@@ -61,9 +62,11 @@ struct ScanArgs {
     const int32_t* lengths;  // nullable
     uint32_t* tickets;       // one counter a queue, 64 bytes apart
     void* words;             // [chain][tile][slot]: uint32_t (kScanChain) or uint64_t (kScanBack)
+    void* group_words;       // kScanBack: uint64_t [chain][group of tiles][slot]
     uint64_t length;
     uint32_t batch, channels;
     uint32_t lanes, groups, tiles, steps, queues;   // lanes a step, channel groups, tiles a chain, steps a tile
+    uint32_t span, spans, most;                     // kScanBack: tiles a group, groups a chain, groups looked at
 };
 
 // Factors on the state and on the input.  With e = exp(-z), a = 1 / (1 + e)
@@ -126,9 +129,13 @@ __device__ __forceinline__ float wait_for_state(const uint32_t* word) {
     return __builtin_nanf("");
 }
 
-// What a tile of kScanBack leaves: the state's bits below kScanKnown once its
-// carried-out state is known; before, the two floats of its composition.
-constexpr uint32_t kScanKnown = 0xFFFFFFFEu;
+// kScanBack: `span` tiles that follow each other on the way of the state make a group.  A tile looks at
+// the words of its own group's tiles and of the group's before, which those tiles leave as soon as they
+// have composed their steps, and at the groups' words before that; a group's word is left by the tile
+// behind it.  A word is a composition (two floats), or a known state where none is needed: the first
+// tile's, and that of every `most`-th group, at which the look ends.  So the state carried into a tile
+// is always joined from the same words in the same order, whichever of them are there first.
+constexpr uint32_t kScanKnown = 0xFFFFFFFEu;   // the high half of a word that holds a state
 __device__ __forceinline__ void leave_pair(uint64_t* word, uint32_t high, float s) {
     __hip_atomic_store(word, uint64_t(high) << 32 | __float_as_uint(s), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -137,56 +144,62 @@ __device__ __forceinline__ uint32_t composed(float a) {
     return bits >= kScanKnown ? 0x7FC00000u : bits;
 }
 
-// The state carried into a tile with `before` tiles before it, word `d` of
-// which (1 the nearest) is at base + d * stride.  All threads look: the subs of
-// a slot take WINDOW tiles each, nearest first, and join their maps
-// through LDS; if no known state is among them, the next window follows.  The
-// result is there for the first `slots` threads.  Every tile leaves its
-// composition before it looks itself, so no wait here hangs on another wait.
-template <uint32_t WINDOW>
-__device__ __forceinline__ float look_back(const uint64_t* base, int64_t stride, uint32_t before, uint32_t slots) {
-    __shared__ float la[kScanThreads], ls[kScanThreads];
-    __shared__ uint32_t known[kScanThreads];
-    const uint32_t tid = threadIdx.x, sub = tid / slots, slot = tid % slots, subs = blockDim.x / slots;
-    bool done = false;
-    float A = 1.f, S = 0.f;
-    for (uint32_t near = 0;; near += subs * WINDOW) {
-        const uint32_t d0 = near + sub * WINDOW + 1;
-        uint64_t w[WINDOW];
+// The n words (at most subs * WINDOW) before a place, word `d` of which (1 the nearest) is at
+// base + d * stride.  All threads look: the subs of a slot take WINDOW words each, nearest first, and
+// join their maps through LDS.
+struct LookBack {
+    static constexpr uint32_t WINDOW = kScanWindow;
+    const uint64_t* base;
+    int64_t stride;
+    uint32_t n, d0;
+    uint64_t w[WINDOW];
+    __device__ __forceinline__ uint64_t word(uint32_t d) const {
+        return __hip_atomic_load(base + int64_t(d) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ __forceinline__ LookBack(const uint64_t* words, int64_t step, uint32_t count, uint32_t slots)
+        : base(words + threadIdx.x % slots), stride(step), n(count), d0(threadIdx.x / slots * WINDOW + 1) {
+        if (n > 0) request();
+    }
+    __device__ __forceinline__ void request() {
 #pragma unroll
-        for (uint32_t u = 0; u < WINDOW; ++u)
-            w[u] = __hip_atomic_load(base + int64_t(min(d0 + u, before)) * stride + slot, __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_AGENT);
+        for (uint32_t u = 0; u < WINDOW; ++u) w[u] = word(min(d0 + u, n));
+    }
+    // Whether a word was not there yet at the last request.
+    __device__ __forceinline__ bool missing() const {
+        bool any = false;
+#pragma unroll
+        for (uint32_t u = 0; u < WINDOW; ++u) any |= uint32_t(w[u] >> 32) == kScanEmpty;
+        return any;
+    }
+    // Waits for the words.  Their map is A s + S; where the farthest is a known state S is the state itself,
+    // and A means nothing.  For the first `slots` threads.
+    __device__ __forceinline__ void join(uint32_t slots, float (&la)[kScanThreads], float (&ls)[kScanThreads], float& A,
+                                         float& S) {
+        const uint32_t tid = threadIdx.x;
+        A = 1.f;
+        S = 0.f;
+        if (n == 0) return;
+        for (uint32_t i = 0; missing() && i < (1u << 22); ++i) {   // past the bound a NaN's bits
+            __builtin_amdgcn_s_sleep(1);
+            request();   // all together: one by one each would wait a load's time again
+        }
         float a = 1.f, s = 0.f;
-        bool found = false;
 #pragma unroll
         for (uint32_t u = 0; u < WINDOW; ++u) {
-            if (found || d0 + u > before) continue;
-            uint32_t i = 0;
-            while (uint32_t(w[u] >> 32) == kScanEmpty && ++i < (1u << 22)) {
-                __builtin_amdgcn_s_sleep(1);
-                w[u] = __hip_atomic_load(base + int64_t(d0 + u) * stride + slot, __ATOMIC_RELAXED,
-                                         __HIP_MEMORY_SCOPE_AGENT);
-            }
-            const uint32_t high = uint32_t(w[u] >> 32);
+            if (d0 + u > n) continue;
             s = __builtin_fmaf(a, __uint_as_float(uint32_t(w[u])), s);
-            found = high >= kScanKnown;   // past the bound of the wait the state is a NaN's bits
-            a *= __uint_as_float(high);
+            a *= __uint_as_float(uint32_t(w[u] >> 32));
         }
         la[tid] = a;
         ls[tid] = s;
-        known[tid] = found;
         __syncthreads();
-        if (tid < slots && !done) {
-            for (uint32_t j = 0; j < subs && !done; ++j) {
-                S = __builtin_fmaf(A, ls[j * slots + tid], S);
-                A *= la[j * slots + tid];
-                done = known[j * slots + tid];
-            }
+        if (tid >= slots) return;
+        for (uint32_t j = 0; j < (n + WINDOW - 1) / WINDOW; ++j) {
+            S = __builtin_fmaf(A, ls[j * slots + tid], S);
+            A *= la[j * slots + tid];
         }
-        if (!__syncthreads_or(tid < slots && !done)) return S;
     }
-}
+};
 
 // Workgroups go to the 8 chiplets in turn.  Of 64 consecutive ones each
 // chiplet's eight take eight neighbouring chains: neighbouring channels of the
@@ -284,12 +297,31 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
             C = __builtin_fmaf(f, C, ss[i * slots + tid]);
             A *= f;
         }
-        if (MODE == kScanBack && !tile.first && !tile.last)
-            leave_pair(static_cast<uint64_t*>(a.words) + word + tid, composed(A), C);
     }
-    if (MODE == kScanBack && !tile.first)
-        s0 = look_back<scan_window(BACK)>(static_cast<const uint64_t*>(a.words) + word,
-                                          BACK ? int64_t(slots) : -int64_t(slots), tile.before, slots);
+    uint64_t* known_at = nullptr;   // kScanBack: where the state carried out goes, if anywhere
+    if (MODE == kScanBack) {
+        uint64_t* words = static_cast<uint64_t*>(a.words) + word;
+        const uint32_t group = tile.before / a.span, place = tile.before % a.span;
+        if (tid < slots && !tile.first && !tile.last) leave_pair(words + tid, composed(A), C);
+        if (tile.first && !tile.last) known_at = words;
+        // the groups' words by their place on the way of the state, from the group before on
+        uint64_t* groups =
+            static_cast<uint64_t*>(a.group_words) + (uint64_t(tile.chain) * a.spans + (group ? group - 1 : 0)) * slots;
+        LookBack near(words, BACK ? int64_t(slots) : -int64_t(slots), group < 2 ? tile.before : place + a.span, slots);
+        LookBack far(groups, -int64_t(slots),
+                     group < 2 ? 0 : group <= a.most ? group - 1 : (group - 1) % a.most + 1, slots);
+        __shared__ float la[2][kScanThreads], ls[2][kScanThreads];
+        float ga, gs, none;
+        near.join(slots, la[0], ls[0], ga, gs);
+        const bool leaves = group > 0 && place == 0 && tid < slots, known = group == 1 || group % a.most == 0;
+        if (leaves && !known) leave_pair(groups + tid, composed(ga), gs);
+        s0 = gs;
+        if (group > 1) {
+            far.join(slots, la[1], ls[1], none, s0);
+            s0 = __builtin_fmaf(ga, s0, gs);
+        }
+        if (leaves && known) leave_pair(groups + tid, kScanKnown, s0);
+    }
     if (tid < slots) {
         const uint32_t sc = min(tile.slot0 + tid / VW * VW, a.channels - VW) + tid % VW;   // the slot's channel
         const uint64_t state = uint64_t(b) * a.channels + sc;
@@ -301,7 +333,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
         }
         const float out = __builtin_fmaf(A, s0, C);
         if (MODE == kScanChain && !tile.last) leave_state(static_cast<uint32_t*>(a.words) + word + tid, out);
-        if (MODE == kScanBack && !tile.last) leave_pair(static_cast<uint64_t*>(a.words) + word + tid, kScanKnown, out);
+        if (MODE == kScanBack && known_at) leave_pair(known_at + tid, kScanKnown, out);
         if (tile.last && a.last) a.last[state] = out;
         // the state each sub-chunk starts from takes the place of its product
 #pragma unroll 8

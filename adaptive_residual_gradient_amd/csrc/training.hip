@@ -467,7 +467,7 @@ int adacomp_layer_norm_backward(const void* dy, uint64_t dy_stride, const void* 
 namespace {
 
 struct ScanLayout {
-    uint32_t lanes, groups, threads, steps, tiles;
+    uint32_t lanes, groups, threads, steps, tiles, span, spans, most;
     bool chain;
     uint64_t ws;
 };
@@ -502,8 +502,12 @@ ScanLayout scan_layout(const adacomp_scan_shape& s, uint32_t vw, bool back) {
     // At 64 chains and more the hop from tile to tile hides behind the other chains' tiles, and looking
     // further back only adds to the traffic.
     l.chain = chains >= 64;
-    // a word of every slot
-    if (l.tiles > 1) l.ws = kScanCountBytes + chains * l.tiles * l.lanes * vw * 8;
+    const uint32_t looks = l.threads / (l.lanes * vw);   // threads a slot; 4 and more where there are several tiles
+    l.span = std::max(looks * kScanWindow / 2, 1u);
+    l.most = looks * kScanWindow;
+    l.spans = (l.tiles + l.span - 1) / l.span;
+    // a word of every slot of a tile, and of a group of tiles
+    if (l.tiles > 1) l.ws = kScanCountBytes + chains * (l.tiles + l.spans) * l.lanes * vw * 8;
     return l;
 }
 // Channels of one thread: 4 bytes.
@@ -623,9 +627,11 @@ int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t
         hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanAlone, ACCESS>), dim3(uint32_t(n)), block, 0, s, a);
         return launch_status();
     }
-    const uint64_t vecs = (kScanCountBytes + n * l.lanes * VW * (l.chain ? 4 : 8) + 15) / 16;
+    const uint64_t slots = l.lanes * VW, words = l.chain ? n * slots * 4 : (n + chains * l.spans) * slots * 8;
+    const uint64_t vecs = (kScanCountBytes + words + 15) / 16;
     a.tickets = static_cast<uint32_t*>(ws);
     a.words = a.tickets + kScanCountBytes / 4;
+    a.group_words = static_cast<uint64_t*>(a.words) + n * slots;
     a.queues = static_cast<uint32_t>(std::min<uint64_t>(chains, kScanQueues));
     hipLaunchKernelGGL(k_scan_clear, dim3(uint32_t((vecs + 255) / 256)), dim3(256), 0, s, static_cast<uint4*>(ws),
                        vecs);
@@ -671,6 +677,9 @@ int run_scan(const ScanCall& c, adacomp::ScanArgs& a, bool back, void* stream) {
     a.groups = l.groups;
     a.tiles = l.tiles;
     a.steps = l.steps;
+    a.span = l.span;
+    a.spans = l.spans;
+    a.most = l.most;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const bool sig = s.sigmoid != 0;
     if (s.type == ADACOMP_FLOAT) return launch_scan_as<float, 1>(a, sig, back, l, c.ws, hs);

@@ -57,3 +57,36 @@ def test_decay_and_step_size_are_rounded_once(packed):
         step(opt, w, zero, m, v, **p)
         size = (lr / (1.0 - R.f32(0.9) ** 3)).astype(np.float32)
         assert np.array_equal(w.cpu().numpy(), -np.repeat(size, 4) * m.cpu().numpy())
+
+
+# ---- gated scan ----
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_long_chains_give_the_same_bits(dtype):
+    """Few long chains of tiles, many times: with other work beside them, and a sequence by itself."""
+    B, T, D = 2, 20000, 130
+    c = Case(B, T, D, dtype, True, seed=10)
+    c.z.add_(8.0)      # gates so close to 1 that a state reaches across many tiles
+    keys = ("h", "last", "dz", "dx", "dh0")
+    c.forward()
+    c.backward()
+    first = {k: getattr(c, k).clone() for k in keys}
+    side, room = torch.cuda.Stream(), torch.empty(1 << 28, device=DEV)
+    for i in range(30):
+        if i % 2:
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                room.add_(1.0)
+        c.forward()
+        c.backward()
+        torch.cuda.synchronize()
+        for k in keys:
+            assert torch.equal(getattr(c, k), first[k]), (i, k)
+    for b in range(B):
+        one = Case(1, T, D, dtype, True)
+        for k in ("z", "x", "dh", "h0", "dl"):
+            setattr(one, k, getattr(c, k)[b:b + 1].contiguous())
+        one.forward()
+        one.backward()
+        for k in keys:
+            assert torch.equal(getattr(one, k), first[k][b:b + 1]), (b, k)
