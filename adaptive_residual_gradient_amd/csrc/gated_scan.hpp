@@ -96,6 +96,17 @@ __device__ __forceinline__ void gates(float z, float& a, float& k) {
     k = e * a;
 }
 
+// Product of two gate products.  Of gates that are not 0 it never becomes 0, so that an infinite state
+// stays infinite under them (0 times infinity is NaN); to any other state the smallest number adds no more
+// than that product's own rounding may.  With the sigmoid no gate is 0 or below.
+template <bool SIG>
+__device__ __forceinline__ float gate_product(float p, float f) {
+    const float least = __uint_as_float(1u), q = p * f;
+    if (SIG) return __builtin_elementwise_maximum(q, least);
+    const float size = __builtin_elementwise_minimum(__builtin_elementwise_minimum(fabsf(p), fabsf(f)), least);
+    return copysignf(__builtin_elementwise_maximum(fabsf(q), size), q);
+}
+
 __device__ __forceinline__ uint64_t scan_steps(const ScanArgs& a, uint32_t b) {
     if (a.lengths == nullptr) return a.length;
     const int32_t n = a.lengths[b];
@@ -147,6 +158,7 @@ __device__ __forceinline__ uint32_t composed(float a) {
 // The n words (at most subs * WINDOW) before a place, word `d` of which (1 the nearest) is at
 // base + d * stride.  All threads look: the subs of a slot take WINDOW words each, nearest first, and
 // join their maps through LDS.
+template <bool SIG>
 struct LookBack {
     static constexpr uint32_t WINDOW = kScanWindow;
     const uint64_t* base;
@@ -188,7 +200,7 @@ struct LookBack {
         for (uint32_t u = 0; u < WINDOW; ++u) {
             if (d0 + u > n) continue;
             s = __builtin_fmaf(a, __uint_as_float(uint32_t(w[u])), s);
-            a *= __uint_as_float(uint32_t(w[u] >> 32));
+            a = gate_product<SIG>(a, __uint_as_float(uint32_t(w[u] >> 32)));
         }
         la[tid] = a;
         ls[tid] = s;
@@ -196,7 +208,7 @@ struct LookBack {
         if (tid >= slots) return;
         for (uint32_t j = 0; j < (n + WINDOW - 1) / WINDOW; ++j) {
             S = __builtin_fmaf(A, ls[j * slots + tid], S);
-            A *= la[j * slots + tid];
+            A = gate_product<SIG>(A, la[j * slots + tid]);
         }
     }
 };
@@ -275,7 +287,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
             gates<T, SIG>(z[v], f, m);
             f = on ? f : 1.f;
             S[v] = BACK ? f * ((on ? x[v] : 0.f) + S[v]) : __builtin_fmaf(f, S[v], on ? m * x[v] : 0.f);
-            P[v] *= f;
+            P[v] = gate_product<SIG>(P[v], f);
         }
         if (!BACK) {
             sv[u] = S;
@@ -295,7 +307,7 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
         for (uint32_t i = 0; i < G; ++i) {
             const float f = sa[i * slots + tid];
             C = __builtin_fmaf(f, C, ss[i * slots + tid]);
-            A *= f;
+            A = gate_product<SIG>(A, f);
         }
     }
     uint64_t* known_at = nullptr;   // kScanBack: where the state carried out goes, if anywhere
@@ -307,8 +319,8 @@ __device__ __forceinline__ void scan_tile(const ScanArgs& a, const ScanTile& til
         // the groups' words by their place on the way of the state, from the group before on
         uint64_t* groups =
             static_cast<uint64_t*>(a.group_words) + (uint64_t(tile.chain) * a.spans + (group ? group - 1 : 0)) * slots;
-        LookBack near(words, BACK ? int64_t(slots) : -int64_t(slots), group < 2 ? tile.before : place + a.span, slots);
-        LookBack far(groups, -int64_t(slots),
+        LookBack<SIG> near(words, BACK ? int64_t(slots) : -int64_t(slots), group < 2 ? tile.before : place + a.span, slots);
+        LookBack<SIG> far(groups, -int64_t(slots),
                      group < 2 ? 0 : group <= a.most ? group - 1 : (group - 1) % a.most + 1, slots);
         __shared__ float la[2][kScanThreads], ls[2][kScanThreads];
         float ga, gs, none;

@@ -477,7 +477,9 @@ int adacomp_layer_norm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t* b
  *   sigmoid = 0:  a = gate,  k = 1
  * states in float32.  The sequence is cut into tiles whose gate products are
  * formed and joined, so with sigmoid = 0 the products of consecutive gates,
- * however many, have to stay within float32's range (gates in [-1, 1] always do). */
+ * however many, have to stay below float32's largest number (gates in [-1, 1]
+ * always do).  Products below its normal numbers keep an absolute error of
+ * 2^-149, and are 0 only where a gate is. */
 typedef struct adacomp_scan_shape {
     uint64_t length;      /* steps, n_b <= length; may be 0 */
     uint32_t batch;       /* sequences; may be 0 */

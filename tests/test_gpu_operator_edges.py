@@ -61,6 +61,49 @@ def test_decay_and_step_size_are_rounded_once(packed):
 
 # ---- gated scan ----
 
+def check_any(got, want, bound, what):
+    """Finite values within their bound; infinities and NaN in the same places."""
+    got = R.f64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(want)), what
+    far = np.isinf(want)
+    assert np.array_equal(got[far], want[far]) and not np.isinf(got[~far]).any(), what
+    fine = np.isfinite(want)
+    R.assert_within(got[fine], want[fine], bound[fine], what)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,T,D", [(2, 15, 40),      # one thread a channel
+                                   (2, 120, 40),     # one tile
+                                   (3, 3000, 40),    # few chains of tiles
+                                   (70, 900, 20)])   # many
+@np.errstate(invalid="ignore", over="ignore")
+def test_infinite_states_stay(B, T, D, dtype, sigmoid):
+    """A carried infinity stays one under gates whose products are far below the smallest number, and
+    turns to NaN at a gate of 0; neighbouring channels stay finite."""
+    c = Case(B, T, D, dtype, sigmoid, seed=8)
+    if sigmoid:
+        c.z.fill_(-0.4)
+    else:
+        c.z.fill_(0.4)
+        c.z[:, :, 1::5] *= -1
+        c.z[:, T // 2, 2::5] = 0
+    c.h0[:, :D // 2], c.h0[:, D // 4:D // 2] = float("inf"), float("-inf")
+    (h, e), (last, el) = R.scan_forward(R.f64(c.z), R.f64(c.x), R.f64(c.h0), c.n, sigmoid, dtype)
+    c.forward()
+    check_any(c.h, h, R.rounded(h, e, dtype), "h")
+    check_any(c.last, last, R.rounded(last, el, torch.float32), "h_last")
+    c.h0 = torch.randn(B, D, device=DEV)
+    c.forward()
+    c.dl[:, :D // 2], c.dl[:, D // 4:D // 2] = float("inf"), float("-inf")
+    want = R.scan_backward(R.f64(c.z), R.f64(c.x), R.f64(c.h), R.f64(c.dh), R.f64(c.h0), R.f64(c.dl), c.n, sigmoid,
+                           dtype)
+    c.backward()
+    for got, (v, err), what, dt in ((c.dz, want[0], "dgate", dtype), (c.dx, want[1], "dx", dtype),
+                                    (c.dh0, want[2], "dh0", torch.float32)):
+        check_any(got, v, R.rounded(v, err, dt), what)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_long_chains_give_the_same_bits(dtype):
     """Few long chains of tiles, many times: with other work beside them, and a sequence by itself."""
