@@ -69,9 +69,10 @@ struct ScanArgs {
     uint32_t span, spans, most;                     // kScanBack: tiles a group, groups a chain, groups looked at
 };
 
-// Factors on the state and on the input.  With e = exp(-z), a = 1 / (1 + e)
-// and k = e a keep their relative accuracy far from 0; z is held from below
-// (NaN stays NaN) where e would overflow: a is below 2e-35 there.
+// Factors on the state and on the input, each within 8 roundings of float32 whatever the type: the states
+// that they form are float32.  With e = exp(-z), a = 1 / (1 + e) and k = e a keep their relative accuracy
+// far from 0.  z is held (NaN stays NaN) from below where e would overflow: a stays at 1.6e-38 from there
+// on; and from above where e is 0.
 template <typename T, bool SIG>
 __device__ __forceinline__ void gates(float z, float& a, float& k) {
     if (!SIG) {
@@ -79,19 +80,16 @@ __device__ __forceinline__ void gates(float z, float& a, float& k) {
         k = 1.f;
         return;
     }
-    constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718f;
-    z = __builtin_elementwise_maximum(z, -80.f);
-    if (sizeof(T) == 4) z = __builtin_elementwise_minimum(z, 100.f);   // e is 0 from there on
+    constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;   // ln 2 = the sum of both
+    z = __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -87.f), 100.f);
     const float p = z * -kLog2e;
     float e = __builtin_amdgcn_exp2f(p);
-    if (sizeof(T) == 4) {
-        // the product's rounding, which the exponential turns into a relative error; 16-bit types do
-        // without (it is at most 2^-18 where |z| < 64)
-        const float r = __builtin_fmaf(z, -kLog2e, -p) + z * -kLog2eLow;
-        e = __builtin_fmaf(e * kLn2, r, e);
-    }
+    // what the rounding of p leaves out, -z - p ln 2: without it e would be off by 2^-24 |z|
+    e = __builtin_fmaf(e, __builtin_fmaf(p, -kLn2Low, __builtin_fmaf(p, -kLn2, -z)), e);
     const float d = 1.f + e;
     a = __builtin_amdgcn_rcpf(d);
+    // the hardware's reciprocal is off by one unit in the last place, which float32 calls take out too
+    // (8 x 4096 x 2048 bf16 85.6 us with it, 84.6 without)
     if (sizeof(T) == 4) a = __builtin_fmaf(a, __builtin_fmaf(-d, a, 1.f), a);
     k = e * a;
 }

@@ -475,7 +475,8 @@ int adacomp_layer_norm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t* b
  *   h_t = a_t * h_(t-1) + k_t * x_t,   t = 0 .. n_b - 1
  *   sigmoid = 1:  a = 1 / (1 + exp(-gate)),  k = 1 / (1 + exp(gate))  (= 1 - a)
  *   sigmoid = 0:  a = gate,  k = 1
- * states in float32.  The sequence is cut into tiles whose gate products are
+ * states in float32, and a and k within 8 of its half units in the last place
+ * (a no smaller than 1.6e-38, whatever the gate).  The sequence is cut into tiles whose gate products are
  * formed and joined, so with sigmoid = 0 the products of consecutive gates,
  * however many, have to stay below float32's largest number (gates in [-1, 1]
  * always do).  Products below its normal numbers keep an absolute error of

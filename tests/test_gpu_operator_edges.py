@@ -104,6 +104,36 @@ def test_infinite_states_stay(B, T, D, dtype, sigmoid):
         check_any(got, v, R.rounded(v, err, dt), what)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [1, 40])
+def test_gate_factors_of_16_bit_types(T, dtype):
+    """The states of 16-bit calls are float32: gates of any size give them as many right bits as float32
+    gates do."""
+    B, D = 3, 1500
+    c = Case(B, T, D, dtype, True, seed=9)
+    c.z.copy_(torch.linspace(-30, 60, D, device=DEV).expand(B, T, D))
+    for h0 in (torch.zeros_like(c.h0), c.h0):
+        c.h0 = h0
+        c.forward()
+        _, (last, el) = R.scan_forward(R.f64(c.z), R.f64(c.x), R.f64(h0), c.n, True, torch.float32)
+        R.assert_within(c.last, last, R.rounded(last, el, torch.float32), "h_last")
+        c.backward()
+        want = R.scan_backward(R.f64(c.z), R.f64(c.x), R.f64(c.h), R.f64(c.dh), R.f64(h0), R.f64(c.dl), c.n, True,
+                               torch.float32)
+        R.assert_within(c.dh0, want[2][0], R.rounded(want[2][0], want[2][1], torch.float32), "dh0")
+
+
+def test_factors_of_far_float32_gates():
+    """Either factor keeps its bits down to float32's smallest normal numbers."""
+    D = 4000
+    z = torch.linspace(-86.9, 86.9, D, device=DEV).view(1, 1, D)
+    one, zero, last = torch.ones(1, D, device=DEV), torch.zeros(1, D, device=DEV), torch.empty(1, D, device=DEV)
+    h = torch.empty_like(z)
+    for x, h0, want in ((zero, one, 1 / (1 + np.exp(-R.f64(z)))), (one, zero, 1 / (1 + np.exp(R.f64(z))))):
+        A.gated_scan(z, x.view(1, 1, D), h, h0=h0, h_last=last)
+        R.assert_within(last, want[0], R.rounded(want[0], 10 * R.U * want[0], torch.float32), "factor")
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_long_chains_give_the_same_bits(dtype):
     """Few long chains of tiles, many times: with other work beside them, and a sequence by itself."""
