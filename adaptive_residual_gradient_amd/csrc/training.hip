@@ -13,12 +13,15 @@
 #include "host_checks.hpp"
 #include "layer_norm.hpp"
 #include "optimizer_layout.hpp"
+#include "views.hpp"
 
 using adacomp::aligned16;
 using adacomp::launch_status;
 using adacomp::overlaps;
 using adacomp::Range;
 using adacomp::range_of;
+using adacomp::view_range;
+using adacomp::views_clash;
 
 struct adacomp_optimizer {
     adacomp_optimizer_info info{};
@@ -530,28 +533,6 @@ int check_view(const adacomp_view* v, const adacomp_scan_shape& s) {
     return ADACOMP_OK;
 }
 
-Range view_range(const adacomp_view& v, const adacomp_scan_shape& s) {
-    return range_of(v.data, type_size(s.type) * ((s.batch - 1) * v.batch_stride + (s.length - 1) * v.time_stride +
-                                                 s.channels));
-}
-
-// Whether two views share an element.  Views side by side in the same rows
-// (parts of one projection) do not, though their ranges cross.
-bool views_clash(const adacomp_view& a, const adacomp_view& b, const adacomp_scan_shape& s) {
-    if (!overlaps(view_range(a, s), view_range(b, s))) return false;
-    const uint64_t size = type_size(s.type), ts = a.time_stride;
-    if (b.time_stride != ts || a.batch_stride != b.batch_stride || a.batch_stride % ts != 0) return true;
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.data), pb = reinterpret_cast<uintptr_t>(b.data);
-    const uint64_t d = (pa > pb ? pa - pb : pb - pa) / size % ts;
-    return d < s.channels || d > ts - s.channels;
-}
-
-// An output view's rows may not meet: steps of one sequence, or two sequences.
-bool view_folds(const adacomp_view& v, const adacomp_scan_shape& s) {
-    return s.batch > 1 && s.length > 0 && v.batch_stride < (s.length - 1) * v.time_stride + s.channels &&
-           !(v.time_stride >= (s.batch - 1) * v.batch_stride + s.channels && v.batch_stride >= s.channels);
-}
-
 adacomp::ScanView dev_view(const adacomp_view* v) {
     return v ? adacomp::ScanView{v->data, v->batch_stride, v->time_stride} : adacomp::ScanView{};
 }
@@ -577,7 +558,8 @@ int check_scan(const ScanCall& c) {
         if ((st = check_view(c.in[i], s)) != ADACOMP_OK) return st;
     for (int i = 0; i < c.nout && steps; ++i) {
         if ((st = check_view(c.out[i], s)) != ADACOMP_OK) return st;
-        if (view_folds(*c.out[i], s)) return ADACOMP_ERR_INVALID_ARGUMENT;
+        adacomp::RowGrid rows;   // an output's rows may not meet
+        if (!adacomp::row_grid(*c.out[i], s, rows)) return ADACOMP_ERR_INVALID_ARGUMENT;
     }
     if (!aligned_to(c.states_in[0], 4) || !aligned_to(c.states_in[1], 4) || !aligned_to(c.state_out, 4) ||
         !aligned_to(c.lengths, 4) || !aligned16(c.ws))
@@ -585,12 +567,12 @@ int check_scan(const ScanCall& c) {
     const uint64_t need = scan_workspace(s);
     if (need > 0 && c.ws == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
     if (c.ws_bytes < need) return ADACOMP_ERR_CAPACITY;
-    const uint64_t state = 4 * uint64_t(s.batch) * s.channels;
+    const uint64_t state = 4 * uint64_t(s.batch) * s.channels, size = type_size(s.type);
     Range r[11] = {range_of(c.state_out, c.state_out ? state : 0), range_of(c.ws, need)};
     int n = 2;
-    for (int i = 0; i < c.nout && steps; ++i) r[n++] = view_range(*c.out[i], s);
+    for (int i = 0; i < c.nout && steps; ++i) r[n++] = view_range(*c.out[i], s, size);
     const int nout = n, nview = steps ? n + c.nin : n;
-    for (int i = 0; i < c.nin && steps; ++i) r[n++] = view_range(*c.in[i], s);
+    for (int i = 0; i < c.nin && steps; ++i) r[n++] = view_range(*c.in[i], s, size);
     for (int i = 0; i < 2; ++i) r[n++] = range_of(c.states_in[i], c.states_in[i] ? state : 0);
     r[n++] = range_of(c.lengths, c.lengths ? 4 * uint64_t(s.batch) : 0);
     for (int i = 0; i < nout; ++i)
@@ -598,7 +580,7 @@ int check_scan(const ScanCall& c) {
             if (!overlaps(r[i], r[j])) continue;
             if (i >= 2 && j < nview) {   // two views
                 const adacomp_view* b = j < nout ? c.out[j - 2] : c.in[j - nout];
-                if (!views_clash(*c.out[i - 2], *b, s)) continue;
+                if (!views_clash(*c.out[i - 2], *b, s, size)) continue;
             }
             return ADACOMP_ERR_INVALID_ARGUMENT;
         }

@@ -163,3 +163,42 @@ def test_long_chains_give_the_same_bits(dtype):
         one.backward()
         for k in keys:
             assert torch.equal(getattr(one, k), first[k][b:b + 1]), (b, k)
+
+
+@pytest.mark.parametrize("B,T", [(4, 1), (3, 2), (1, 1), (1, 300), (5, 40)])
+@pytest.mark.parametrize("time_first", [False, True])
+def test_halves_of_one_projection(B, T, time_first):
+    """gate and input, and their gradients, as halves of one buffer, for one step and with time first in memory."""
+    D = 64
+    c = Case(B, T, D, torch.bfloat16, True)
+    c.forward()
+    c.backward()
+    size = (T, B, 2 * D) if time_first else (B, T, 2 * D)
+    both, grads = (torch.full(size, 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    if time_first:
+        both, grads = both.transpose(0, 1), grads.transpose(0, 1)
+    both[:, :, :D], both[:, :, D:] = c.z, c.x
+    h, dh0 = torch.empty_like(c.h), torch.empty_like(c.dh0)
+    A.gated_scan(both[:, :, :D], both[:, :, D:], h, h0=c.h0, ws=c.ws)
+    A.gated_scan_backward(both[:, :, :D], both[:, :, D:], h, c.dh, grads[:, :, :D], grads[:, :, D:], h0=c.h0,
+                          dh_last=c.dl, dh0=dh0, ws=c.ws)
+    assert torch.equal(h, c.h) and torch.equal(dh0, c.dh0)
+    assert torch.equal(grads[:, :, :D], c.dz) and torch.equal(grads[:, :, D:], c.dx)
+    # the input's half of the buffer receives the states
+    out = both.clone(memory_format=torch.preserve_format)
+    x = c.x.clone()
+    A.gated_scan(out[:, :, :D], x, out[:, :, D:], h0=c.h0, ws=c.ws)
+    assert torch.equal(out[:, :, D:], c.h) and torch.equal(out[:, :, :D], c.z)
+    # halves that share a channel
+    with pytest.raises(A.AdaCompError):
+        A.gated_scan(out[:, :, :D], x, out[:, :, D - 1:2 * D - 1], h0=c.h0, ws=c.ws)
+
+
+def test_example_with_one_step():
+    """The example's layers on one token of several sequences."""
+    import pathlib
+    import sys
+    sys.path.insert(0, str(pathlib.Path(__file__).resolve().parent.parent / "examples"))
+    import train_gated_layers as E
+    losses = E.train(layers=1, width=64, batch=4, length=1, learners=2, steps=3, log=lambda s: None)
+    assert all(x == x for x in losses)
