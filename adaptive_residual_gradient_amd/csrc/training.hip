@@ -225,12 +225,14 @@ int check_rows(const void* p, uint64_t stride, uint64_t rows, uint32_t cols, int
     return ADACOMP_OK;
 }
 
-int check_norm_shape(uint64_t rows, uint32_t cols, int type) {
+// Rows that a workgroup each takes are as many as work-items of one launch fit in 32 bits; the kernels of
+// shorter rows step over them with a bounded grid.
+int check_norm_shape(uint64_t rows, uint32_t cols, int type, bool back) {
     if (type_size(type) == 0 || cols == 0) return ADACOMP_ERR_INVALID_ARGUMENT;
-    // work-items of one launch must fit in 32 bits
-    const uint64_t threads = cols > adacomp::kNormRegCols ? adacomp::kNormWideThreads
-                                                          : 64 * ((cols - 1) / adacomp::kNormWaveCols + 1);
-    if (cols > ADACOMP_NORM_MAX_COLS || rows >= ((uint64_t(1) << 32) - 1024) / threads) return ADACOMP_ERR_TOO_LARGE;
+    const bool wide = cols > (back ? adacomp::kNormBackRegCols : adacomp::kNormRegCols);
+    const uint64_t items = (uint64_t(1) << 32) - 1;
+    if (cols > ADACOMP_NORM_MAX_COLS || rows > (wide ? items / adacomp::kNormWideThreads : items))
+        return ADACOMP_ERR_TOO_LARGE;
     return ADACOMP_OK;
 }
 
@@ -273,9 +275,9 @@ template <typename T, int KEEP>
 void launch_norm(const adacomp::NormArgs& a, hipStream_t s) {
     using namespace adacomp;
     constexpr int VEC = norm_vec<T>(), NVMAX = kNormElems / VEC;
-    const uint32_t rows = uint32_t(a.rows);
+    const uint64_t rows = a.rows;
     if (a.cols > kNormRegCols) {
-        hipLaunchKernelGGL(k_layer_norm_wide<T>, dim3(rows), dim3(kNormWideThreads), 0, s, a);
+        hipLaunchKernelGGL(k_layer_norm_wide<T>, dim3(uint32_t(rows)), dim3(kNormWideThreads), 0, s, a);
     } else if (a.cols > kNormWaveCols) {
         const uint32_t waves = (a.cols + kNormWaveCols - 1) / kNormWaveCols;
         hipLaunchKernelGGL((k_layer_norm<T, VEC, NVMAX, 64, true, KEEP>), dim3(norm_blocks(rows, kNormMaxWaves / waves)),
@@ -295,10 +297,11 @@ template <typename T, int KEEP>
 uint32_t launch_norm_backward(const adacomp::NormArgs& a, hipStream_t s) {
     using namespace adacomp;
     constexpr int VEC = norm_vec<T>(), NVMAX = kNormElems / VEC;
-    const uint32_t rows = uint32_t(a.rows), most = norm_partials(a.rows);
+    const uint64_t rows = a.rows;
+    const uint32_t most = norm_partials(rows);
     if (a.cols > kNormBackRegCols) {
-        hipLaunchKernelGGL(k_layer_norm_backward_wide<T>, dim3(rows), dim3(kNormWideThreads), 0, s, a);
-        if (a.partial == nullptr) return 0;
+        hipLaunchKernelGGL(k_layer_norm_backward_wide<T>, dim3(uint32_t(rows)), dim3(kNormWideThreads), 0, s, a);
+        if (a.partial == nullptr || hipPeekAtLastError() != hipSuccess) return 0;   // the caller reports it
         const uint32_t n = std::min(most, 64u);
         hipLaunchKernelGGL(k_norm_partial_wide<T>, dim3((a.cols + 255) / 256, n), dim3(256), 0, s, a);
         return n;
@@ -358,7 +361,7 @@ extern "C" {
 int adacomp_layer_norm(const void* x, uint64_t x_stride, const float* weight, const float* bias, void* y,
                        uint64_t y_stride, float* mean, float* rstd, uint64_t rows, uint32_t cols, int type, float eps,
                        void* stream_) {
-    int st = check_norm_shape(rows, cols, type);
+    int st = check_norm_shape(rows, cols, type, false);
     if (st != ADACOMP_OK) return st;
     if (!(eps >= 0.f) || std::isinf(eps)) return ADACOMP_ERR_INVALID_ARGUMENT;
     if (rows == 0) return ADACOMP_OK;
@@ -396,7 +399,7 @@ int adacomp_layer_norm(const void* x, uint64_t x_stride, const float* weight, co
 
 int adacomp_layer_norm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t* bytes) {
     if (bytes == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
-    const int st = check_norm_shape(rows, cols, ADACOMP_FLOAT);
+    const int st = check_norm_shape(rows, cols, ADACOMP_FLOAT, true);
     if (st != ADACOMP_OK) return st;
     *bytes = uint64_t(norm_partials(rows)) * 2 * cols * 4;
     return ADACOMP_OK;
@@ -406,7 +409,7 @@ int adacomp_layer_norm_backward(const void* dy, uint64_t dy_stride, const void* 
                                 const float* weight, const float* mean, const float* rstd, void* dx,
                                 uint64_t dx_stride, float* dweight, float* dbias, uint64_t rows, uint32_t cols,
                                 int type, void* ws, uint64_t ws_bytes, void* stream_) {
-    int st = check_norm_shape(rows, cols, type);
+    int st = check_norm_shape(rows, cols, type, true);
     if (st != ADACOMP_OK) return st;
     const bool sums = dweight != nullptr;
     if ((dbias != nullptr) != sums) return ADACOMP_ERR_INVALID_ARGUMENT;

@@ -448,7 +448,9 @@ int adacomp_adamw_packed_step(const adacomp_optimizer* optimizer, float* weights
  *                 aligned to their element.
  *   weight, bias  nullable [cols] float32 (absent: 1, 0).
  *   mean, rstd    nullable [rows] float32 outputs, as the backward pass takes them.
- * rows = 0 is no work; cols from 1 to ADACOMP_NORM_MAX_COLS, else ERR_TOO_LARGE. */
+ * rows = 0 is no work.  ERR_TOO_LARGE for more than ADACOMP_NORM_MAX_COLS
+ * columns, 2^32 rows and more, 2^22 rows and more of over 16384 columns, or a
+ * matrix that reaches past 2^40 elements. */
 #define ADACOMP_NORM_MAX_COLS 65536u
 int adacomp_layer_norm(const void* x, uint64_t x_stride, const float* weight, const float* bias,
                        void* y, uint64_t y_stride, float* mean, float* rstd, uint64_t rows,
@@ -463,7 +465,8 @@ int adacomp_layer_norm(const void* x, uint64_t x_stride, const float* weight, co
  *                   with rows = 0 they become zero.
  *   ws              16-byte aligned, ws_bytes >= adacomp_layer_norm_workspace_bytes(rows,
  *                   cols); not used, and may be NULL, without dweight and dbias.  No
- *                   initial contents required. */
+ *                   initial contents required.
+ * ERR_TOO_LARGE as above, but from over 8192 columns on for 2^22 rows. */
 int adacomp_layer_norm_backward(const void* dy, uint64_t dy_stride, const void* x,
                                 uint64_t x_stride, const float* weight, const float* mean,
                                 const float* rstd, void* dx, uint64_t dx_stride, float* dweight,

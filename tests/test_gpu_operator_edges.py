@@ -202,3 +202,37 @@ def test_example_with_one_step():
     import train_gated_layers as E
     losses = E.train(layers=1, width=64, batch=4, length=1, learners=2, steps=3, log=lambda s: None)
     assert all(x == x for x in losses)
+
+
+# ---- layer norm ----
+
+def test_layer_norm_of_more_rows_than_one_workgroup_each():
+    """67 million rows: as the two halves of them give, and the weight's sums within their bound."""
+    rows, cols, half = (1 << 26) + 77, 4, 1 << 25
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    new = lambda: torch.randn(rows, cols, generator=gen, device=DEV, dtype=torch.float16)
+    x, dy = new(), new()
+    w = 1 + 0.2 * torch.randn(cols, generator=gen, device=DEV)
+    y, y2 = torch.empty_like(x), torch.empty_like(x)
+    kept = [torch.empty(rows, device=DEV) for _ in range(4)]
+    parts = (slice(0, half), slice(half, rows))
+    A.layer_norm(x, w, None, y, *kept[:2])
+    for s in parts:
+        A.layer_norm(x[s], w, None, y2[s], *(k[s] for k in kept[2:]))
+    assert torch.equal(y, y2) and torch.equal(kept[0], kept[2]) and torch.equal(kept[1], kept[3])
+    dw, db = torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    A.layer_norm_backward(dy, x, w, *kept[:2], y, dw, db, A.layer_norm_workspace(rows, cols, DEV))
+    for s in parts:
+        A.layer_norm_backward(dy[s], x[s], w, *(k[s] for k in kept[:2]), y2[s])
+    assert torch.equal(y, y2)
+    want = [torch.zeros(cols, dtype=torch.float64, device=DEV) for _ in range(4)]
+    for i in range(0, rows, 1 << 23):
+        s = slice(i, min(rows, i + (1 << 23)))
+        hat = (x[s].double() - kept[0][s, None].double()) * kept[1][s, None].double()
+        d = dy[s].double()
+        for t, v in zip(want, (d * hat, d, (d * hat).abs(), d.abs())):
+            t += v.sum(0)
+    # 256 workgroups of 64 teams: a team's rows one after the other, the teams, the partial rows
+    chain = rows / (256 * 64) + 64 + R.SUM
+    for got, value, size in ((dw, want[0], want[2]), (db, want[1], want[3])):
+        R.assert_within(got, R.f64(value), chain * R.U * R.f64(size), "weight's sums")
