@@ -605,11 +605,12 @@ template <typename T, int VW, bool SIG, bool BACK, int ACCESS>
 int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t s) {
     using namespace adacomp;
     const uint64_t chains = uint64_t(a.batch) * l.groups, n = chains * l.tiles;
-    // work-items of one launch must fit in 32 bits (the queues round the chains up)
-    if ((chains + kScanQueues) * l.tiles * l.threads >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;
+    a.queues = static_cast<uint32_t>(std::min<uint64_t>(chains, kScanQueues));
+    const uint64_t blocks = l.tiles == 1 ? n : (chains + a.queues - 1) / a.queues * a.queues * l.tiles;
+    if (blocks * l.threads >= (uint64_t(1) << 32)) return ADACOMP_ERR_TOO_LARGE;   // work-items of one launch
     const dim3 block(l.threads);
     if (l.tiles == 1) {
-        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanAlone, ACCESS>), dim3(uint32_t(n)), block, 0, s, a);
+        hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanAlone, ACCESS>), dim3(uint32_t(blocks)), block, 0, s, a);
         return launch_status();
     }
     const uint64_t slots = l.lanes * VW, words = l.chain ? n * slots * 4 : (n + chains * l.spans) * slots * 8;
@@ -617,11 +618,10 @@ int launch_scan(adacomp::ScanArgs& a, const ScanLayout& l, void* ws, hipStream_t
     a.tickets = static_cast<uint32_t*>(ws);
     a.words = a.tickets + kScanCountBytes / 4;
     a.group_words = static_cast<uint64_t*>(a.words) + n * slots;
-    a.queues = static_cast<uint32_t>(std::min<uint64_t>(chains, kScanQueues));
     hipLaunchKernelGGL(k_scan_clear, dim3(uint32_t((vecs + 255) / 256)), dim3(256), 0, s, static_cast<uint4*>(ws),
                        vecs);
     if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-    const dim3 grid(uint32_t((chains + a.queues - 1) / a.queues * a.queues * l.tiles));
+    const dim3 grid(static_cast<uint32_t>(blocks));
     if (l.chain) hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanChain, ACCESS>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_scan_tile<T, VW, SIG, BACK, kScanBack, ACCESS>), grid, block, 0, s, a);
     return launch_status();

@@ -483,7 +483,11 @@ int adacomp_layer_norm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t* b
  * formed and joined, so with sigmoid = 0 the products of consecutive gates,
  * however many, have to stay below float32's largest number (gates in [-1, 1]
  * always do).  Products below its normal numbers keep an absolute error of
- * 2^-149, and are 0 only where a gate is. */
+ * 2^-149, and are 0 only where a gate is.
+ * ERR_TOO_LARGE: length or batch * channels from 2^31 on, batch or channels
+ * from 2^24 on, strides past 2^32 (time) or 2^40 (batch), or more work-items than a launch has,
+ * 2^32: one for each 8 steps (backward with the sigmoid) or 16 of 4 bytes of
+ * adjacent channels, whole tiles counted. */
 typedef struct adacomp_scan_shape {
     uint64_t length;      /* steps, n_b <= length; may be 0 */
     uint32_t batch;       /* sequences; may be 0 */

@@ -165,6 +165,23 @@ def test_long_chains_give_the_same_bits(dtype):
             assert torch.equal(getattr(one, k), first[k][b:b + 1]), (b, k)
 
 
+def test_one_sequence_of_millions_of_steps():
+    """The two parts of one very long sequence, the state handed over, give what the whole does."""
+    B, T, D, cut = 1, 16_600_000, 64, 8_000_000
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    z, x = (torch.randn(B, T, D, generator=gen, device=DEV) for _ in range(2))
+    h, part = torch.empty_like(z), torch.empty_like(z)
+    last, state = torch.empty(B, D, device=DEV), torch.empty(B, D, device=DEV)
+    ws = A.gated_scan_workspace(B, T, D, DEV)
+    A.gated_scan(z, x, h, h_last=last, ws=ws)
+    A.gated_scan(z[:, :cut], x[:, :cut], part[:, :cut], h_last=state, ws=ws)
+    tail = torch.empty_like(state)
+    A.gated_scan(z[:, cut:], x[:, cut:], part[:, cut:], h0=state, h_last=tail, ws=ws)
+    # a state is a mean of inputs of about 1 over the few steps that its gates reach back, with 10 roundings a step
+    bound = 10 * 64 * R.U * float(x.abs().max())
+    assert float((h - part).abs().max()) <= bound and float((last - tail).abs().max()) <= bound
+
+
 @pytest.mark.parametrize("B,T", [(4, 1), (3, 2), (1, 1), (1, 300), (5, 40)])
 @pytest.mark.parametrize("time_first", [False, True])
 def test_halves_of_one_projection(B, T, time_first):
