@@ -190,7 +190,7 @@ int adamw(PyObject* const* a) {
                               clip, stream);
 }
 
-// A tensor whose last axis is adjacent and whose other axes have one stride between them.
+// A tensor whose columns are adjacent and whose rows, over all leading axes, lie at one distance.
 struct Rows {
     void* p;
     uint64_t stride, rows;
@@ -203,10 +203,22 @@ struct Rows {
         // more columns than 32 bits hold are more than the C ABI takes, in any number
         cols = uint32_t(std::min<int64_t>(n, 0xFFFFFFFF));
         rows = n ? uint64_t(t.numel() / n) : 0;
-        const bool adjacent = n == 1 || t.stride(-1) == 1;
-        if (t.is_contiguous() || (rows <= 1 && adjacent)) stride = uint64_t(n);
-        else if (t.dim() == 2 && adjacent) stride = uint64_t(t.stride(0));
-        else throw WrongType(std::string(name) + " must be contiguous, or a matrix with adjacent columns");
+        if (t.is_contiguous()) {
+            stride = uint64_t(n);
+        } else {
+            // the leading axes of more than one place, innermost first: each has to go on where the one
+            // inside it ends
+            bool one = n == 1 || t.stride(-1) == 1;
+            int64_t step = -1, next = 0;
+            for (int64_t i = t.dim() - 2; i >= 0 && one; --i) {
+                if (t.size(i) == 1) continue;
+                if (step < 0) step = t.stride(i);
+                else one = t.stride(i) == next;
+                next = t.stride(i) * t.size(i);
+            }
+            if (!one) throw WrongType(std::string(name) + " must have adjacent columns and one distance between its rows");
+            stride = uint64_t(rows > 1 ? step : n);
+        }
         p = address(t);
     }
     Rows(const at::Tensor& t, const char* name, const at::Tensor& like) : Rows(t, name) {

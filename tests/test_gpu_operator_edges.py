@@ -223,6 +223,37 @@ def test_example_with_one_step():
 
 # ---- layer norm ----
 
+def test_layer_norm_of_parts_of_wider_rows():
+    """Any leading axes whose rows lie at one distance, and axes of one place wherever they lie."""
+    B, T, D = 3, 50, 96
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    both, grads = (torch.randn(B, T, 2 * D, generator=gen, device=DEV) for _ in range(2))
+    x, dy = both[:, :, :D], both[:, :, D:]
+    y, dx = grads[:, :, :D], grads[:, :, D:]
+    kept = [torch.empty(B * T, device=DEV) for _ in range(4)]
+    sums = [torch.empty(D, device=DEV) for _ in range(4)]
+    ws = A.layer_norm_workspace(B * T, D, DEV)
+    A.layer_norm(x, None, None, y, *kept[:2])
+    A.layer_norm_backward(dy, x, None, *kept[:2], dx, *sums[:2], ws)
+    x2, dy2 = x.contiguous(), dy.contiguous()
+    y2, dx2 = torch.empty_like(x2), torch.empty_like(x2)
+    A.layer_norm(x2, None, None, y2, *kept[2:])
+    A.layer_norm_backward(dy2, x2, None, *kept[2:], dx2, *sums[2:], ws)
+    assert torch.equal(y, y2) and torch.equal(dx, dx2) and torch.equal(sums[0], sums[2])
+    assert torch.equal(kept[0], kept[2]) and torch.equal(sums[1], sums[3])
+    last = both[:, -1:, :D]          # [B, 1, D]: one distance between its rows
+    A.layer_norm(last, None, None, y2[:, :1].contiguous())
+    out = torch.empty(B, 1, D, device=DEV)
+    A.layer_norm(last, None, None, out)
+    assert torch.equal(out[:, 0], y2[:, -1])
+    spread = torch.zeros(B, 1, D, device=DEV).expand(B, T, D)
+    for bad in (both[:, ::2, :D].transpose(0, 1), both[:2, :7, :D], both[:, :, ::2], spread, spread.transpose(0, 1)):
+        with pytest.raises(TypeError):
+            A.layer_norm(bad, None, None, torch.empty(bad.shape, device=DEV))
+    with pytest.raises(A.AdaCompError):      # one row for all of them
+        A.layer_norm(torch.zeros(D, device=DEV).expand(B, T, D), None, None, torch.empty(B, T, D, device=DEV))
+
+
 def test_layer_norm_of_more_rows_than_one_workgroup_each():
     """67 million rows: as the two halves of them give, and the weight's sums within their bound."""
     rows, cols, half = (1 << 26) + 77, 4, 1 << 25
