@@ -37,7 +37,25 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
     return THPVariable_Unpack(o);
 }
 
+// The current device, asked once a call: the C ABI launches there, on its stream, so every tensor has to
+// be there.
+thread_local int device = -1;
+int here() {
+    if (device >= 0) return device;
+    PyObject* o = PyObject_CallNoArgs(current_device);
+    if (o == nullptr) throw PythonError();
+    device = int(PyLong_AsLong(o));
+    Py_DECREF(o);
+    if (device < 0) throw PythonError();
+    return device;
+}
+// Of a CUDA tensor.
+void check_device(const at::Tensor& t, const char* name) {
+    if (t.device().index() != here()) throw WrongValue(std::string(name) + " must be on the current device");
+}
+
 int type_of(const at::Tensor& t, const char* name) {
+    if (t.is_cuda()) check_device(t, name);
     if (t.is_cuda()) switch (t.scalar_type()) {
         case at::kFloat: return ADACOMP_FLOAT;
         case at::kBFloat16: return ADACOMP_BFLOAT;
@@ -56,6 +74,7 @@ T* address(const at::Tensor& t) {
 void check(const at::Tensor& t, at::ScalarType type, const char* name) {
     if (t.scalar_type() != type || !t.is_cuda() || !t.is_contiguous())
         throw WrongType(std::string(name) + " must be a contiguous CUDA tensor of " + at::toString(type));
+    check_device(t, name);
 }
 
 // Address of a nullable contiguous tensor of n elements.
@@ -105,10 +124,10 @@ bool truth(PyObject* o) {
 void* stream_of(PyObject* o) {
     PyObject* handle = nullptr;
     if (o == Py_None) {
-        PyObject* device = PyObject_CallNoArgs(current_device);
-        if (device != nullptr) {
-            handle = PyObject_CallOneArg(current_stream, device);
-            Py_DECREF(device);
+        PyObject* index = PyLong_FromLong(here());
+        if (index != nullptr) {
+            handle = PyObject_CallOneArg(current_stream, index);
+            Py_DECREF(index);
         }
     } else {
         handle = PyObject_GetAttrString(o, "cuda_stream");
@@ -164,10 +183,12 @@ int adamw(PyObject* const* a) {
         if (s.numel() < 2 * nblocks) throw WrongValue("scales shorter than the optimizer's blocks");
         check(s, at::kByte, "scales");
         scales = address(s);
-        for (const at::Tensor* t : {&m, &v})
+        for (const at::Tensor* t : {&m, &v}) {
             if ((t->scalar_type() != at::kByte && t->scalar_type() != at::kFloat8_e4m3fn) || !t->is_cuda() ||
                 !t->is_contiguous())
                 throw WrongType("m and v must be contiguous float8_e4m3fn or uint8 CUDA tensors");
+            check_device(*t, "m and v");
+        }
     } else {
         check(m, at::kFloat, "m");
         check(v, at::kFloat, "v");
@@ -269,6 +290,7 @@ struct View : adacomp_view {
         const at::Tensor& t = tensor(o, name);
         if (!t.is_cuda() || t.scalar_type() != gate.t.scalar_type() || t.sizes() != gate.t.sizes())
             throw WrongValue(std::string(name) + " must be a CUDA tensor of the gate's shape and type");
+        check_device(t, name);
         const int64_t B = t.size(0), T = t.size(1), D = t.size(2);
         data = address(t);
         if (t.is_contiguous()) {
@@ -311,6 +333,7 @@ int gated_scan_backward(PyObject* const* a) {
 // No C++ exception leaves an entry point.
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
+    device = -1;
     try {
         if (n != want) throw WrongType("wrong number of arguments");
         return f();
