@@ -139,6 +139,16 @@ void* stream_of(PyObject* o) {
     return p;
 }
 
+// A C call without the interpreter's lock: other threads go on while a launch waits for room in a queue,
+// also a host function in that queue that needs the lock.
+template <typename F>
+int unlocked(F f) {
+    PyThreadState* state = PyEval_SaveThread();
+    const int status = f();   // the C ABI throws nothing
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 // The gradient of an optimizer call.
 struct Gradient {
     int type;
@@ -164,8 +174,11 @@ int grad_norm(PyObject* const* a) {
     const Gradient g(a[1]);
     float* clip = optional(a[2], 2, "clip");
     const Workspace ws(a[3]);
-    return adacomp_grad_norm(opt, g.p, g.type, uint64_t(g.n), real(a[4]), real(a[5]), clip, ws.p, ws.bytes,
-                             stream_of(a[6]));
+    const float max_norm = real(a[4]), scale = real(a[5]);
+    void* stream = stream_of(a[6]);
+    return unlocked([&] {
+        return adacomp_grad_norm(opt, g.p, g.type, uint64_t(g.n), max_norm, scale, clip, ws.p, ws.bytes, stream);
+    });
 }
 
 // optimizer, span, nblocks, weights, grad, m, v, scales (None: float32 moments), lr, beta1, beta2, eps, step, scale,
@@ -203,12 +216,13 @@ int adamw(PyObject* const* a) {
     }
     const adacomp_adamw p = {real(a[8]), real(a[9]), real(a[10]), real(a[11]), real(a[13]), whole32(a[12], "step")};
     const float* clip = optional(a[15], 2, "clip");
+    const uint32_t seed = whole32(a[14], "seed");
     void* stream = stream_of(a[17]);
-    if (packed)
-        return adacomp_adamw_packed_step(opt, address<float>(w), g.p, g.type, address(m), address(v), scales, copy, n, &p,
-                                         whole32(a[14], "seed"), clip, stream);
-    return adacomp_adamw_step(opt, address<float>(w), g.p, g.type, address<float>(m), address<float>(v), copy, n, &p,
-                              clip, stream);
+    float *wp = address<float>(w), *mp = address<float>(m), *vp = address<float>(v);
+    return unlocked([&] {
+        return packed ? adacomp_adamw_packed_step(opt, wp, g.p, g.type, mp, vp, scales, copy, n, &p, seed, clip, stream)
+                      : adacomp_adamw_step(opt, wp, g.p, g.type, mp, vp, copy, n, &p, clip, stream);
+    });
 }
 
 // A tensor whose columns are adjacent and whose rows, over all leading axes, lie at one distance.
@@ -253,9 +267,14 @@ int layer_norm(PyObject* const* a) {
     const at::Tensor& tx = tensor(a[0], "x");
     const Rows x(tx, "x"), y(tensor(a[3], "out"), "out", tx);
     const int64_t rows = int64_t(x.rows);
-    return adacomp_layer_norm(x.p, x.stride, optional(a[1], x.cols, "weight"), optional(a[2], x.cols, "bias"), y.p,
-                              y.stride, optional(a[4], rows, "mean"), optional(a[5], rows, "rstd"), x.rows, x.cols,
-                              x.type, real(a[6]), stream_of(a[7]));
+    const float *weight = optional(a[1], x.cols, "weight"), *bias = optional(a[2], x.cols, "bias");
+    float *mean = optional(a[4], rows, "mean"), *rstd = optional(a[5], rows, "rstd");
+    const float eps = real(a[6]);
+    void* stream = stream_of(a[7]);
+    return unlocked([&] {
+        return adacomp_layer_norm(x.p, x.stride, weight, bias, y.p, y.stride, mean, rstd, x.rows, x.cols, x.type, eps,
+                                  stream);
+    });
 }
 
 // dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream
@@ -264,10 +283,14 @@ int layer_norm_backward(PyObject* const* a) {
     const Rows dy(td, "dy"), x(tensor(a[1], "x"), "x", td), dx(tensor(a[5], "dx"), "dx", td);
     const int64_t rows = int64_t(dy.rows), cols = dy.cols;
     const Workspace ws(a[8]);
-    return adacomp_layer_norm_backward(dy.p, dy.stride, x.p, x.stride, optional(a[2], cols, "weight"),
-                                       optional(a[3], rows, "mean"), optional(a[4], rows, "rstd"), dx.p, dx.stride,
-                                       optional(a[6], cols, "dweight"), optional(a[7], cols, "dbias"), dy.rows, dy.cols,
-                                       dy.type, ws.p, ws.bytes, stream_of(a[9]));
+    const float *weight = optional(a[2], cols, "weight"), *mean = optional(a[3], rows, "mean"),
+                *rstd = optional(a[4], rows, "rstd");
+    float *dweight = optional(a[6], cols, "dweight"), *dbias = optional(a[7], cols, "dbias");
+    void* stream = stream_of(a[9]);
+    return unlocked([&] {
+        return adacomp_layer_norm_backward(dy.p, dy.stride, x.p, x.stride, weight, mean, rstd, dx.p, dx.stride, dweight,
+                                           dbias, dy.rows, dy.cols, dy.type, ws.p, ws.bytes, stream);
+    });
 }
 
 // The gate, whose shape and type the other tensors of a scan have.
@@ -313,9 +336,13 @@ int gated_scan(PyObject* const* a) {
     const Gate gate(a[0], truth(a[6]));
     const View z(a[0], gate, "gate"), x(a[1], gate, "x"), h(a[2], gate, "h");
     const Workspace ws(a[7]);
-    return adacomp_gated_scan(&gate.shape, &z, &x, &h, optional(a[3], gate.states, "h0"),
-                              optional(a[4], gate.states, "h_last"), lengths_of(a[5], gate), ws.p, ws.bytes,
-                              stream_of(a[8]));
+    const float* h0 = optional(a[3], gate.states, "h0");
+    float* last = optional(a[4], gate.states, "h_last");
+    const int32_t* lengths = lengths_of(a[5], gate);
+    void* stream = stream_of(a[8]);
+    return unlocked([&] {
+        return adacomp_gated_scan(&gate.shape, &z, &x, &h, h0, last, lengths, ws.p, ws.bytes, stream);
+    });
 }
 
 // gate, x (or None), h, dh, dgate, dx, h0, dh_last, dh0, lengths, sigmoid, ws, stream
@@ -324,10 +351,15 @@ int gated_scan_backward(PyObject* const* a) {
     const View z(a[0], gate, "gate"), x(a[1] == Py_None ? a[0] : a[1], gate, "x"), h(a[2], gate, "h"),
         dh(a[3], gate, "dh"), dz(a[4], gate, "dgate"), dx(a[5], gate, "dx");
     const Workspace ws(a[11]);
-    return adacomp_gated_scan_backward(&gate.shape, &z, a[1] == Py_None ? nullptr : &x, &h, &dh, &dz, &dx,
-                                       optional(a[6], gate.states, "h0"), optional(a[7], gate.states, "dh_last"),
-                                       optional(a[8], gate.states, "dh0"), lengths_of(a[9], gate), ws.p, ws.bytes,
-                                       stream_of(a[12]));
+    const bool with_x = a[1] != Py_None;
+    const float *h0 = optional(a[6], gate.states, "h0"), *dh_last = optional(a[7], gate.states, "dh_last");
+    float* dh0 = optional(a[8], gate.states, "dh0");
+    const int32_t* lengths = lengths_of(a[9], gate);
+    void* stream = stream_of(a[12]);
+    return unlocked([&] {
+        return adacomp_gated_scan_backward(&gate.shape, &z, with_x ? &x : nullptr, &h, &dh, &dz, &dx, h0, dh_last, dh0,
+                                           lengths, ws.p, ws.bytes, stream);
+    });
 }
 
 // No C++ exception leaves an entry point.

@@ -96,3 +96,10 @@ for t in (new(64, t=torch.float32, device=1), new(3, device=1)):
     else:
         raise AssertionError("taken")
 """)
+
+
+def test_calls_are_made_without_the_interpreter_lock(stub):
+    run(stub, """
+for name in CALLS:
+    assert call(name) == 100, name
+""")
