@@ -6,12 +6,13 @@
 //   w = w * keep - size * (m / (sqrt(v) * rbc2 + eps))
 // keep = 1 - lr_i wd_i, size = lr_i / (1 - b1^t), rbc2 = 1 / sqrt(1 - b2^t).
 //
-// About 15 operations per 28 bytes (float32 moments, float32 gradient) or 18
-// bytes (8-bit moments with the bf16 copy): memory bounds it.  A work tile is
+// About 15 operations per 28 bytes with float32 moments, about 80 per 18 bytes
+// with 8-bit ones (float64 moments, the hash, two quantisations) and the bf16
+// copy: memory bounds the first, and the second nearly so.  A work tile is
 // 1024 elements of one tensor, 256 threads with one vector of four elements
 // each; every buffer is touched once a step, so its accesses are non-temporal.
 // 268 M elements with float32 moments take 1.19 ms (6.3 TB/s), 25.2 M with 8-bit
-// moments, a bf16 gradient and the bf16 copy 65.5 us (6.2 TB/s).
+// moments, a bf16 gradient and the bf16 copy 66.2 us (6.1 TB/s).
 #pragma once
 
 #include "common.hpp"
@@ -68,8 +69,7 @@ __device__ __forceinline__ void store_part(T* p, V v, int left) {
 
 // One float64 partial sum of squares per workgroup: squares of float32 values
 // are exact in float64, each thread adds its own in tile order, the workgroup
-// joins its threads in a fixed order.  The loads leave the gradient in the
-// cache for the step that follows.  One tile at a time and 2048 workgroups:
+// joins its threads in a fixed order.  One tile at a time and 2048 workgroups:
 // 1.07 GB are read at 6.3 TB/s, and at 5.2 to 5.7 with two to eight tiles at
 // once, whose addresses lie further apart.
 __device__ __forceinline__ double join_256(double sum, int tid) {
@@ -121,12 +121,6 @@ k_grad_norm_finish(const double* __restrict__ partial, uint32_t n, double max_no
     }
 }
 
-// A workgroup's tile.  After a norm the step goes through the table backwards:
-// the gradient's end is what the norm's pass left in the cache.
-__device__ __forceinline__ OptTile step_tile(const AdamwArgs& a) {
-    return a.tiles[a.clip ? gridDim.x - 1 - blockIdx.x : blockIdx.x];
-}
-
 // A tile's step size and decay factor, formed in float64 and rounded once: six operations a thread,
 // beside 60 and more on its elements.
 struct Factors {
@@ -141,7 +135,7 @@ __device__ __forceinline__ Factors tile_factors(const AdamwArgs& a, const OptTil
 
 template <typename G>
 __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
-    const OptTile tile = step_tile(a);
+    const OptTile tile = a.tiles[blockIdx.x];
     const int tid = threadIdx.x;
     const Factors f = tile_factors(a, tile);
     const float factor = a.clip ? a.clip[1] * a.scale : a.scale;
@@ -227,7 +221,7 @@ __device__ __forceinline__ int e4m3_code(double x, double up, int random) {
 
 template <typename G>
 __global__ __launch_bounds__(256) void k_adamw_packed(AdamwArgs a) {
-    const OptTile tile = step_tile(a);
+    const OptTile tile = a.tiles[blockIdx.x];
     const int tid = threadIdx.x;
     const Factors f = tile_factors(a, tile);
     const double factor = a.clip ? double(a.clip[1]) * double(a.scale) : double(a.scale);
@@ -276,8 +270,9 @@ __global__ __launch_bounds__(256) void k_adamw_packed(AdamwArgs a) {
         m[c] = b1 * m[c] + a.omb1 * g;
         v[c] = b2 * v[c] + omb2 * (g * g);
     }
-    // the weights' step: the hardware's root and reciprocal are off by one unit in the last place of a
-    // term that is far below the weight
+    // The weights' step takes the hardware's root and reciprocal, each off by one unit in the last place of
+    // a term that is far below the weight: rounded to nearest they are a dozen instructions each
+    // (25.2 M elements with a bf16 gradient 73.3 us against 67.6).
     float q[4];
     bool far = false;
 #pragma unroll
