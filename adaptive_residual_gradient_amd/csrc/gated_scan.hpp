@@ -6,11 +6,12 @@
 // Each step is a map s -> a s + b of the carried state, and maps compose: the
 // steps of a tile are composed without knowing the state carried into it.  Once
 // it is known every forward result is one multiply-add of it, and the backward
-// recurrence runs again.  A tile is up to 256 steps (more where a sequence has
-// few channels) of 64 or 128 channels: 512 threads, each with 4 bytes of
-// channels and up to 16 consecutive steps that stay in registers between the two
-// halves, so inputs are read once and results written once.  The tile's threads
-// join their steps through LDS.  The state travels from tile to tile
+// recurrence runs again.  A tile is at most 128 steps (64 backward with the
+// sigmoid; more where a sequence has few channels) of 64 float32 or 128 16-bit
+// channels: 512 threads, each with 4 bytes of channels and up to 16 consecutive
+// steps that stay in registers between the two halves, so inputs are read once
+// and results written once.  The tile's threads join their steps through LDS.
+// The state travels from tile to tile
 //   - not at all, where one tile holds the whole sequence (kScanAlone);
 //   - through one word a channel that each tile leaves for its successor
 //     (kScanChain), where there are enough independent chains of tiles to hide
@@ -20,8 +21,8 @@
 // Sequences of at most kScanShort steps take one thread per 4 bytes of
 // channels (k_scan_short).
 //
-// Memory bounds it: 8 x 4096 x 2048 bf16 takes 78.6 us (5.1 TB/s), the gradients
-// of 1 x 65536 x 256 float32 70 us (4.9 TB/s).  The accesses of a tile alone, rows
+// Memory bounds it: 8 x 4096 x 2048 bf16 takes 82.5 us (4.9 TB/s), the gradients
+// of 1 x 65536 x 256 float32 69.4 us (4.8 TB/s).  The accesses of a tile alone, rows
 // of 256 bytes in 128 steps, run at 6.0 TB/s.
 #pragma once
 
@@ -30,9 +31,10 @@
 
 namespace adacomp {
 
-// Steps a thread holds.  Backward with the sigmoid 8: 16 of them take 110 registers, two workgroups
-// a CU (8 x 4096 x 2048 bf16 171 us against 142).  The others 16, for fewer tiles on the way of the state
-// (backward without the sigmoid, 1 x 65536 x 256 f32: 73 us against 85 with 8).
+// Steps a thread holds.  Backward with the sigmoid 8: 16 of them take more registers than there are (8 x
+// 4096 x 2048 bf16 238 us against 145), or one workgroup a CU fewer (1 x 65536 x 256 f32 83 against 95, but
+// 8 x 4096 x 2048 f32 296 against 278).  The others 16, for fewer tiles on the way of the state (backward without the sigmoid, 1 x 65536 x 256 f32
+// 71 us against 86 with 8, though 8 x 4096 x 2048 f32 270 against 236).
 constexpr int scan_thread_steps(bool sigmoid, bool back) { return sigmoid && back ? 8 : 16; }
 constexpr uint32_t kScanShort = 16;     // longest sequence of the short kernels
 constexpr uint32_t kScanThreads = 512;  // most threads of a tile
@@ -45,8 +47,9 @@ constexpr int kScanAlone = 0, kScanChain = 1, kScanBack = 2;
 constexpr uint32_t kScanWindow = 4;
 
 // Accesses: non-temporal; non-temporal results and inputs of at most kKeepBytes, which the call before
-// has just written, through the cache (8 x 2048 x 1024 bf16 22.0 us and 26.8, but backward, with twice
-// the inputs, 48.8 and 44.7); all through the cache.
+// has just written, through the cache (8 x 2048 x 1024 bf16, again and again on one set of buffers, 23.1 us
+// and 27.1 past it; its gradient's 134 MB, past the bound, 43.6 us and 36.2 through the cache); all
+// through the cache.
 constexpr int kScanStream = 0, kScanKeepIn = 1, kScanCached = 2;
 
 struct ScanView {

@@ -337,7 +337,7 @@ int adacomp_timer_reset(adacomp_timer* timer);
  * current device, asynchronous on `stream`, errors found on the host before
  * anything is enqueued, nothing allocated, deterministic); additions are
  * named at each call.  An output buffer must not overlap any other buffer of
- * the call. */
+ * the call; views of the gated scan may be parts of the same rows. */
 
 /* Element types of the operators' activations and gradients. */
 #define ADACOMP_FLOAT 0
@@ -425,8 +425,8 @@ int adacomp_adamw_step(const adacomp_optimizer* optimizer, float* weights, const
  *   scales            [2 * info.nblocks] bytes, 16-byte aligned: of block b (tensors
  *                     in table order), m's at 2b and v's at 2b + 1.  All zeros
  *                     is the state before the first step.
- * g, m and v are formed in float64 (the weights' step from them in float32)
- * and rounded once: the scale is the smallest in 0..254 under which the
+ * g, m and v are formed in float64 (the weights' step from them in float32, its
+ * root and quotient to a unit in the last place each) and rounded once: the scale is the smallest in 0..254 under which the
  * block's largest magnitude, cut to 20 fraction bits, is at most 448; each
  * magnitude, cut to a multiple of 2^-17 of its code's step, is rounded up with
  * the probability of its remainder.  The random bits of an element are a hash
@@ -479,15 +479,16 @@ int adacomp_layer_norm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t* b
  *   sigmoid = 1:  a = 1 / (1 + exp(-gate)),  k = 1 / (1 + exp(gate))  (= 1 - a)
  *   sigmoid = 0:  a = gate,  k = 1
  * states in float32, and a and k within 8 of its half units in the last place
- * (a no smaller than 1.6e-38, whatever the gate).  The sequence is cut into tiles whose gate products are
- * formed and joined, so with sigmoid = 0 the products of consecutive gates,
- * however many, have to stay below float32's largest number (gates in [-1, 1]
- * always do).  Products below its normal numbers keep an absolute error of
- * 2^-149, and are 0 only where a gate is.
+ * (a no smaller than 1.6e-38 whatever the gate, k 0 below 1.2e-38).  The
+ * sequence is cut into tiles whose gate products are formed and joined, so with
+ * sigmoid = 0 the products of consecutive gates, however many, have to stay
+ * below float32's largest number (gates in [-1, 1] always do).  Products below
+ * its normal numbers keep an absolute error of 2^-149, and are 0 only where a
+ * gate is.
  * ERR_TOO_LARGE: length or batch * channels from 2^31 on, batch or channels
- * from 2^24 on, strides past 2^32 (time) or 2^40 (batch), or more work-items than a launch has,
- * 2^32: one for each 8 steps (backward with the sigmoid) or 16 of 4 bytes of
- * adjacent channels, whole tiles counted. */
+ * from 2^24 on, time strides from 2^32 or batch strides from 2^40 on, or 2^32
+ * work-items and more: one for each 8 steps (backward with the sigmoid) or 16
+ * of 4 bytes of adjacent channels, whole tiles counted. */
 typedef struct adacomp_scan_shape {
     uint64_t length;      /* steps, n_b <= length; may be 0 */
     uint32_t batch;       /* sequences; may be 0 */
