@@ -8,7 +8,6 @@ import adaptive_residual_gradient_amd as A
 import operator_refs as R
 from test_gpu_adamw import P
 from test_gpu_gated_scan import Case
-from test_gpu_layer_norm import EPS, backward
 
 pytestmark = pytest.mark.gpu
 
