@@ -113,10 +113,31 @@ class _View(ctypes.Structure):
                 ("time_stride", ctypes.c_uint64)]
 
 
+class _ConvShape(ctypes.Structure):
+    _fields_ = [("length", ctypes.c_uint64), ("batch", ctypes.c_uint32), ("channels", ctypes.c_uint32),
+                ("taps", ctypes.c_uint32), ("type", ctypes.c_int), ("silu", ctypes.c_int)]
+
+
+class _SsmShape(ctypes.Structure):
+    _fields_ = [("length", ctypes.c_uint64), ("batch", ctypes.c_uint32), ("channels", ctypes.c_uint32),
+                ("states", ctypes.c_uint32), ("type", ctypes.c_int), ("softplus", ctypes.c_int)]
+
+
+class _SsmInputs(ctypes.Structure):
+    _fields_ = ([(k, _View) for k in ("x", "dt", "b", "c", "z")] +
+                [(k, ctypes.c_void_p) for k in ("a", "d", "dt_bias", "lengths")])
+
+
+class _SsmGradients(ctypes.Structure):
+    _fields_ = ([(k, _View) for k in ("dx", "ddt", "db", "dc", "dz")] +
+                [(k, ctypes.c_void_p) for k in ("da", "dd", "ddt_bias", "dh0")])
+
+
 # Every exported symbol, with its C signature (argtypes, restype).
 _P = ctypes.c_void_p
 _U32, _U64, _INT, _FLT = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
 _SHAPE, _VIEW = ctypes.POINTER(_ScanShape), ctypes.POINTER(_View)
+_CONV, _SSM = ctypes.POINTER(_ConvShape), ctypes.POINTER(_SsmShape)
 SIGNATURES = {
     "adacomp_plan_query": ([ctypes.POINTER(_Segment), _U32, ctypes.POINTER(PlanInfo)], _INT),
     "adacomp_plan_create": ([ctypes.POINTER(_Segment), _U32, ctypes.POINTER(_P)], _INT),
@@ -158,6 +179,14 @@ SIGNATURES = {
     "adacomp_gated_scan_backward": ([_SHAPE, _VIEW, _VIEW, _VIEW, _VIEW, _VIEW, _VIEW, _P, _P, _P, _P, _P,
                                      _U64, _P], _INT),
     "adacomp_gated_scan_workspace_bytes": ([_SHAPE, ctypes.POINTER(_U64)], _INT),
+    "adacomp_causal_conv": ([_CONV, _VIEW, _P, _P, _VIEW, _P, _P, _P, _P], _INT),
+    "adacomp_causal_conv_backward": ([_CONV, _VIEW, _VIEW, _P, _P, _VIEW, _P, _P, _P, _P, _P, _P, _U64, _P], _INT),
+    "adacomp_causal_conv_workspace_bytes": ([_CONV, ctypes.POINTER(_U64)], _INT),
+    "adacomp_selective_scan": ([_SSM, ctypes.POINTER(_SsmInputs), _VIEW, _P, _P, _P, _P, _U64, _P], _INT),
+    "adacomp_selective_scan_backward": ([_SSM, ctypes.POINTER(_SsmInputs), _VIEW, _P, _P,
+                                         ctypes.POINTER(_SsmGradients), _P, _U64, _P], _INT),
+    "adacomp_selective_scan_workspace_bytes": ([_SSM, _INT, ctypes.POINTER(_U64)], _INT),
+    "adacomp_selective_scan_kept_bytes": ([_SSM, ctypes.POINTER(_U64)], _INT),
     "adacomp_status_str": ([_INT], ctypes.c_char_p),
 }
 
@@ -563,3 +592,87 @@ def gated_scan_backward(gate, x, h, dh, dgate, dx, h0=None, dh_last=None, dh0=No
     st = _operators().gated_scan_backward(gate, x, h, dh, dgate, dx, h0, dh_last, dh0, lengths, sigmoid, ws, stream)
     if st:
         raise AdaCompError("adacomp_gated_scan_backward", st)
+
+
+CONV_MAX_TAPS = 8         # longest filter of causal_conv
+SCAN_MAX_STATES = 64      # most states of a channel of selective_scan
+
+
+def _type(dtype) -> int:
+    import torch
+    try:
+        return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
+    except KeyError:
+        raise TypeError(f"{dtype} is not float32, bfloat16 or float16") from None
+
+
+def _bytes(what, *args) -> int:
+    n = _U64(0)
+    _check(what, getattr(lib(), what)(*args, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _workspace(nbytes: int, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def causal_conv_workspace(batch: int, length: int, channels: int, taps: int, device="cuda"):
+    """Workspace of causal_conv_backward for one shape and any type."""
+    need = max(_bytes("adacomp_causal_conv_workspace_bytes",
+                      ctypes.byref(_ConvShape(int(length), int(batch), int(channels), int(taps), t, 0)))
+               for t in range(3))
+    return _workspace(need, device)
+
+
+def causal_conv(x, weight, bias, y, state=None, state_out=None, lengths=None, silu: bool = True, stream=None) -> None:
+    """y_t = act(bias + sum_k weight[:, k] x_(t - taps + 1 + k)) along axis 1 of [batch, length, channels]
+    tensors, act the identity or p * sigmoid(p); weight [channels, taps] and bias float32.  state and
+    state_out [batch, taps - 1, channels]: the steps before the first one, and before the next call's."""
+    st = _operators().causal_conv(x, weight, bias, y, state, state_out, lengths, silu, stream)
+    if st:
+        raise AdaCompError("adacomp_causal_conv", st)
+
+
+def causal_conv_backward(dy, x, weight, bias, dx, dweight, dbias=None, state=None, dstate=None, lengths=None,
+                         silu: bool = True, ws=None, stream=None) -> None:
+    """Gradients of causal_conv: dx, dweight and dbias (float32), and that of ``state``."""
+    st = _operators().causal_conv_backward(dy, x, weight, bias, dx, dweight, dbias, state, dstate, lengths, silu, ws,
+                                           stream)
+    if st:
+        raise AdaCompError("adacomp_causal_conv_backward", st)
+
+
+def selective_scan_workspace(batch: int, length: int, channels: int, states: int, backward: bool = False,
+                             device="cuda"):
+    """Workspace of selective_scan, or (``backward``) of it and selective_scan_backward, for one shape."""
+    shape = _SsmShape(int(length), int(batch), int(channels), int(states), 0, 0)
+    return _workspace(_bytes("adacomp_selective_scan_workspace_bytes", ctypes.byref(shape), int(bool(backward))), device)
+
+
+def selective_scan_states(batch: int, length: int, channels: int, states: int, device="cuda"):
+    """What selective_scan keeps for selective_scan_backward."""
+    import torch
+    shape = _SsmShape(int(length), int(batch), int(channels), int(states), 0, 0)
+    return torch.empty(_bytes("adacomp_selective_scan_kept_bytes", ctypes.byref(shape)) // 4, device=device)
+
+
+def selective_scan(x, dt, a, b, c, y, d=None, z=None, dt_bias=None, h0=None, h_last=None, states=None, lengths=None,
+                   softplus: bool = True, ws=None, stream=None) -> None:
+    """h <- exp(s a) h + s x b, y = (c . h + d x) * (z sigmoid(z) or 1) along axis 1, with s = softplus(dt + dt_bias)
+    or dt + dt_bias.  x, dt, z, y [batch, length, channels]; b, c [batch, length, states]; a [channels, states],
+    d, dt_bias [channels], h0, h_last [batch, channels, states] float32; ``states`` as
+    selective_scan_states gives it, for the gradients."""
+    st = _operators().selective_scan(x, dt, a, b, c, y, d, z, dt_bias, h0, h_last, states, lengths, softplus, ws, stream)
+    if st:
+        raise AdaCompError("adacomp_selective_scan", st)
+
+
+def selective_scan_backward(dy, x, dt, a, b, c, states, dx, ddt, da, db, dc, d=None, z=None, dt_bias=None, dz=None,
+                            dd=None, ddt_bias=None, dh_last=None, dh0=None, lengths=None, softplus: bool = True,
+                            ws=None, stream=None) -> None:
+    """Gradients of selective_scan from the ``states`` that it kept; da, dd, ddt_bias and dh0 float32."""
+    st = _operators().selective_scan_backward(dy, x, dt, a, b, c, states, dx, ddt, da, db, dc, d, z, dt_bias, dz, dd,
+                                              ddt_bias, dh_last, dh0, lengths, softplus, ws, stream)
+    if st:
+        raise AdaCompError("adacomp_selective_scan_backward", st)

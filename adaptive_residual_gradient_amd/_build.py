@@ -2,18 +2,20 @@
 operators' Python entry points (host code only) with g++."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import pathlib
 import subprocess
 import sysconfig
+import tempfile
 
 HERE = pathlib.Path(__file__).resolve().parent
-SOURCES = [HERE / "csrc" / "adacomp.hip", HERE / "csrc" / "training.hip"]
+SOURCES = [HERE / "csrc" / name for name in ("adacomp.hip", "training.hip", "sequence.hip")]
 LIB = HERE / "libadacomp.so"
 BINDING = HERE / "_binding.so"
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # Bit-exact float32: no contraction of a*b+c into fused multiply-adds.
     "-ffp-contract=off",
     # No packed fp32 instructions (v_pk_add_f32 and friends).
@@ -25,10 +27,19 @@ HIPCC_FLAGS = [
 def build(verbose: bool = False) -> pathlib.Path:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     tmp = LIB.with_suffix(".so.tmp")
-    cmd = [hipcc, *HIPCC_FLAGS, "-o", str(tmp), *map(str, SOURCES)]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+
+    def run(*args):
+        cmd = [hipcc, *HIPCC_FLAGS, *map(str, args)]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    # the sources side by side, each into an object of its own
+    with tempfile.TemporaryDirectory() as at, concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+        objects = [pathlib.Path(at) / (source.stem + ".o") for source in SOURCES]
+        for done in [pool.submit(run, "-c", s, "-o", o) for s, o in zip(SOURCES, objects)]:
+            done.result()
+        run("-shared", "-o", tmp, *objects)
     os.replace(tmp, LIB)
     build_binding(verbose)
     return LIB

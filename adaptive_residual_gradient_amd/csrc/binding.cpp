@@ -362,6 +362,175 @@ int gated_scan_backward(PyObject* const* a) {
     });
 }
 
+// ---- causal convolution and selective scan ----
+
+// [batch, length, channels] of the first view of a call, which the others have to match.
+struct Sequence {
+    const at::Tensor& t;
+    int type;
+    int64_t B, T, C;
+    Sequence(PyObject* o, const char* name) : t(tensor(o, name)), type(type_of(t, name)) {
+        if (t.dim() != 3) throw WrongValue(std::string(name) + " must be [batch, length, channels]");
+        B = t.size(0);
+        T = t.size(1);
+        C = t.size(2);
+    }
+    // sizes past 32 bits are past the C ABI's limits, in any number
+    static uint32_t narrow(int64_t n) { return uint32_t(std::min<int64_t>(n, 0xFFFFFFFF)); }
+    // A view of the same batch, length and type, `width` wide.
+    adacomp_view view(PyObject* o, int64_t width, const char* name) const {
+        const at::Tensor& v = tensor(o, name);
+        if (!v.is_cuda() || v.scalar_type() != t.scalar_type() || v.dim() != 3 || v.size(0) != B || v.size(1) != T ||
+            v.size(2) != width)
+            throw WrongValue(std::string(name) + " must be a CUDA tensor [" + std::to_string(B) + ", " + std::to_string(T) +
+                             ", " + std::to_string(width) + "] of the input's type");
+        check_device(v, name);
+        adacomp_view out{address(v), uint64_t(T * width), uint64_t(width)};
+        if (v.is_contiguous()) return out;
+        if (width > 1 && v.stride(2) != 1) throw WrongType(std::string(name) + " must have adjacent channels");
+        out.batch_stride = uint64_t(B > 1 ? v.stride(0) : 0);
+        out.time_stride = uint64_t(T > 1 ? v.stride(1) : width);
+        return out;
+    }
+    adacomp_view view(PyObject* o, const char* name) const { return view(o, C, name); }
+    // A nullable one.
+    adacomp_view optional_view(PyObject* o, const char* name) const {
+        return o == Py_None ? adacomp_view{nullptr, 0, 0} : view(o, C, name);
+    }
+    const int32_t* lengths(PyObject* o) const { return optional<int32_t>(o, B, "lengths", at::kInt); }
+};
+
+// Address of a contiguous tensor of n elements that has to be there.
+float* needed(PyObject* o, int64_t n, const char* name) {
+    if (o == Py_None) throw WrongType(std::string(name) + " must be a tensor");
+    return optional(o, n, name);
+}
+
+struct Conv {
+    adacomp_conv_shape shape;
+    float* weight;
+    int64_t taps, states;
+    Conv(const Sequence& q, PyObject* w, bool silu) {
+        const at::Tensor& t = tensor(w, "weight");
+        if (t.dim() != 2 || t.size(0) != q.C) throw WrongValue("weight must be [channels, taps]");
+        taps = t.size(1);
+        weight = needed(w, q.C * taps, "weight");
+        states = q.B * (taps - 1) * q.C;
+        shape = {uint64_t(q.T), Sequence::narrow(q.B), Sequence::narrow(q.C), Sequence::narrow(taps), q.type, silu ? 1 : 0};
+    }
+    void* state(PyObject* o, const Sequence& q, const char* name) const {
+        return optional<void>(o, states, name, q.t.scalar_type());
+    }
+};
+
+// x, weight, bias, y, state, state_out, lengths, silu, stream
+int causal_conv(PyObject* const* a) {
+    const Sequence q(a[0], "x");
+    const Conv k(q, a[1], truth(a[7]));
+    const adacomp_view x = q.view(a[0], "x"), y = q.view(a[3], "y");
+    const float* bias = optional(a[2], q.C, "bias");
+    const void* state = k.state(a[4], q, "state");
+    void* state_out = k.state(a[5], q, "state_out");
+    const int32_t* lengths = q.lengths(a[6]);
+    void* stream = stream_of(a[8]);
+    return unlocked([&] {
+        return adacomp_causal_conv(&k.shape, &x, k.weight, bias, &y, state, state_out, lengths, stream);
+    });
+}
+
+// dy, x, weight, bias, dx, dweight, dbias, state, dstate, lengths, silu, ws, stream
+int causal_conv_backward(PyObject* const* a) {
+    const Sequence q(a[0], "dy");
+    const Conv k(q, a[2], truth(a[10]));
+    const adacomp_view dy = q.view(a[0], "dy"), x = q.view(a[1], "x"), dx = q.view(a[4], "dx");
+    const float* bias = optional(a[3], q.C, "bias");
+    float *dweight = needed(a[5], q.C * k.taps, "dweight"), *dbias = optional(a[6], q.C, "dbias");
+    const void* state = k.state(a[7], q, "state");
+    void* dstate = k.state(a[8], q, "dstate");
+    const int32_t* lengths = q.lengths(a[9]);
+    const Workspace ws(a[11]);
+    void* stream = stream_of(a[12]);
+    return unlocked([&] {
+        return adacomp_causal_conv_backward(&k.shape, &dy, &x, k.weight, bias, &dx, dweight, dbias, state, dstate, lengths,
+                                            ws.p, ws.bytes, stream);
+    });
+}
+
+// The inputs that both directions of the selective scan take.
+struct Ssm {
+    adacomp_ssm_shape shape;
+    adacomp_ssm_inputs in;
+    int64_t N, states;
+    // x, dt, a, b, c; d, z, dt_bias; lengths
+    Ssm(const Sequence& q, PyObject* const* five, PyObject* const* three, PyObject* lengths, bool softplus) {
+        const at::Tensor& t = tensor(five[2], "a");
+        if (t.dim() != 2 || t.size(0) != q.C) throw WrongValue("a must be [channels, states]");
+        N = t.size(1);
+        states = q.B * q.C * N;
+        in.x = q.view(five[0], "x");
+        in.dt = q.view(five[1], "dt");
+        in.a = needed(five[2], q.C * N, "a");
+        in.b = q.view(five[3], N, "b");
+        in.c = q.view(five[4], N, "c");
+        in.d = optional(three[0], q.C, "d");
+        in.z = q.optional_view(three[1], "z");
+        in.dt_bias = optional(three[2], q.C, "dt_bias");
+        in.lengths = q.lengths(lengths);
+        shape = {uint64_t(q.T), Sequence::narrow(q.B), Sequence::narrow(q.C), Sequence::narrow(N), q.type, softplus ? 1 : 0};
+    }
+};
+
+// What the forward call keeps for the gradients.
+float* kept_of(PyObject* o, const Ssm& s) {
+    if (o == Py_None) return nullptr;
+    uint64_t bytes = 0;
+    const at::Tensor& t = tensor(o, "states");
+    check(t, at::kFloat, "states");
+    if (adacomp_selective_scan_kept_bytes(&s.shape, &bytes) == ADACOMP_OK && uint64_t(t.numel()) * 4 < bytes)
+        throw WrongValue("states must have " + std::to_string(bytes / 4) + " elements");
+    return address<float>(t);
+}
+
+// x, dt, a, b, c, y, d, z, dt_bias, h0, h_last, states, lengths, softplus, ws, stream
+int selective_scan(PyObject* const* a) {
+    const Sequence q(a[0], "x");
+    const Ssm s(q, a, a + 6, a[12], truth(a[13]));
+    const adacomp_view y = q.view(a[5], "y");
+    const float* h0 = optional(a[9], s.states, "h0");
+    float *h_last = optional(a[10], s.states, "h_last"), *kept = kept_of(a[11], s);
+    const Workspace ws(a[14]);
+    void* stream = stream_of(a[15]);
+    return unlocked([&] {
+        return adacomp_selective_scan(&s.shape, &s.in, &y, h0, h_last, kept, ws.p, ws.bytes, stream);
+    });
+}
+
+// dy, x, dt, a, b, c, states, dx, ddt, da, db, dc, d, z, dt_bias, dz, dd, ddt_bias, dh_last, dh0, lengths, softplus, ws,
+// stream
+int selective_scan_backward(PyObject* const* a) {
+    const Sequence q(a[0], "dy");
+    const Ssm s(q, a + 1, a + 12, a[20], truth(a[21]));
+    const adacomp_view dy = q.view(a[0], "dy");
+    const float* kept = kept_of(a[6], s);
+    adacomp_ssm_gradients g;
+    g.dx = q.view(a[7], "dx");
+    g.ddt = q.view(a[8], "ddt");
+    g.da = needed(a[9], q.C * s.N, "da");
+    g.db = q.view(a[10], s.N, "db");
+    g.dc = q.view(a[11], s.N, "dc");
+    g.dz = q.optional_view(a[15], "dz");
+    if ((a[13] == Py_None) != (a[15] == Py_None)) throw WrongValue("z and dz must be given together");
+    g.dd = optional(a[16], q.C, "dd");
+    g.ddt_bias = optional(a[17], q.C, "ddt_bias");
+    const float* dh_last = optional(a[18], s.states, "dh_last");
+    g.dh0 = optional(a[19], s.states, "dh0");
+    const Workspace ws(a[22]);
+    void* stream = stream_of(a[23]);
+    return unlocked([&] {
+        return adacomp_selective_scan_backward(&s.shape, &s.in, &dy, kept, dh_last, &g, ws.p, ws.bytes, stream);
+    });
+}
+
 // No C++ exception leaves an entry point.
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -399,6 +568,10 @@ PyMethodDef methods[] = {
     ENTRY("layer_norm_backward", (entry<layer_norm_backward, 10>)),
     ENTRY("gated_scan", (entry<gated_scan, 9>)),
     ENTRY("gated_scan_backward", (entry<gated_scan_backward, 13>)),
+    ENTRY("causal_conv", (entry<causal_conv, 9>)),
+    ENTRY("causal_conv_backward", (entry<causal_conv_backward, 13>)),
+    ENTRY("selective_scan", (entry<selective_scan, 16>)),
+    ENTRY("selective_scan_backward", (entry<selective_scan_backward, 24>)),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

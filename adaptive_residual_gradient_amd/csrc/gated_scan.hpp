@@ -27,7 +27,7 @@
 #pragma once
 
 #include "common.hpp"
-#include "elements.hpp"
+#include "sequence.hpp"
 
 namespace adacomp {
 
@@ -51,11 +51,6 @@ constexpr uint32_t kScanWindow = 4;
 // and 27.1 past it; its gradient's 134 MB, past the bound, 43.6 us and 36.2 through the cache); all
 // through the cache.
 constexpr int kScanStream = 0, kScanKeepIn = 1, kScanCached = 2;
-
-struct ScanView {
-    void* p;
-    uint64_t bs, ts;   // batch and time strides in elements
-};
 
 struct ScanArgs {
     ScanView gate, x, h, dh, dgate, dx;
@@ -83,12 +78,8 @@ __device__ __forceinline__ void gates(float z, float& a, float& k) {
         k = 1.f;
         return;
     }
-    constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;   // ln 2 = the sum of both
     z = __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -87.f), 100.f);
-    const float p = z * -kLog2e;
-    float e = __builtin_amdgcn_exp2f(p);
-    // what the rounding of p leaves out, -z - p ln 2: without it e would be off by 2^-24 |z|
-    e = __builtin_fmaf(e, __builtin_fmaf(p, -kLn2Low, __builtin_fmaf(p, -kLn2, -z)), e);
+    const float e = exp_of_minus(z);
     const float d = 1.f + e;
     a = __builtin_amdgcn_rcpf(d);
     // the hardware's reciprocal is off by one unit in the last place, which float32 calls take out too
@@ -109,14 +100,7 @@ __device__ __forceinline__ float gate_product(float p, float f) {
 }
 
 __device__ __forceinline__ uint64_t scan_steps(const ScanArgs& a, uint32_t b) {
-    if (a.lengths == nullptr) return a.length;
-    const int32_t n = a.lengths[b];
-    return n <= 0 ? 0 : (uint64_t(n) < a.length ? uint64_t(n) : a.length);
-}
-
-template <typename T>
-__device__ __forceinline__ T* view_at(const ScanView& v, uint32_t b, uint64_t t, uint32_t c) {
-    return static_cast<T*>(v.p) + uint64_t(b) * v.bs + t * v.ts + c;
+    return steps_of(a.lengths, a.length, b);
 }
 
 // ---- tiles ----

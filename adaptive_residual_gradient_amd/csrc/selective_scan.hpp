@@ -1,0 +1,642 @@
+// Selective state space scan along the sequence, and its gradients, for gfx950.
+//
+//   h_n <- e_n h_n + u b_n,  e_n = exp(s a_n),  u = s x       (forward, t ascending)
+//   y = (sum_n c_n h_n + d x) silu(z)
+//   l_n = r c_n + f_n,  f_n <- e_n l_n,  r = dy silu(z)        (backward, t descending; f_n is carried)
+//   dc_n = sum r h_n,  db_n = sum l_n u  (over channels),  du = sum_n l_n b_n,
+//   q_n = f_n h_n(before),  ds = sum_n q_n a_n + du x,  da_n = sum q_n s,  dx = du s + d r
+//
+// The exponentials and the states' updates bound it, not the memory: forward 5
+// instructions for every step, channel and state, one of them an exponential,
+// and backward 17.  So a lane has one channel and a block of its states in
+// registers, nothing is reduced across lanes on the way to y, and b and c, which
+// all channels share, come through scalar registers: a kernel before lays them
+// out as float32 rows (k_ssm_rows).
+//
+// A long sequence is cut into chunks, for there are too few channels to fill the
+// chip.  A first pass forms each chunk's states from 0 (k_ssm_forward, ENDS), a
+// second joins them (k_ssm_join): the decay of a whole chunk is exp(a_n sum s).
+// Then the chunks run on their own.  Backward does the same with f.
+//
+// Backward needs the states of every step.  Forward keeps every 8th, and a
+// block of 8 steps is formed again in registers: 8 states a wavefront, whose
+// decays and states of 8 steps just fit, so the states' blocks of one channel
+// are different wavefronts, which add up du and the like through LDS.  The sums over
+// channels of db and dc are formed by exchanging halves of the values with
+// halves of the lanes: 16 values of 64 lanes take 33 instructions a step, not
+// the 192 of 16 reductions.
+#pragma once
+
+#include "sequence.hpp"
+
+namespace adacomp {
+
+constexpr uint32_t kSsmKeep = 8;        // steps from one kept state to the next; also a block of the kernels
+constexpr uint32_t kSsmBlock = 16;      // states of a wavefront forward (8 where there are no more)
+constexpr uint32_t kSsmBackBlock = 8;   // and backward
+constexpr uint32_t kSsmShort = 8;       // longest sequence of the short kernel
+
+struct SsmArgs {
+    ScanView x, dt, z, y, dy, dx, ddt, dz;   // z.p nullable
+    ScanView b, c, db, dc;
+    const float* a;          // [channels][states]
+    const float* d;          // nullable
+    const float* dt_bias;    // nullable
+    const float* h0;         // nullable; backward: dh_last
+    float* last;             // nullable: h_last, or dh0
+    float* kept;             // [batch][length / 8][padded][channels], nullable forward
+    const int32_t* lengths;  // nullable
+    float* rows;             // [batch][length][2][padded]: b and c
+    float* ends;             // [batch][chunk][padded][channels]: a chunk's end from 0, then what is carried in
+    float* sums;             // [batch][chunk][channels]: sum of s
+    float* part_rows;        // [group of 64 channels][batch][length][2][padded]: db and dc
+    float* part_a;           // [batch][chunk][padded + 2][channels]: da, dd, ddt_bias
+    uint64_t length;
+    uint32_t batch, channels, states, padded;   // padded: states in whole blocks of the forward pass
+    uint32_t chunks, steps;                     // steps a chunk, a multiple of 8
+    uint32_t groups, blocks;                    // wavefronts that cover the channels, and the states
+    bool softplus;
+};
+
+// log(1 + exp(v)).
+__device__ __forceinline__ float softplus(float v) {
+    const float e = exp_of_minus(__builtin_elementwise_minimum(__builtin_fabsf(v), 100.f));
+    const float w = 1.f + e;
+    // what the rounding of 1 + e leaves out, relative to it
+    const float low = (e - (w - 1.f)) * __builtin_amdgcn_rcpf(w);
+    const float l = __builtin_fmaf(__builtin_amdgcn_logf(w), kLn2, low);
+    return __builtin_elementwise_maximum(v, 0.f) + l;
+}
+// 1 / (1 + exp(-v)); from -87 down it stays at 1.6e-38.
+__device__ __forceinline__ float logistic(float v) {
+    v = __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, -87.f), 100.f);
+    const float w = 1.f + exp_of_minus(v), r = __builtin_amdgcn_rcpf(w);
+    return __builtin_fmaf(r, __builtin_fmaf(-w, r, 1.f), r);
+}
+
+// b and c as float32 rows of whole blocks, zeros behind the states.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ssm_rows(SsmArgs a) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t n = uint32_t(i % a.padded), which = uint32_t(i / a.padded) & 1u;
+    const uint64_t row = i / (2 * a.padded), b = row / a.length, t = row % a.length;
+    if (b >= a.batch) return;
+    float v = 0.f;
+    if (n < a.states && t < steps_of(a.lengths, a.length, uint32_t(b)))
+        v = float(*view_at<T>(which ? a.c : a.b, uint32_t(b), t, n));
+    a.rows[i] = v;
+}
+
+// A wavefront's place in its workgroup, as a number that all its lanes share.
+__device__ __forceinline__ uint32_t wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
+// b and c are the same for all lanes and are not written while a kernel reads them: scalar loads.
+typedef const float __attribute__((address_space(4))) SsmRow;
+__device__ __forceinline__ SsmRow* ssm_row(const float* p) {
+    return reinterpret_cast<SsmRow*>(reinterpret_cast<uintptr_t>(p));
+}
+
+// The place of a wavefront.
+struct SsmPlace {
+    uint32_t b, chunk, group, block, c, lane;
+    uint64_t t0, t1, n;      // the chunk's steps of the tensor, and the sequence's steps
+    __device__ __forceinline__ SsmPlace(const SsmArgs& a) {
+        // a workgroup's wavefronts: the blocks of one group of channels, then the next group's
+        const uint32_t wave = wave_of(), per = blockDim.x / 64 / a.blocks, wide = (a.groups + per - 1) / per;
+        lane = threadIdx.x % 64;
+        block = wave % a.blocks;
+        group = blockIdx.x % wide * per + wave / a.blocks;
+        const uint32_t at = blockIdx.x / wide;
+        chunk = at % a.chunks;
+        b = at / a.chunks;
+        c = min(group * 64 + lane, a.channels - 1);
+        n = steps_of(a.lengths, a.length, b);
+        t0 = uint64_t(chunk) * a.steps;
+        t1 = t0 + a.steps < a.length ? t0 + a.steps : a.length;
+    }
+};
+
+// The rates a_n of a block in units of log 2; zeros behind the states.
+template <int NB>
+__device__ __forceinline__ void ssm_rates(const SsmArgs& a, const SsmPlace& w, float (&a2)[NB]) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const uint32_t at = w.block * NB + n;
+        a2[n] = at < a.states ? a.a[uint64_t(w.c) * a.states + at] * kLog2e : 0.f;
+    }
+}
+
+// Forward.  ENDS: only the states at the chunk's end, from 0.
+template <typename T, int NB, bool ENDS>
+__global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
+    constexpr int S = kSsmKeep;
+    extern __shared__ float lds[];   // [2][wavefront][S][64], where a channel's states are several blocks
+    const SsmPlace w(a);
+    const uint32_t c = w.c, b = w.b;
+    const bool mine = w.group < a.groups;
+    float a2[NB], h[NB], total = 0.f;
+    ssm_rates<NB>(a, w, a2);
+    const uint64_t end = w.t1 < w.n ? w.t1 : w.n;
+    const uint64_t ends = ((uint64_t(b) * a.chunks + w.chunk) * a.padded + w.block * NB) * a.channels + c;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        h[n] = 0.f;
+        const uint32_t at = w.block * NB + n;
+        if (ENDS) continue;
+        if (a.chunks > 1) {
+            h[n] = a.ends[ends + uint64_t(n) * a.channels];
+        } else if (a.h0 != nullptr && at < a.states) {
+            h[n] = a.h0[(uint64_t(b) * a.channels + c) * a.states + at];
+        }
+    }
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, d = a.d ? a.d[c] : 0.f;
+    const bool gated = a.z.p != nullptr, soft = a.softplus;
+    uint32_t turn = 0;
+    for (uint64_t t = w.t0; t < end; t += S, turn ^= 1u) {
+        const int left = end - t < uint64_t(S) ? int(end - t) : S;
+        T xr[S], sr[S], zr[S];
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            const uint64_t at = u < left ? t + u : end - 1;
+            xr[u] = *view_at<T>(a.x, b, at, c);
+            sr[u] = *view_at<T>(a.dt, b, at, c);
+            if (!ENDS && gated) zr[u] = *view_at<T>(a.z, b, at, c);
+        }
+        if (!ENDS && a.kept != nullptr && mine) {
+            float* k = a.kept + ((uint64_t(b) * ((a.length + S - 1) / S) + t / S) * a.padded + w.block * NB) * a.channels + c;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) k[uint64_t(n) * a.channels] = h[n];
+        }
+        float y[S];
+        SsmRow* row = ssm_row(a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB);
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            y[u] = 0.f;
+            if (u >= left) continue;
+            SsmRow* bs = row + uint64_t(u) * 2 * a.padded;
+            float s = float(sr[u]) + bias;
+            if (soft) s = softplus(s);
+            const float v = s * float(xr[u]);
+            if (ENDS) total += s;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * a2[n]), h[n], v * bs[n]);
+                if (!ENDS) y[u] = __builtin_fmaf(bs[a.padded + n], h[n], y[u]);
+            }
+        }
+        if (ENDS) continue;
+        auto finish = [&](int u, float sum) {
+            sum = __builtin_fmaf(d, float(xr[u]), sum);
+            if (gated) {
+                const float z = float(zr[u]);
+                sum *= z * logistic(z);
+            }
+            if (mine) *view_at<T>(a.y, b, t + u, c) = T(sum);
+        };
+        if (a.blocks == 1) {
+#pragma unroll
+            for (int u = 0; u < S; ++u)
+                if (u < left) finish(u, y[u]);
+        } else {
+            float* at = lds + turn * blockDim.x * S;
+            const uint32_t wave = wave_of(), first = wave - w.block;
+#pragma unroll
+            for (int u = 0; u < S; ++u) at[(wave * S + u) * 64 + w.lane] = y[u];
+            __syncthreads();   // the other half is free again: whoever writes it next has passed this
+#pragma unroll
+            for (int u = 0; u < S; ++u) {
+                if (u >= left || u % a.blocks != w.block) continue;
+                float sum = 0.f;
+                for (uint32_t j = 0; j < a.blocks; ++j) sum += at[((first + j) * S + u) * 64 + w.lane];
+                finish(u, sum);
+            }
+        }
+    }
+    if (!mine) return;
+    if (ENDS) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) a.ends[ends + uint64_t(n) * a.channels] = h[n];
+        if (w.block == 0) a.sums[(uint64_t(b) * a.chunks + w.chunk) * a.channels + c] = total;
+        return;
+    }
+    if (a.chunks == 1 && a.last != nullptr)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            if (w.block * NB + n < a.states) a.last[(uint64_t(b) * a.channels + c) * a.states + w.block * NB + n] = h[n];
+    if (w.block == 0)
+        for (uint64_t t = end > w.t0 ? end : w.t0; t < w.t1; ++t) *view_at<T>(a.y, b, t, c) = T(0.f);
+}
+
+// What is carried into each chunk takes the place of its end from 0; backward
+// (BACK) from the last chunk to the first.  One thread a sequence, state and channel.
+template <bool BACK>
+__global__ __launch_bounds__(256) void k_ssm_join(SsmArgs a) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t c = uint32_t(i % a.channels), n = uint32_t(i / a.channels % a.padded);
+    const uint64_t b = i / a.channels / a.padded;
+    if (b >= a.batch) return;
+    const uint64_t place = (b * a.channels + c) * a.states + n;
+    float h = 0.f, a2 = 0.f;
+    if (n < a.states) {
+        a2 = a.a[uint64_t(c) * a.states + n] * kLog2e;
+        if (a.h0 != nullptr) h = a.h0[place];
+    }
+    constexpr uint32_t U = 4;   // chunks requested together
+    for (uint32_t k = 0; k < a.chunks; k += U) {
+        float end[U], sum[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t at = min(k + u, a.chunks - 1), chunk = BACK ? a.chunks - 1 - at : at;
+            end[u] = a.ends[((b * a.chunks + chunk) * a.padded + n) * a.channels + c];
+            sum[u] = a.sums[(b * a.chunks + chunk) * a.channels + c];
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            if (k + u >= a.chunks) continue;
+            const uint32_t chunk = BACK ? a.chunks - 1 - (k + u) : k + u;
+            a.ends[((b * a.chunks + chunk) * a.padded + n) * a.channels + c] = h;
+            h = __builtin_fmaf(__builtin_amdgcn_exp2f(sum[u] * a2), h, end[u]);
+        }
+    }
+    if (a.last != nullptr && n < a.states) a.last[place] = h;
+}
+
+// Sequences of at most kSsmShort steps: `quads` lanes a channel with 4 states each.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ssm_short(SsmArgs a, uint32_t quads) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t q = uint32_t(i % quads);
+    const uint64_t unit = i / quads;
+    const bool mine = unit < uint64_t(a.batch) * a.channels;
+    // lanes past the end go along with the last channel: the sum over the quads takes all lanes
+    const uint64_t at = mine ? unit : uint64_t(a.batch) * a.channels - 1;
+    const uint32_t c = uint32_t(at % a.channels), b = uint32_t(at / a.channels);
+    const uint32_t n0 = q * 4, left = n0 < a.states ? min(a.states - n0, 4u) : 0;
+    const uint32_t n = uint32_t(steps_of(a.lengths, a.length, b));
+    FVec<4> h = 0.f, a2 = 0.f;
+    const uint64_t place = at * a.states + n0;
+    if (left == 4) {
+        a2 = load_any<4>(a.a + uint64_t(c) * a.states + n0);
+        if (a.h0) h = load_any<4>(a.h0 + place);
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+            if (k >= left) continue;
+            a2[k] = a.a[uint64_t(c) * a.states + n0 + k];
+            if (a.h0) h[k] = a.h0[place + k];
+        }
+    }
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, d = a.d ? a.d[c] : 0.f;
+    for (uint32_t t = 0; t < n; ++t) {
+        const T* bp = view_at<T>(a.b, b, t, n0);
+        const T* cp = view_at<T>(a.c, b, t, n0);
+        FVec<4> bv = 0.f, cv = 0.f;
+        if (left == 4) {
+            bv = to_float<4, T>(load_any<4>(bp));
+            cv = to_float<4, T>(load_any<4>(cp));
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                if (k >= left) continue;
+                bv[k] = float(bp[k]);
+                cv[k] = float(cp[k]);
+            }
+        }
+        const float x = float(*view_at<T>(a.x, b, t, c));
+        float s = float(*view_at<T>(a.dt, b, t, c)) + bias, y = 0.f;
+        if (a.softplus) s = softplus(s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * (a2[k] * kLog2e)), h[k], s * x * bv[k]);
+            y = __builtin_fmaf(cv[k], h[k], y);
+        }
+        for (uint32_t m = 1; m < quads; m *= 2) y += __shfl_xor(y, int(m));
+        y = __builtin_fmaf(d, x, y);
+        if (a.z.p != nullptr) {
+            const float z = float(*view_at<T>(a.z, b, t, c));
+            y *= z * logistic(z);
+        }
+        if (mine && q == 0) *view_at<T>(a.y, b, t, c) = T(y);
+    }
+    if (!mine) return;
+    if (q == 0)
+        for (uint64_t t = n; t < a.length; ++t) *view_at<T>(a.y, b, t, c) = T(0.f);
+    if (a.last == nullptr) return;
+    if (left == 4) {
+        store_any<4>(a.last + place, h);
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            if (k < left) a.last[place + k] = h[k];
+    }
+}
+
+// ---- backward ----
+
+// r = dy silu(z), and what dz needs.
+struct SsmGate {
+    float gate = 1.f, slope = 0.f;   // silu(z) and its derivative
+    __device__ __forceinline__ SsmGate() {}
+    __device__ __forceinline__ explicit SsmGate(float z) {
+        const float q = logistic(z);
+        gate = z * q;
+        slope = __builtin_fmaf(gate, 1.f - q, q);
+    }
+};
+
+// f at each chunk's first step from 0 at its end, and the sum of s.
+template <typename T, int NB>
+__global__ __launch_bounds__(256) void k_ssm_back_ends(SsmArgs a) {
+    constexpr int S = kSsmKeep;
+    const SsmPlace w(a);
+    if (w.group >= a.groups) return;
+    const uint32_t c = w.c, b = w.b;
+    float a2[NB], f[NB], total = 0.f;
+    ssm_rates<NB>(a, w, a2);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) f[n] = 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+    const bool gated = a.z.p != nullptr, soft = a.softplus;
+    const uint64_t end = w.t1 < w.n ? w.t1 : w.n;
+    for (uint64_t t = end; t > w.t0;) {
+        const int left = t - w.t0 < uint64_t(S) ? int(t - w.t0) : S;
+        T dr[S], sr[S], zr[S];
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            const uint64_t at = u < left ? t - 1 - u : w.t0;
+            dr[u] = *view_at<T>(a.dy, b, at, c);
+            sr[u] = *view_at<T>(a.dt, b, at, c);
+            if (gated) zr[u] = *view_at<T>(a.z, b, at, c);
+        }
+        t -= uint32_t(left);
+        SsmRow* row = ssm_row(a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + a.padded + w.block * NB);
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            if (u >= left) continue;
+            SsmRow* cs = row + uint64_t(left - 1 - u) * 2 * a.padded;
+            float s = float(sr[u]) + bias;
+            if (soft) s = softplus(s);
+            total += s;
+            float r = float(dr[u]);
+            if (gated) {
+                const float z = float(zr[u]);
+                r *= z * logistic(z);
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+                f[n] = __builtin_amdgcn_exp2f(s * a2[n]) * __builtin_fmaf(r, cs[n], f[n]);
+        }
+    }
+    const uint64_t ends = ((uint64_t(b) * a.chunks + w.chunk) * a.padded + w.block * NB) * a.channels + c;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) a.ends[ends + uint64_t(n) * a.channels] = f[n];
+    if (w.block == 0) a.sums[(uint64_t(b) * a.chunks + w.chunk) * a.channels + c] = total;
+}
+
+template <int N>
+struct Const {
+    static constexpr int value = N;
+};
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false));
+}
+
+// The sums over lanes of v[0..15], each over a quarter of 16 lanes: lane l has value
+// 8 (l / 32) + 4 (l / 16 % 2) + 2 (l / 8 % 2) + l / 4 % 2, summed over the lanes that are congruent to l modulo 4.
+__device__ __forceinline__ float sum_halves(float (&v)[16]) {
+    typedef unsigned int Pair __attribute__((ext_vector_type(2)));
+    float p[8], q[4], r[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {   // the lower 32 lanes keep v[i], the upper ones v[i + 8]
+        const Pair x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]), false, false);
+        p[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // rows of 16 lanes
+        const Pair x = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[i]), __float_as_uint(p[i + 4]), false, false);
+        q[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+    auto move = [](float old, float from, auto ctrl, auto banks) {
+        return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+            static_cast<int>(__float_as_uint(old)), static_cast<int>(__float_as_uint(from)), decltype(ctrl)::value, 0xf,
+            decltype(banks)::value, false)));
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {   // halves of a row: row_ror:8
+        const float own = move(q[i], q[i + 2], Const<0x128>{}, Const<0xc>{});
+        const float other = move(q[i + 2], q[i], Const<0x128>{}, Const<0x3>{});
+        r[i] = own + other;
+    }
+    // quarters: row_shr:4 and row_shl:4.  own: in the odd quarters r[1] of the lane 4 before; other: in the
+    // even ones r[0] of the lane 4 behind
+    const float own = move(r[0], r[1], Const<0x114>{}, Const<0xa>{});
+    const float other = move(r[1], r[0], Const<0x104>{}, Const<0x5>{});
+    return own + other;
+}
+// Of four such values the sums over the four lanes: lane l has that of value l % 4.
+__device__ __forceinline__ float sum_quads(float v0, float v1, float v2, float v3, uint32_t lane) {
+    auto swap1 = [](float x) {   // quad_perm:[1,0,3,2]
+        return __uint_as_float(dpp_move<0xB1>(__float_as_uint(x)));
+    };
+    auto swap2 = [](float x) {   // quad_perm:[2,3,0,1]
+        return __uint_as_float(dpp_move<0x4E>(__float_as_uint(x)));
+    };
+    const bool hi = lane & 2u, odd = lane & 1u;
+    const float a = (hi ? v2 : v0) + swap2(hi ? v0 : v2);   // lanes 0, 1: v0; 2, 3: v2
+    const float b = (hi ? v3 : v1) + swap2(hi ? v1 : v3);
+    return (odd ? b : a) + swap1(odd ? a : b);
+}
+
+template <typename T, bool GATED>
+__global__ __launch_bounds__(512) void k_ssm_backward(SsmArgs a) {
+    constexpr int S = kSsmKeep, NB = kSsmBackBlock, V = GATED ? 3 : 2;
+    extern __shared__ float lds[];   // [2][wavefront][V][S][64], where a channel's states are several blocks
+    const SsmPlace w(a);
+    const uint32_t c = w.c, b = w.b, wave = wave_of(), first = wave - w.block;
+    // a lane past the last channel goes along with it, without a part in the sums over channels
+    const bool mine = w.group < a.groups && w.group * 64 + w.lane < a.channels;
+    const uint32_t group = w.group < a.groups ? w.group : a.groups - 1;
+    float a2[NB], f[NB], da[NB], dd = 0.f, dbias = 0.f;
+    ssm_rates<NB>(a, w, a2);
+    const uint64_t ends = ((uint64_t(b) * a.chunks + w.chunk) * a.padded + w.block * NB) * a.channels + c;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        da[n] = f[n] = 0.f;
+        const uint32_t at = w.block * NB + n;
+        if (a.chunks > 1) f[n] = a.ends[ends + uint64_t(n) * a.channels];
+        else if (a.h0 != nullptr && at < a.states) f[n] = a.h0[(uint64_t(b) * a.channels + c) * a.states + at];
+    }
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, d = a.d ? a.d[c] : 0.f;
+    const bool soft = a.softplus;
+    const uint64_t end = w.t1 < w.n ? w.t1 : w.n, keeps = (a.length + S - 1) / S;
+    uint32_t turn = 0;
+    for (uint64_t t = w.t0 < end ? (end - 1) / S * S : 0; w.t0 < end; t -= S, turn ^= 1u) {
+        const int left = end - t < uint64_t(S) ? int(end - t) : S;
+        T xr[S], sr[S], dr[S], zr[S];
+        float h[S + 1][NB], e[S][NB], s[S], u_[S], r[S], du[S], ds[S], sum[S];
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            const uint64_t at = u < left ? t + u : end - 1;
+            xr[u] = *view_at<T>(a.x, b, at, c);
+            sr[u] = *view_at<T>(a.dt, b, at, c);
+            dr[u] = *view_at<T>(a.dy, b, at, c);
+            if (GATED) zr[u] = *view_at<T>(a.z, b, at, c);
+        }
+        const float* k = a.kept + ((uint64_t(b) * keeps + t / S) * a.padded + w.block * NB) * a.channels + c;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) h[0][n] = k[uint64_t(n) * a.channels];
+        SsmRow* row = ssm_row(a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB);
+        // the block's decays and states; behind the sequence's end nothing moves
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            SsmRow* bs = row + uint64_t(u < left ? u : 0) * 2 * a.padded;
+            const bool on = u < left;
+            s[u] = float(sr[u]) + bias;
+            if (soft) s[u] = softplus(s[u]);
+            s[u] = on ? s[u] : 0.f;
+            u_[u] = on && mine ? s[u] * float(xr[u]) : 0.f;
+            r[u] = float(dr[u]);
+            if (GATED) {
+                const float z = float(zr[u]);
+                r[u] *= z * logistic(z);
+            }
+            r[u] = on && mine ? r[u] : 0.f;
+            if (GATED) sum[u] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                e[u][n] = __builtin_amdgcn_exp2f(s[u] * a2[n]);
+                h[u + 1][n] = __builtin_fmaf(e[u][n], h[u][n], u_[u] * bs[n]);
+                if (GATED) sum[u] = __builtin_fmaf(bs[a.padded + n], h[u + 1][n], sum[u]);
+            }
+        }
+        float quad[4];
+#pragma unroll
+        for (int u = S - 1; u >= 0; --u) {
+            SsmRow* bs = row + uint64_t(u < left ? u : 0) * 2 * a.padded;
+            du[u] = ds[u] = 0.f;
+            float v[16];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const float l = __builtin_fmaf(r[u], bs[a.padded + n], f[n]);
+                f[n] = e[u][n] * l;
+                const float q = f[n] * h[u][n];
+                du[u] = __builtin_fmaf(l, bs[n], du[u]);
+                ds[u] = __builtin_fmaf(q, a2[n], ds[u]);
+                da[n] = __builtin_fmaf(q, s[u], da[n]);
+                v[n] = l * u_[u];
+                v[n + 8] = r[u] * h[u + 1][n];
+            }
+            quad[u % 4] = sum_halves(v);
+            if (u % 4 == 0) {
+                const float total = sum_quads(quad[0], quad[1], quad[2], quad[3], w.lane);
+                const int at = u + int(w.lane % 4);
+                if (at < left && w.group < a.groups)
+                    a.part_rows[(((uint64_t(group) * a.batch + b) * a.length + t + at) * 2 + w.lane / 32) * a.padded +
+                                w.block * NB + w.lane / 4 % 8] = total;
+            }
+        }
+        auto finish = [&](int u, float du_, float ds_, float sum_) {
+            const float x = float(xr[u]);
+            const float dx = __builtin_fmaf(du_, s[u], d * r[u]);
+            float dv = __builtin_fmaf(ds_, kLn2, du_ * x);   // the rates were in units of log 2
+            if (soft) dv *= logistic(float(sr[u]) + bias);
+            dd = __builtin_fmaf(r[u], x, dd);
+            dbias += dv;
+            if (!mine) return;
+            *view_at<T>(a.dx, b, t + u, c) = T(dx);
+            *view_at<T>(a.ddt, b, t + u, c) = T(dv);
+            if (GATED) *view_at<T>(a.dz, b, t + u, c) = T(float(dr[u]) * __builtin_fmaf(d, x, sum_) * SsmGate(float(zr[u])).slope);
+        };
+        if (a.blocks == 1) {
+#pragma unroll
+            for (int u = 0; u < S; ++u)
+                if (u < left) finish(u, du[u], ds[u], GATED ? sum[u] : 0.f);
+        } else {
+            float* at = lds + turn * (blockDim.x * V * S);
+#pragma unroll
+            for (int u = 0; u < S; ++u) {
+                at[((wave * V + 0) * S + u) * 64 + w.lane] = du[u];
+                at[((wave * V + 1) * S + u) * 64 + w.lane] = ds[u];
+                if (GATED) at[((wave * V + 2) * S + u) * 64 + w.lane] = sum[u];
+            }
+            __syncthreads();   // the other half is free again: whoever writes it next has passed this
+#pragma unroll
+            for (int u = 0; u < S; ++u) {
+                if (u >= left || u % a.blocks != w.block) continue;
+                float v[3] = {0.f, 0.f, 0.f};
+                for (uint32_t j = 0; j < a.blocks; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] += at[(((first + j) * V + i) * S + u) * 64 + w.lane];
+                finish(u, v[0], v[1], v[2]);
+            }
+        }
+        if (t == w.t0) break;
+    }
+    // sums over the chunk's steps
+    float* part = a.part_a + (uint64_t(b) * a.chunks + w.chunk) * (a.padded + 2) * a.channels + c;
+    if (mine)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) part[uint64_t(w.block * NB + n) * a.channels] = da[n];
+    if (a.blocks > 1) {
+        __syncthreads();
+        lds[(wave * 2 + 0) * 64 + w.lane] = dd;
+        lds[(wave * 2 + 1) * 64 + w.lane] = dbias;
+        __syncthreads();
+        dd = dbias = 0.f;
+        for (uint32_t j = 0; j < a.blocks; ++j) {
+            dd += lds[((first + j) * 2 + 0) * 64 + w.lane];
+            dbias += lds[((first + j) * 2 + 1) * 64 + w.lane];
+        }
+    }
+    if (!mine) return;
+    if (w.block == 0) {
+        part[uint64_t(a.padded) * a.channels] = dd;
+        part[uint64_t(a.padded + 1) * a.channels] = dbias;
+        for (uint64_t t = end > w.t0 ? end : w.t0; t < w.t1; ++t) {
+            *view_at<T>(a.dx, b, t, c) = T(0.f);
+            *view_at<T>(a.ddt, b, t, c) = T(0.f);
+            if (GATED) *view_at<T>(a.dz, b, t, c) = T(0.f);
+        }
+    }
+    if (a.chunks == 1 && a.last != nullptr)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            if (w.block * NB + n < a.states) a.last[(uint64_t(b) * a.channels + c) * a.states + w.block * NB + n] = f[n];
+}
+
+// db and dc: the groups' sums over their channels joined.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ssm_row_grad(SsmArgs a) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t n = uint32_t(i % a.padded), which = uint32_t(i / a.padded) & 1u;
+    const uint64_t row = i / (2 * a.padded), b = row / a.length, t = row % a.length;
+    if (b >= a.batch || n >= a.states) return;
+    float s = 0.f;
+    if (t < steps_of(a.lengths, a.length, uint32_t(b))) {
+        const uint64_t stride = uint64_t(a.batch) * a.length * 2 * a.padded;
+        for (uint32_t g = 0; g < a.groups; ++g) s += a.part_rows[g * stride + i];
+    }
+    *view_at<T>(which ? a.dc : a.db, uint32_t(b), t, n) = T(s);
+}
+
+// da, dd and ddt_bias: the chunks' sums over their steps joined.
+__global__ __launch_bounds__(256) void k_ssm_channel_grad(const float* part, uint32_t rows, uint32_t padded,
+                                                          uint32_t states, uint32_t channels, float* da, float* dd,
+                                                          float* ddt_bias) {
+    __shared__ double sums[16][17];
+    const uint32_t lane = threadIdx.x % 16, sub = threadIdx.x / 16;
+    const uint32_t c = blockIdx.x * 16 + lane, n = blockIdx.y;
+    double s = 0.0;
+    if (c < channels)
+        for (uint32_t i = sub; i < rows; i += 16) s += part[(uint64_t(i) * (padded + 2) + n) * channels + c];
+    sums[sub][lane] = s;
+    __syncthreads();
+    if (sub != 0 || c >= channels) return;
+    for (uint32_t j = 1; j < 16; ++j) s += sums[j][lane];
+    if (n < states) da[uint64_t(c) * states + n] = float(s);
+    else if (n == padded && dd != nullptr) dd[c] = float(s);
+    else if (n == padded + 1 && ddt_bias != nullptr) ddt_bias[c] = float(s);
+}
+
+}  // namespace adacomp

@@ -16,10 +16,13 @@
 #include "views.hpp"
 
 using adacomp::aligned16;
+using adacomp::aligned_to;
 using adacomp::launch_status;
+using adacomp::outputs_clash;
 using adacomp::overlaps;
 using adacomp::Range;
 using adacomp::range_of;
+using adacomp::type_size;
 using adacomp::view_range;
 using adacomp::views_clash;
 
@@ -31,19 +34,6 @@ struct adacomp_optimizer {
 };
 
 namespace {
-
-uint64_t type_size(int type) {
-    return type == ADACOMP_FLOAT ? 4 : type == ADACOMP_BFLOAT || type == ADACOMP_HALF ? 2 : 0;
-}
-bool aligned_to(const void* p, uint64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// No output may share a byte with any other buffer; the first `nout` ranges are outputs.
-bool outputs_clash(const Range* r, int nout, int n) {
-    for (int i = 0; i < nout; ++i)
-        for (int j = i + 1; j < n; ++j)
-            if (overlaps(r[i], r[j])) return true;
-    return false;
-}
 
 int check_device(const adacomp_optimizer* o) {
     int dev = -1;

@@ -534,6 +534,118 @@ int adacomp_gated_scan_backward(const adacomp_scan_shape* shape, const adacomp_v
                                 void* stream);
 int adacomp_gated_scan_workspace_bytes(const adacomp_scan_shape* shape, uint64_t* bytes);
 
+/* Short causal convolution along the sequence, one filter a channel:
+ *   p_t = bias + sum_k weight[k] * x_(t - taps + 1 + k),   t = 0 .. n_b - 1
+ *   y = p, or p / (1 + exp(-p)) with silu
+ * in float32 whatever the type, y rounded once.  x at the taps - 1 steps
+ * before step 0 is `state` (zero without it).  ERR_TOO_LARGE: as for the gated
+ * scan's sizes and strides, or 2^32 work-items and more (one for each 4 steps
+ * of 16 bytes of channels). */
+#define ADACOMP_CONV_MAX_TAPS 8u
+typedef struct adacomp_conv_shape {
+    uint64_t length;      /* steps, n_b <= length; may be 0 */
+    uint32_t batch;       /* sequences; may be 0 */
+    uint32_t channels;    /* >= 1 */
+    uint32_t taps;        /* 1 .. ADACOMP_CONV_MAX_TAPS */
+    int type;             /* element type of x, y, the states and their gradients */
+    int silu;             /* 0 or 1 */
+} adacomp_conv_shape;
+
+/* Forward.
+ *   x          input;  y  output, zero at steps from n_b on.
+ *   weight     [channels, taps] float32;  bias  nullable [channels] float32.
+ *   state      nullable [batch, taps - 1, channels] of the type: the steps before
+ *              step 0, the earliest first.
+ *   state_out  nullable output, the same layout: the last taps - 1 steps before
+ *              step n_b, as the next call's `state`.
+ *   lengths    nullable device int32[batch]: n_b, taken into 0 .. length; what lies at
+ *              steps from n_b on is not used, whatever it holds. */
+int adacomp_causal_conv(const adacomp_conv_shape* shape, const adacomp_view* x,
+                        const float* weight, const float* bias, const adacomp_view* y,
+                        const void* state, void* state_out, const int32_t* lengths, void* stream);
+
+/* Gradients, with g = dy (silu: dy times the derivative at p, which is formed again):
+ *   dx_t = sum_k weight[k] * g_(t + taps - 1 - k),  dstate the same at the steps before step 0
+ *   dweight[k] = sum over sequences and steps of g_t * x_(t - taps + 1 + k),  dbias = sum g
+ * the sums joined in float64 in a fixed order.  state_out has no part in them.
+ *   dx             output, zero at steps from n_b on.
+ *   dweight, dbias float32 outputs; dbias nullable.
+ *   dstate         nullable output of the type.
+ *   ws             16-byte aligned, ws_bytes >= adacomp_causal_conv_workspace_bytes(shape);
+ *                  no initial contents required. */
+int adacomp_causal_conv_backward(const adacomp_conv_shape* shape, const adacomp_view* dy,
+                                 const adacomp_view* x, const float* weight, const float* bias,
+                                 const adacomp_view* dx, float* dweight, float* dbias,
+                                 const void* state, void* dstate, const int32_t* lengths, void* ws,
+                                 uint64_t ws_bytes, void* stream);
+int adacomp_causal_conv_workspace_bytes(const adacomp_conv_shape* shape, uint64_t* bytes);
+
+/* Selective state space scan along the sequence: per sequence and channel, `states`
+ * states h_n that the steps' b and c, shared by the channels, write and read.
+ *   s_t = dt_t + dt_bias, or log(1 + exp(dt_t + dt_bias)) with softplus
+ *   h_n <- exp(s_t * a_n) * h_n + s_t * x_t * b_t,n
+ *   y_t = (sum_n c_t,n * h_n + d * x_t) * (z_t / (1 + exp(-z_t)) with z, else 1)
+ * in float32 whatever the type, y rounded once.  Long sequences are cut into
+ * chunks whose decays exp(a_n * sum s_t) are formed from the sum.
+ * ERR_TOO_LARGE: as for the gated scan's sizes and strides, or states past
+ * ADACOMP_SCAN_MAX_STATES. */
+#define ADACOMP_SCAN_MAX_STATES 64u
+#define ADACOMP_SCAN_KEEP 8u   /* a state of every so many steps is kept for the gradients */
+typedef struct adacomp_ssm_shape {
+    uint64_t length;      /* steps, n_b <= length; may be 0 */
+    uint32_t batch;       /* sequences; may be 0 */
+    uint32_t channels;    /* >= 1 */
+    uint32_t states;      /* 1 .. ADACOMP_SCAN_MAX_STATES */
+    int type;             /* element type of x, dt, b, c, z, y and their gradients */
+    int softplus;         /* 0 or 1 */
+} adacomp_ssm_shape;
+
+/* The inputs of both directions.  b and c are views of [batch, length, states],
+ * the others of [batch, length, channels]. */
+typedef struct adacomp_ssm_inputs {
+    adacomp_view x, dt, b, c;
+    adacomp_view z;          /* data NULL: no gate */
+    const float* a;          /* [channels, states] */
+    const float* d;          /* nullable [channels] (0) */
+    const float* dt_bias;    /* nullable [channels] (0) */
+    const int32_t* lengths;  /* nullable device int32[batch], as for the convolution */
+} adacomp_ssm_inputs;
+
+/* Forward.
+ *   y       output, zero at steps from n_b on.
+ *   h0      nullable [batch, channels, states] float32: the states before step 0 (NULL: 0).
+ *   h_last  nullable float32 output, the same layout: the states after the last step.
+ *   kept    nullable output of adacomp_selective_scan_kept_bytes(shape) bytes, 16-byte
+ *           aligned: the states that the gradients start from.
+ *   ws      16-byte aligned, ws_bytes >= adacomp_selective_scan_workspace_bytes(shape, 0);
+ *           no initial contents required. */
+int adacomp_selective_scan(const adacomp_ssm_shape* shape, const adacomp_ssm_inputs* inputs,
+                           const adacomp_view* y, const float* h0, float* h_last, float* kept,
+                           void* ws, uint64_t ws_bytes, void* stream);
+
+/* Gradients.  dx, ddt (and dz with z) are outputs, zero at steps from n_b on;
+ * db and dc, views like b and c, too.  da [channels, states], dd and ddt_bias
+ * [channels] (nullable) and dh0 [batch, channels, states] (nullable) are float32
+ * outputs.  dh_last: nullable float32 gradient of h_last.  Sums over channels,
+ * sequences and steps are joined in a fixed order, those of a, d and dt_bias in
+ * float64.  ws as above, adacomp_selective_scan_workspace_bytes(shape, 1). */
+typedef struct adacomp_ssm_gradients {
+    adacomp_view dx, ddt, db, dc;
+    adacomp_view dz;         /* data NULL without z */
+    float* da;
+    float* dd;               /* nullable */
+    float* ddt_bias;         /* nullable */
+    float* dh0;              /* nullable */
+} adacomp_ssm_gradients;
+int adacomp_selective_scan_backward(const adacomp_ssm_shape* shape,
+                                    const adacomp_ssm_inputs* inputs, const adacomp_view* dy,
+                                    const float* kept, const float* dh_last,
+                                    const adacomp_ssm_gradients* gradients, void* ws,
+                                    uint64_t ws_bytes, void* stream);
+int adacomp_selective_scan_workspace_bytes(const adacomp_ssm_shape* shape, int backward,
+                                           uint64_t* bytes);
+int adacomp_selective_scan_kept_bytes(const adacomp_ssm_shape* shape, uint64_t* bytes);
+
 const char* adacomp_status_str(int status);
 
 #ifdef __cplusplus
