@@ -133,11 +133,18 @@ class _SsmGradients(ctypes.Structure):
                 [(k, ctypes.c_void_p) for k in ("da", "dd", "ddt_bias", "dh0")])
 
 
+class _Head(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("width", ctypes.c_uint32), ("vocabulary", ctypes.c_uint32),
+                ("type", ctypes.c_int), ("hidden_stride", ctypes.c_uint64), ("weight_stride", ctypes.c_uint64),
+                ("hidden", ctypes.c_void_p), ("weight", ctypes.c_void_p)]
+
+
 # Every exported symbol, with its C signature (argtypes, restype).
 _P = ctypes.c_void_p
 _U32, _U64, _INT, _FLT = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
 _SHAPE, _VIEW = ctypes.POINTER(_ScanShape), ctypes.POINTER(_View)
 _CONV, _SSM = ctypes.POINTER(_ConvShape), ctypes.POINTER(_SsmShape)
+_HEAD = ctypes.POINTER(_Head)
 SIGNATURES = {
     "adacomp_plan_query": ([ctypes.POINTER(_Segment), _U32, ctypes.POINTER(PlanInfo)], _INT),
     "adacomp_plan_create": ([ctypes.POINTER(_Segment), _U32, ctypes.POINTER(_P)], _INT),
@@ -187,6 +194,12 @@ SIGNATURES = {
                                          ctypes.POINTER(_SsmGradients), _P, _U64, _P], _INT),
     "adacomp_selective_scan_workspace_bytes": ([_SSM, _INT, ctypes.POINTER(_U64)], _INT),
     "adacomp_selective_scan_kept_bytes": ([_SSM, ctypes.POINTER(_U64)], _INT),
+    "adacomp_head_workspace_bytes": ([_HEAD, _U32, _INT, ctypes.POINTER(_U64)], _INT),
+    "adacomp_linear_cross_entropy": ([_HEAD, _P, _P, _P, _P, _U64, _P], _INT),
+    "adacomp_linear_cross_entropy_backward": ([_HEAD, _P, _P, _P, _P, _P, _U64, _P, _U64, _P, _U64, _P], _INT),
+    "adacomp_linear_distillation": ([_HEAD, _P, _P, _U32, _FLT, _P, _P, _P, _P, _U64, _P], _INT),
+    "adacomp_linear_distillation_backward": ([_HEAD, _P, _P, _U32, _FLT, _P, _P, _P, _P, _U64, _P, _U64, _P, _U64, _P],
+                                             _INT),
     "adacomp_status_str": ([_INT], ctypes.c_char_p),
 }
 
@@ -676,3 +689,49 @@ def selective_scan_backward(dy, x, dt, a, b, c, states, dx, ddt, da, db, dc, d=N
                                               ddt_bias, dh_last, dh0, lengths, softplus, ws, stream)
     if st:
         raise AdaCompError("adacomp_selective_scan_backward", st)
+
+
+MAX_PICKS = 1024          # most picks of a row of linear_distillation
+
+
+def linear_loss_workspace(rows: int, width: int, vocabulary: int, dtype, backward: bool = False, device="cuda"):
+    """Workspace of linear_cross_entropy and linear_distillation, and (``backward``) of their gradients too, for
+    hidden states and weights of one type."""
+    head = _Head(int(rows), int(width), int(vocabulary), _type(dtype), int(width), int(width), None, None)
+    return _workspace(_bytes("adacomp_head_workspace_bytes", ctypes.byref(head), 1, int(bool(backward))), device)
+
+
+def linear_cross_entropy(hidden, weight, targets, loss, lse, ws, stream=None) -> None:
+    """loss = log sum exp(z) - z[target] of the rows' logits z = hidden weight^T, which are not kept; lse is what the
+    gradients need.  hidden [..., width], weight [vocabulary, width], targets int64, loss and lse float32, one a
+    row.  A row whose target is no word (-100, say) does not count: loss 0."""
+    st = _operators().linear_cross_entropy(hidden, weight, targets, loss, lse, ws, stream)
+    if st:
+        raise AdaCompError("adacomp_linear_cross_entropy", st)
+
+
+def linear_cross_entropy_backward(hidden, weight, targets, loss, lse, dloss, dhidden, dweight, ws, stream=None) -> None:
+    """Gradients of linear_cross_entropy under dloss (float32, one a row); dhidden or dweight may be None."""
+    st = _operators().linear_cross_entropy_backward(hidden, weight, targets, loss, lse, dloss, dhidden, dweight, ws,
+                                                    stream)
+    if st:
+        raise AdaCompError("adacomp_linear_cross_entropy_backward", st)
+
+
+def linear_distillation(hidden, weight, ids, teacher, loss, lse, picked, ws, temperature: float = 1.0,
+                        stream=None) -> None:
+    """loss = sum p (log p - log q) with p the softmax of the teacher's logits of the words ``ids`` and q that of
+    hidden weight^T over the vocabulary, both at ``temperature``.  ids int64 and teacher float32 [rows, picks];
+    loss, lse [rows] and picked [rows, picks] float32 outputs.  Picks that are no word (-1, say) are left out."""
+    st = _operators().linear_distillation(hidden, weight, ids, teacher, loss, lse, picked, ws, temperature, stream)
+    if st:
+        raise AdaCompError("adacomp_linear_distillation", st)
+
+
+def linear_distillation_backward(hidden, weight, ids, teacher, lse, picked, dloss, dhidden, dweight, ws,
+                                 temperature: float = 1.0, stream=None) -> None:
+    """Gradients of linear_distillation under dloss (float32, one a row); dhidden or dweight may be None."""
+    st = _operators().linear_distillation_backward(hidden, weight, ids, teacher, lse, picked, dloss, dhidden, dweight,
+                                                   ws, temperature, stream)
+    if st:
+        raise AdaCompError("adacomp_linear_distillation_backward", st)

@@ -10,7 +10,7 @@ import sysconfig
 import tempfile
 
 HERE = pathlib.Path(__file__).resolve().parent
-SOURCES = [HERE / "csrc" / name for name in ("adacomp.hip", "training.hip", "sequence.hip")]
+SOURCES = [HERE / "csrc" / name for name in ("adacomp.hip", "training.hip", "sequence.hip", "losses.hip")]
 LIB = HERE / "libadacomp.so"
 BINDING = HERE / "_binding.so"
 

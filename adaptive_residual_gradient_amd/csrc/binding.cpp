@@ -531,6 +531,114 @@ int selective_scan_backward(PyObject* const* a) {
     });
 }
 
+// ---- losses over a vocabulary ----
+
+// A matrix whose rows lie at one distance: the last axis, and all axes before it.
+struct Head {
+    adacomp_head head;
+    int64_t rows, width, words;
+    at::ScalarType type;
+    Head(PyObject* hidden, PyObject* weight) {
+        const at::Tensor &th = tensor(hidden, "hidden"), &tw = tensor(weight, "weight");
+        const Rows h(th, "hidden"), w(tw, "weight");
+        if (tw.dim() != 2 || tw.size(1) != th.size(-1) || tw.scalar_type() != th.scalar_type())
+            throw WrongValue("weight must be [vocabulary, width] of the type and width of hidden");
+        rows = int64_t(h.rows);
+        width = th.size(-1);
+        words = tw.size(0);
+        type = th.scalar_type();
+        head = {h.rows, h.cols, uint32_t(std::min<int64_t>(words, 0xFFFFFFFF)), h.type, h.stride, w.stride, h.p, w.p};
+    }
+    // A nullable gradient.
+    void* gradient(PyObject* o, PyObject* like, const char* name, uint64_t& stride) const {
+        stride = uint64_t(width);
+        if (o == Py_None) return nullptr;
+        const Rows r(tensor(o, name), name, tensor(like, name));
+        stride = r.stride;
+        return r.p;
+    }
+};
+
+template <typename T>
+T* of_size(PyObject* o, int64_t n, const char* name, at::ScalarType type) {
+    if (o == Py_None) throw WrongType(std::string(name) + " must be a tensor");
+    return optional<T>(o, n, name, type);
+}
+
+// hidden, weight, targets, loss, lse, ws, stream
+int linear_cross_entropy(PyObject* const* a) {
+    const Head h(a[0], a[1]);
+    const int64_t* targets = of_size<int64_t>(a[2], h.rows, "targets", at::kLong);
+    float *loss = needed(a[3], h.rows, "loss"), *lse = needed(a[4], h.rows, "lse");
+    const Workspace ws(a[5]);
+    void* stream = stream_of(a[6]);
+    return unlocked([&] { return adacomp_linear_cross_entropy(&h.head, targets, loss, lse, ws.p, ws.bytes, stream); });
+}
+
+// hidden, weight, targets, loss, lse, dloss, dhidden, dweight, ws, stream
+int linear_cross_entropy_backward(PyObject* const* a) {
+    const Head h(a[0], a[1]);
+    const int64_t* targets = of_size<int64_t>(a[2], h.rows, "targets", at::kLong);
+    const float *loss = needed(a[3], h.rows, "loss"), *lse = needed(a[4], h.rows, "lse"),
+                *dloss = needed(a[5], h.rows, "dloss");
+    uint64_t hs, ws_stride;
+    void *dhidden = h.gradient(a[6], a[0], "dhidden", hs), *dweight = h.gradient(a[7], a[1], "dweight", ws_stride);
+    const Workspace ws(a[8]);
+    void* stream = stream_of(a[9]);
+    return unlocked([&] {
+        return adacomp_linear_cross_entropy_backward(&h.head, targets, loss, lse, dloss, dhidden, hs, dweight, ws_stride,
+                                                     ws.p, ws.bytes, stream);
+    });
+}
+
+// The picks of a distillation.
+struct Picks {
+    int64_t n;
+    const int64_t* ids;
+    const float* teacher;
+    Picks(const Head& h, PyObject* i, PyObject* t) {
+        const at::Tensor& ti = tensor(i, "ids");
+        if (ti.dim() < 1) throw WrongValue("ids must be [rows, picks]");
+        n = ti.size(-1);
+        if (n > 0xFFFFFFFFll || (n > 0 && ti.numel() / n != h.rows) || n == 0)
+            throw WrongValue("ids must be [rows, picks] of one pick or more");
+        ids = of_size<int64_t>(i, h.rows * n, "ids", at::kLong);
+        teacher = needed(t, h.rows * n, "teacher");
+    }
+};
+
+// hidden, weight, ids, teacher, loss, lse, picked, ws, temperature, stream
+int linear_distillation(PyObject* const* a) {
+    const Head h(a[0], a[1]);
+    const Picks p(h, a[2], a[3]);
+    float *loss = needed(a[4], h.rows, "loss"), *lse = needed(a[5], h.rows, "lse"),
+          *picked = needed(a[6], h.rows * p.n, "picked");
+    const Workspace ws(a[7]);
+    const float temperature = real(a[8]);
+    void* stream = stream_of(a[9]);
+    return unlocked([&] {
+        return adacomp_linear_distillation(&h.head, p.ids, p.teacher, uint32_t(p.n), temperature, loss, lse, picked, ws.p,
+                                           ws.bytes, stream);
+    });
+}
+
+// hidden, weight, ids, teacher, lse, picked, dloss, dhidden, dweight, ws, temperature, stream
+int linear_distillation_backward(PyObject* const* a) {
+    const Head h(a[0], a[1]);
+    const Picks p(h, a[2], a[3]);
+    const float *lse = needed(a[4], h.rows, "lse"), *picked = needed(a[5], h.rows * p.n, "picked"),
+                *dloss = needed(a[6], h.rows, "dloss");
+    uint64_t hs, ws_stride;
+    void *dhidden = h.gradient(a[7], a[0], "dhidden", hs), *dweight = h.gradient(a[8], a[1], "dweight", ws_stride);
+    const Workspace ws(a[9]);
+    const float temperature = real(a[10]);
+    void* stream = stream_of(a[11]);
+    return unlocked([&] {
+        return adacomp_linear_distillation_backward(&h.head, p.ids, p.teacher, uint32_t(p.n), temperature, lse, picked, dloss,
+                                                    dhidden, hs, dweight, ws_stride, ws.p, ws.bytes, stream);
+    });
+}
+
 // No C++ exception leaves an entry point.
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -572,6 +680,10 @@ PyMethodDef methods[] = {
     ENTRY("causal_conv_backward", (entry<causal_conv_backward, 13>)),
     ENTRY("selective_scan", (entry<selective_scan, 16>)),
     ENTRY("selective_scan_backward", (entry<selective_scan_backward, 24>)),
+    ENTRY("linear_cross_entropy", (entry<linear_cross_entropy, 7>)),
+    ENTRY("linear_cross_entropy_backward", (entry<linear_cross_entropy_backward, 10>)),
+    ENTRY("linear_distillation", (entry<linear_distillation, 10>)),
+    ENTRY("linear_distillation_backward", (entry<linear_distillation_backward, 12>)),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,206 @@
+// Tiles of a matrix product on the matrix cores of gfx950: the sum over k of
+// A[m, k] B[n, k] in float32, of bfloat16 or half operands.
+//
+// A workgroup of WM x WN wavefronts forms TM x TN results, a wavefront MT x NT
+// blocks of 32 x 32 of them, in registers.  Steps of 64 of the inner axis lie in
+// two LDS buffers: while one is read, the next step's elements go straight from
+// memory into the other.
+//
+// An operand is read in either order.  K inner (rows of the inner axis): its
+// tile lies in LDS as rows of 64 elements, whose 16-byte pieces change places by
+// the row, so that the 8 lanes of a cycle find 8 different bank groups.  K
+// outer: the tile lies as 64 rows along m (or n), 64-byte pieces change places
+// by the row, and the transposing LDS read hands each lane its 4 elements along k.
+//
+// Wide operands: float32 matrices are split into three bfloat16 planes whose
+// sum they are to 2^-24, and the product is the sum of the six products of
+// planes that are not below that (`planes` = 3).
+#pragma once
+
+#include "elements.hpp"
+
+namespace adacomp {
+
+constexpr uint32_t kTileK = 64;      // the inner axis in LDS
+constexpr int kPlanePairs = 6;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+template <typename E>
+using Eight = E __attribute__((ext_vector_type(8)));
+template <typename E>
+using Four = E __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x16 mfma(Eight<bf16> a, Eight<bf16> b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(Eight<f16> a, Eight<f16> b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+#define ADACOMP_LDS __attribute__((address_space(3)))
+#define ADACOMP_GLOBAL __attribute__((address_space(1)))
+template <typename E>
+__device__ __forceinline__ Four<E> read_transposed(const E* p) {
+    typedef short V __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(Four<E>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ADACOMP_LDS V*)p));
+}
+
+// A matrix, 16-byte aligned, whose lines are 16-byte aligned too.
+struct Operand {
+    const void* p;
+    uint64_t line;      // elements from one line to the next: along m, or along k where K is outer
+    uint64_t plane;     // from one plane to the next
+    uint32_t extent;    // of m, above 0; where K is outer a multiple of 8 within the line
+    uint32_t inner;     // of k; where K is inner, zeros up to a multiple of 8
+};
+
+__device__ __constant__ const uint4 kTileZeros = {0u, 0u, 0u, 0u};
+
+// One operand's tile on its way into LDS.
+template <typename E, bool OUTER, int ROWS, int THREADS>
+struct TileLoader {
+    static constexpr int PIECES = ROWS * kTileK / 8;       // of 16 bytes
+    static constexpr int N = PIECES / THREADS;
+    static constexpr int LINE = (OUTER ? ROWS : kTileK) / 8;   // pieces of a line in LDS
+    static_assert(PIECES % THREADS == 0, "whole turns");
+    uint32_t offset[N];   // bytes from the tile's first element
+    uint32_t k[N];        // the piece's place on the inner axis
+    // Where piece c of a line lies.
+    static __device__ __forceinline__ uint32_t place(uint32_t line, uint32_t c) {
+        if (!OUTER) return c ^ (line & 7u);
+        const uint32_t turn = ROWS >= 256 ? (line & 3u) | (line >> 1 & 4u) : ROWS >= 128 ? line & 3u : line >> 1 & 1u;
+        return c ^ turn << 2;
+    }
+    __device__ __forceinline__ TileLoader(const Operand& x, uint32_t m0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t at = i * THREADS + threadIdx.x, line = at / LINE, c = place(line, at % LINE);   // its own inverse
+            if (OUTER) {
+                // past the last column an earlier one again: nobody looks at the results
+                const uint32_t m = min(m0 + c * 8, x.extent - 8) - m0;
+                offset[i] = (line * uint32_t(x.line) + m) * 2;
+                k[i] = line;
+            } else {
+                const uint32_t m = min(m0 + line, x.extent - 1) - m0;
+                offset[i] = (m * uint32_t(x.line) + c * 8) * 2;
+                k[i] = c * 8;
+            }
+        }
+    }
+    // Step [k0, k0 + 64) of a plane; past the end zeros.
+    __device__ __forceinline__ void request(const Operand& x, uint32_t plane, uint32_t m0, uint32_t k0, uint32_t kend,
+                                            E* tile) const {
+        const E* first = static_cast<const E*>(x.p) + plane * x.plane;
+        first += OUTER ? uint64_t(k0) * x.line + m0 : uint64_t(m0) * x.line + k0;
+        const char* base = reinterpret_cast<const char*>(first);
+        char* to = reinterpret_cast<char*>(tile) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * 1024;
+        const uint32_t end = min(kend, x.inner);
+        const bool whole = k0 + kTileK <= end;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const char* from = base + offset[i];
+            if (!whole) from = k0 + k[i] < end ? from : reinterpret_cast<const char*>(&kTileZeros);
+            __builtin_amdgcn_global_load_lds((ADACOMP_GLOBAL const void*)from, (ADACOMP_LDS void*)(to + i * THREADS * 16),
+                                             16, 0, 0);
+        }
+    }
+    // A wavefront's 32 rows from m on, elements k .. k + 15 of the step.
+    static __device__ __forceinline__ Eight<E> read(const E* tile, uint32_t m, uint32_t k) {
+        const uint32_t lane = threadIdx.x % 64;
+        if (!OUTER) {
+            const uint32_t line = m + lane % 32;
+            return *reinterpret_cast<const Eight<E>*>(tile + line * kTileK + place(line, k / 8 + lane / 32) * 8);
+        }
+        // lanes 16 g .. 16 g + 15: the columns from m + 16 (g % 2) on and k from 8 (g / 2) on, in two halves
+        const uint32_t g = lane / 16, i = lane % 16;
+        const uint32_t column = m + 16 * (g % 2) + i % 4 * 4, line = k + 8 * (g / 2) + i / 4;
+        const Four<E> low = read_transposed(tile + line * ROWS + place(line, column / 8) * 8 + column % 8);
+        const Four<E> high = read_transposed(tile + (line + 4) * ROWS + place(line + 4, column / 8) * 8 + column % 8);
+        return __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+template <typename E_, int WM_, int WN_, int MT_, int NT_, bool AOUTER, bool BOUTER>
+struct TileProduct {
+    typedef E_ E;
+    static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
+    static constexpr int TM = WM * MT * 32, TN = WN * NT * 32, THREADS = WM * WN * 64;
+    typedef TileLoader<E, AOUTER, TM, THREADS> LoadA;
+    typedef TileLoader<E, BOUTER, TN, THREADS> LoadB;
+    static constexpr uint32_t STEP = (TM + TN) * kTileK;   // elements of one buffer
+    static constexpr uint32_t LDS_BYTES = 2 * STEP * 2;
+
+    f32x16 acc[MT][NT];
+    // the wavefront's first row and column of the tile
+    __device__ static __forceinline__ uint32_t wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+    __device__ static __forceinline__ uint32_t row() { return wave() % WM * (MT * 32); }
+    __device__ static __forceinline__ uint32_t column() { return wave() / WM * (NT * 32); }
+    // Row of register i of a block; the lane's column is lane % 32.
+    __device__ static __forceinline__ uint32_t block_row(int i) {
+        return 8 * (i / 4) + i % 4 + 4 * (threadIdx.x % 64 / 32);
+    }
+
+    // The sum over k in [kbegin, kend) of every pair of planes.
+    __device__ __forceinline__ void run(const Operand& a, const Operand& b, uint32_t m0, uint32_t n0, uint32_t kbegin,
+                                        uint32_t kend, uint32_t planes, E* lds) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = 0.f;
+        const LoadA la(a, m0);
+        const LoadB lb(b, n0);
+        const uint32_t steps = (kend - kbegin + kTileK - 1) / kTileK, total = planes == 3 ? steps * kPlanePairs : steps;
+        uint32_t k = kbegin, pair = 0;
+        auto request = [&](E* to) {
+            // smallest products first: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0)
+            const uint32_t pa = planes == 3 ? 0x021010u >> (4 * (5 - pair)) & 3u : 0;
+            const uint32_t pb = planes == 3 ? 0x201100u >> (4 * (5 - pair)) & 3u : 0;
+            la.request(a, pa, m0, k, kend, to);
+            lb.request(b, pb, n0, k, kend, to + TM * kTileK);
+            k += kTileK;
+            if (k >= kend) {
+                k = kbegin;
+                ++pair;
+            }
+        };
+        if (total > 0) request(lds);
+        const uint32_t r = row(), c = column();
+        for (uint32_t step = 0; step < total; ++step) {
+            // this step's elements are there, and the other buffer has been read
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            const E* ta = lds + (step & 1u) * STEP;
+            const E* tb = ta + TM * kTileK;
+            if (step + 1 < total) request(lds + (~step & 1u) * STEP);
+#pragma unroll
+            for (uint32_t kk = 0; kk < kTileK; kk += 16) {
+                Eight<E> av[MT], bv[NT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) av[i] = LoadA::read(ta, r + i * 32, kk);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) bv[j] = LoadB::read(tb, c + j * 32, kk);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[i][j] = mfma(av[i], bv[j], acc[i][j]);
+            }
+        }
+        __syncthreads();   // the buffers are free
+    }
+};
+
+// The tile of a workgroup.  Workgroups go to the 8 chiplets in turn: each chiplet takes a run of
+// neighbouring tiles, 4 along m and then along n, whose operands its cache holds.
+struct TilePlace {
+    uint32_t m, n;
+    __device__ __forceinline__ TilePlace(uint32_t i, uint32_t tiles_m, uint32_t tiles_n) {
+        const uint32_t total = tiles_m * tiles_n, each = total / 8, rest = total % 8;
+        const uint32_t xcd = i % 8;
+        i = xcd * each + min(xcd, rest) + i / 8;
+        constexpr uint32_t G = 4;
+        const uint32_t group = i / (G * tiles_n), high = min(tiles_m - group * G, G), at = i - group * G * tiles_n;
+        m = group * G + at % high;
+        n = at / high;
+    }
+};
+
+}  // namespace adacomp

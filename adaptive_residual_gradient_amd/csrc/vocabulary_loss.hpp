@@ -1,0 +1,418 @@
+// Losses over a large vocabulary straight from the hidden states, and their
+// gradients, for gfx950: z = hidden weight^T / temperature is formed in tiles
+// and never kept.
+//
+//   cross entropy   loss = lse - z_t,                dz_v = exp(z_v - lse) - [v = t]
+//   distillation    loss = sum_k p_k (log p_k - z_k + lse),  p = softmax(teacher / temperature)
+//                   dz_v = exp(z_v - lse) - sum of p_k over the picks k of word v
+//   dhidden = dz weight,  dweight = dz^T hidden
+//
+// Forward is one product: a tile of 256 words leaves each row's largest logit and
+// sum of exponentials (k_logits<false>), which k_loss joins; the logits at the
+// targets or picks are dot products of their own (k_picks).  Backward takes a
+// piece of the vocabulary at a time: the product again, whose tiles leave dz in
+// 16 bits (k_logits<true>), the target's or picks' elements put right from the
+// forward call's float32 values (k_target_grad, k_pick_grad), and the two
+// products from dz (k_product).  A pass is three products for the gradients and
+// one for the loss, bound by the matrix cores.
+//
+// dz is rounded to the operands' 16 bits, as they are, for the matrix cores take no
+// wider ones: each term of the gradients' sums is off by at most half a step
+// of its type.  It is scaled by a power of two that brings the largest row
+// factor up to 2^14: half's smallest numbers would not hold a probability over the number
+// of rows.  float32 calls split every operand, dz too, into three bfloat16
+// planes (tile_product.hpp), and their products are as exact as float32's own.
+#pragma once
+
+#include "sequence.hpp"
+#include "tile_product.hpp"
+
+namespace adacomp {
+
+constexpr uint32_t kLossMaxPicks = 1024;
+
+// Where a matrix of the caller's lies; T elements.
+struct LossMatrix {
+    const void* p;
+    uint64_t stride;
+};
+
+struct LossArgs {
+    LossMatrix hidden, weight;
+    Operand x, w;               // the same as operands, 16-bit
+    const int64_t* ids;         // [rows][picks]; targets: one a row
+    const float* teacher;       // [rows][picks], nullptr: cross entropy
+    float* loss;
+    float* lse;
+    float* picked;              // [rows][picks]: z at the ids
+    const float* dloss;
+    float* factor;              // [rows]: dloss / temperature of the rows that count, times the scale
+    float* scale;               // [2]: the scale and its reciprocal
+    float2* part;               // [tile of the vocabulary][rows]
+    uint32_t rows, width, words, picks;
+    float sharp;                // 1 / temperature
+};
+
+__device__ __forceinline__ bool is_word(int64_t id, uint32_t words) { return uint64_t(id) < words; }
+
+// Whether a row has a word of the vocabulary among its picks.
+__device__ __forceinline__ bool row_counts(const LossArgs& a, uint32_t row) {
+    for (uint32_t k = 0; k < a.picks; ++k)
+        if (is_word(a.ids[uint64_t(row) * a.picks + k], a.words)) return true;
+    return false;
+}
+
+// ---- operands ----
+
+// A matrix as bfloat16 planes or padded rows: to [plane][rows][line], zeros behind the columns and,
+// where `live` says so, in whole rows.
+template <typename T, typename E, int PLANES>
+__global__ __launch_bounds__(256) void k_pack(const T* from, uint64_t stride, uint32_t rows, uint32_t cols, uint32_t line,
+                                              const float* live, E* to) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t per = line / 8;
+    const uint64_t row = i / per;
+    const uint32_t c = uint32_t(i % per) * 8;
+    if (row >= rows) return;
+    FVec<8> v = 0.f;
+    if (live == nullptr || live[row] != 0.f) {
+        const T* p = from + row * stride + c;
+        if (c + 8 <= cols) {
+            v = to_float<8, T>(load_any<8>(p));
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k)
+                if (c + k < cols) v[k] = float(p[k]);
+        }
+    }
+    E* out = to + row * line + c;
+#pragma unroll
+    for (int plane = 0; plane < PLANES; ++plane) {
+        const Eight<E> part = __builtin_convertvector(v, Eight<E>);
+        *reinterpret_cast<Eight<E>*>(out + plane * uint64_t(rows) * line) = part;
+        if (PLANES == 1) break;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float rest = v[k] - float(part[k]);
+            v[k] = __builtin_isfinite(float(part[k])) ? rest : 0.f;   // an infinity is whole in the first plane
+        }
+    }
+}
+
+// ---- forward ----
+
+// The rows' largest logits and sums of exponentials over a tile's words.
+template <typename P>
+__device__ __forceinline__ void leave_sums(const P& p, const LossArgs& a, uint32_t word0, uint32_t m0, uint32_t n0, uint32_t tile,
+                                           float2* lds) {
+    const uint32_t lane = threadIdx.x % 64;
+#pragma unroll
+    for (int j = 0; j < P::NT; ++j) {
+        float most = -__builtin_inff(), sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < P::MT; ++i)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if (word0 + m0 + p.row() + i * 32 + p.block_row(q) < a.words) most = fmaxf(most, p.acc[i][j][q]);
+        // exponentials from a finite number on, also where every logit is -infinity
+        const float from = most == -__builtin_inff() ? 0.f : most * a.sharp;
+#pragma unroll
+        for (int i = 0; i < P::MT; ++i)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                if (word0 + m0 + p.row() + i * 32 + p.block_row(q) < a.words)
+                    sum += __builtin_amdgcn_exp2f((p.acc[i][j][q] * a.sharp - from) * kLog2e);
+        most *= a.sharp;
+        const float other = __shfl_xor(most, 32), theirs = __shfl_xor(sum, 32), top = fmaxf(most, other);
+        const float f0 = top == -__builtin_inff() ? 0.f : top;
+        sum = sum * __builtin_amdgcn_exp2f((most - f0) * kLog2e) + theirs * __builtin_amdgcn_exp2f((other - f0) * kLog2e);
+        if (lane < 32) lds[(p.wave() % P::WM) * P::TN + p.column() + j * 32 + lane] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (uint32_t n = threadIdx.x; n < P::TN; n += P::THREADS) {
+        if (n0 + n >= a.rows) continue;
+        float2 s = lds[n];
+        for (int w = 1; w < P::WM; ++w) {
+            const float2 t = lds[w * P::TN + n];
+            const float top = fmaxf(s.x, t.x), f0 = top == -__builtin_inff() ? 0.f : top;
+            s.y = s.y * __builtin_amdgcn_exp2f((s.x - f0) * kLog2e) + t.y * __builtin_amdgcn_exp2f((t.x - f0) * kLog2e);
+            s.x = top;
+        }
+        a.part[uint64_t(tile) * a.rows + n0 + n] = s;
+    }
+}
+
+// dz of a tile, scaled, into [plane][rows][line]: columns from the piece's first word on, zeros behind the last.
+template <typename P>
+__device__ __forceinline__ void leave_dz(const P& p, const LossArgs& a, uint32_t word0, uint32_t m0, uint32_t n0,
+                                         const Operand& dz, uint32_t planes) {
+    typedef typename P::E E;
+    const uint32_t lane = threadIdx.x % 64;
+#pragma unroll
+    for (int j = 0; j < P::NT; ++j) {
+        const uint32_t row = n0 + p.column() + j * 32 + lane % 32;
+        if (row >= a.rows) continue;
+        const float lse = a.lse[row], f = a.factor[row];
+        E* out = static_cast<E*>(const_cast<void*>(dz.p)) + uint64_t(row) * dz.line;
+#pragma unroll
+        for (int i = 0; i < P::MT; ++i)
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) {
+                const uint32_t m = m0 + p.row() + i * 32 + p.block_row(q);
+                FVec<4> v;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float e = exp_of_minus(__builtin_elementwise_minimum(lse - p.acc[i][j][q + k] * a.sharp, 200.f));
+                    // a row that does not count stays out of it, whatever it holds
+                    v[k] = f != 0.f && word0 + m + k < a.words ? e * f : 0.f;
+                }
+                for (uint32_t plane = 0; plane < planes; ++plane) {
+                    const Four<E> part = __builtin_convertvector(v, Four<E>);
+                    *reinterpret_cast<Four<E>*>(out + plane * dz.plane + m) = part;
+                    v -= __builtin_convertvector(part, FVec<4>);
+                }
+            }
+    }
+}
+
+// A piece of the vocabulary from word0 on; w is its operand.
+template <typename P, bool BACK>
+__global__ __launch_bounds__(P::THREADS) void k_logits(LossArgs a, Operand w, uint32_t word0, uint32_t tiles_m,
+                                                       uint32_t tiles_n, uint32_t planes, Operand dz, uint32_t tile0) {
+    extern __shared__ uint4 lds[];
+    P p;
+    const TilePlace t(blockIdx.x, tiles_m, tiles_n);
+    const uint32_t m0 = t.m * P::TM, n0 = t.n * P::TN;
+    p.run(w, a.x, m0, n0, 0, w.inner, planes, reinterpret_cast<typename P::E*>(lds));
+    if (BACK) leave_dz(p, a, word0, m0, n0, dz, planes);
+    else leave_sums(p, a, word0, m0, n0, tile0 + t.m, reinterpret_cast<float2*>(lds));
+}
+
+// z at the picks: a wavefront a pick.
+template <typename T>
+__global__ __launch_bounds__(256) void k_picks(LossArgs a) {
+    const uint64_t i = uint64_t(blockIdx.x) * 4 + threadIdx.x / 64;
+    if (i >= uint64_t(a.rows) * a.picks) return;
+    const uint32_t lane = threadIdx.x % 64;
+    const int64_t id = a.ids[i];
+    if (!is_word(id, a.words)) {
+        if (lane == 0) a.picked[i] = 0.f;
+        return;
+    }
+    const T* x = static_cast<const T*>(a.hidden.p) + i / a.picks * a.hidden.stride;
+    const T* w = static_cast<const T*>(a.weight.p) + uint64_t(id) * a.weight.stride;
+    constexpr int V = 16 / sizeof(T);
+    float s = 0.f;
+    uint32_t c = lane * V;
+    for (; c + V <= a.width; c += 64 * V) {
+        const FVec<V> u = to_float<V, T>(load_any<V>(x + c)), v = to_float<V, T>(load_any<V>(w + c));
+#pragma unroll
+        for (int k = 0; k < V; ++k) s = __builtin_fmaf(u[k], v[k], s);
+    }
+    for (; c < a.width; ++c) s = __builtin_fmaf(float(x[c]), float(w[c]), s);   // the one lane at the rows' end
+    for (int m = 32; m > 0; m /= 2) s += __shfl_xor(s, m);
+    if (lane == 0) a.picked[i] = s * a.sharp;
+}
+
+// p of a row's picks by one wavefront: the largest teacher logit and the sum of exponentials.
+struct Teacher {
+    float most, sum;
+    __device__ __forceinline__ Teacher(const LossArgs& a, uint32_t row, uint32_t lane) {
+        most = -__builtin_inff();
+        sum = 0.f;
+        const uint64_t first = uint64_t(row) * a.picks;
+        for (uint32_t k = lane; k < a.picks; k += 64)
+            if (is_word(a.ids[first + k], a.words)) most = fmaxf(most, a.teacher[first + k]);
+        for (int m = 32; m > 0; m /= 2) most = fmaxf(most, __shfl_xor(most, m));
+        for (uint32_t k = lane; k < a.picks; k += 64)
+            if (is_word(a.ids[first + k], a.words)) sum += expf((a.teacher[first + k] - most) * a.sharp);
+        for (int m = 32; m > 0; m /= 2) sum += __shfl_xor(sum, m);
+    }
+    __device__ __forceinline__ float log_p(float logit, float sharp) const { return (logit - most) * sharp - logf(sum); }
+};
+
+// A wavefront a row: the tiles' sums joined, and the loss.
+__global__ __launch_bounds__(256) void k_loss(LossArgs a, uint32_t tiles) {
+    const uint32_t row = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
+    if (row >= a.rows) return;
+    float most = -__builtin_inff(), sum = 0.f;
+    auto join = [&](float m, float s) {
+        const float top = fmaxf(most, m), f0 = top == -__builtin_inff() ? 0.f : top;
+        sum = sum * expf(most - f0) + s * expf(m - f0);
+        most = top;
+    };
+    for (uint32_t t = lane; t < tiles; t += 64) {
+        const float2 s = a.part[uint64_t(t) * a.rows + row];
+        join(s.x, s.y);
+    }
+    for (int m = 32; m > 0; m /= 2) join(__shfl_xor(most, m), __shfl_xor(sum, m));
+    const float lse = most + logf(sum);
+    if (lane == 0) a.lse[row] = lse;
+    float loss = 0.f;
+    if (a.teacher == nullptr) {
+        if (is_word(a.ids[row], a.words)) loss = lse - a.picked[row];
+    } else {
+        const Teacher p(a, row, lane);
+        for (uint32_t k = lane; k < a.picks; k += 64) {
+            const uint64_t i = uint64_t(row) * a.picks + k;
+            if (!is_word(a.ids[i], a.words)) continue;
+            const float l = p.log_p(a.teacher[i], a.sharp);
+            if (l > -__builtin_inff()) loss += expf(l) * (l + (lse - a.picked[i]));   // p log p is 0 at p = 0
+        }
+        for (int m = 32; m > 0; m /= 2) loss += __shfl_xor(loss, m);
+    }
+    if (lane == 0) a.loss[row] = loss;
+}
+
+// ---- backward ----
+
+// The scale, a power of two: 2^14 over the largest factor's own, from the rows that count.  One workgroup.
+__global__ __launch_bounds__(1024) void k_loss_scale(LossArgs a) {
+    __shared__ float most[16];
+    float m = 0.f;
+    for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) {
+        const float f = row_counts(a, row) ? a.dloss[row] * a.sharp : 0.f;
+        a.factor[row] = f;
+        m = fmaxf(m, fabsf(f));
+    }
+    for (int s = 32; s > 0; s /= 2) m = fmaxf(m, __shfl_xor(m, s));
+    if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = m;
+    __syncthreads();
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, most[i]);
+    int e = 0;
+    if (m > 0.f && m < __builtin_inff()) e = min(max(14 - ilogbf(m), -100), 100);
+    const float scale = ldexpf(1.f, e);
+    for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) a.factor[row] *= scale;
+    if (threadIdx.x == 0) {
+        a.scale[0] = scale;
+        a.scale[1] = ldexpf(1.f, -e);
+    }
+}
+
+// One element of dz in all planes.
+template <typename E>
+__device__ __forceinline__ void put_dz(const Operand& dz, uint32_t planes, uint32_t row, uint32_t column, float v) {
+    E* out = static_cast<E*>(const_cast<void*>(dz.p)) + uint64_t(row) * dz.line + column;
+    for (uint32_t plane = 0; plane < planes; ++plane) {
+        const E part = E(v);
+        out[plane * dz.plane] = part;
+        v -= float(part);
+    }
+}
+
+// dz at the targets of a piece: exp(z_t - lse) - 1 without the difference of two numbers near 1.
+template <typename E>
+__global__ __launch_bounds__(256) void k_target_grad(LossArgs a, uint32_t word0, uint32_t words, Operand dz, uint32_t planes) {
+    const uint32_t row = blockIdx.x * 256 + threadIdx.x;
+    if (row >= a.rows) return;
+    const int64_t id = a.ids[row];
+    if (!is_word(id, a.words) || uint64_t(id) - word0 >= words || a.factor[row] == 0.f) return;
+    put_dz<E>(dz, planes, row, uint32_t(id) - word0, expm1f(-a.loss[row]) * a.factor[row]);
+}
+
+// dz at the picks of a piece, a wavefront a row.  A word that was picked twice has both its shares of p, from every
+// one of its picks.
+template <typename E>
+__global__ __launch_bounds__(256) void k_pick_grad(LossArgs a, uint32_t word0, uint32_t words, Operand dz, uint32_t planes) {
+    __shared__ int64_t ids[4][kLossMaxPicks];
+    __shared__ float ps[4][kLossMaxPicks];
+    const uint32_t row = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64, w = threadIdx.x / 64;
+    const bool on = row < a.rows && a.factor[row < a.rows ? row : 0] != 0.f;
+    if (on) {
+        const Teacher p(a, row, lane);
+        for (uint32_t k = lane; k < a.picks; k += 64) {
+            const uint64_t i = uint64_t(row) * a.picks + k;
+            ids[w][k] = a.ids[i];
+            ps[w][k] = is_word(a.ids[i], a.words) ? expf(p.log_p(a.teacher[i], a.sharp)) : 0.f;
+        }
+    }
+    __syncthreads();
+    if (!on) return;
+    for (uint32_t k = lane; k < a.picks; k += 64) {
+        const int64_t id = ids[w][k];
+        if (!is_word(id, a.words) || uint64_t(id) - word0 >= words) continue;
+        float p = 0.f;
+        for (uint32_t j = 0; j < a.picks; ++j) p += ids[w][j] == id ? ps[w][j] : 0.f;
+        const float q = expf(a.picked[uint64_t(row) * a.picks + k] - a.lse[row]);
+        put_dz<E>(dz, planes, row, uint32_t(id) - word0, (q - p) * a.factor[row]);
+    }
+}
+
+// What becomes of a product's tile.
+struct ProductOut {
+    void* p;              // [n][m], of T, or float32 partial sums [share][n][m]
+    uint64_t stride;
+    uint32_t rows, cols;  // n and m that are there
+    const float* scale;   // scale[1] is a factor of the result
+    bool add;             // partial sums: to what is there
+};
+
+// One product from dz: [n, m] = sum over k; shares of the inner axis where PARTIAL.
+template <typename P, typename T, bool PARTIAL>
+__global__ __launch_bounds__(P::THREADS) void k_product(Operand x, Operand y, uint32_t inner, uint32_t planes,
+                                                        uint32_t tiles_m, uint32_t tiles_n, uint32_t shares, ProductOut out) {
+    extern __shared__ uint4 lds[];
+    P p;
+    const uint32_t tiles = tiles_m * tiles_n, share = blockIdx.x / tiles;
+    const TilePlace t(blockIdx.x % tiles, tiles_m, tiles_n);
+    const uint32_t m0 = t.m * P::TM, n0 = t.n * P::TN;
+    const uint32_t each = (inner + shares * kTileK - 1) / (shares * kTileK) * kTileK;
+    const uint32_t begin = min(share * each, inner), end = min(begin + each, inner);
+    p.run(x, y, m0, n0, begin, end, planes, reinterpret_cast<typename P::E*>(lds));
+    const float factor = PARTIAL ? 1.f : out.scale[1];
+    const uint32_t lane = threadIdx.x % 64;
+#pragma unroll
+    for (int j = 0; j < P::NT; ++j) {
+        const uint32_t n = n0 + p.column() + j * 32 + lane % 32;
+        if (n >= out.rows) continue;
+        T* row = static_cast<T*>(out.p) + (PARTIAL ? uint64_t(share) * out.rows * out.stride : 0) + n * out.stride;
+#pragma unroll
+        for (int i = 0; i < P::MT; ++i)
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) {
+                const uint32_t m = m0 + p.row() + i * 32 + p.block_row(q);
+                FVec<4> v;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = p.acc[i][j][q + k] * factor;
+                if (m + 4 <= out.cols) {
+                    if (PARTIAL && out.add) v += to_float<4, T>(load_any<4>(row + m));
+                    store_any<4>(row + m, from_float<T, 4>(v));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (m + k < out.cols) row[m + k] = T(PARTIAL && out.add ? v[k] + float(row[m + k]) : v[k]);
+                }
+            }
+    }
+}
+
+// The shares' partial sums joined, scaled and rounded.
+template <typename T>
+__global__ __launch_bounds__(256) void k_join_shares(const float* part, uint32_t shares, uint64_t rows, uint32_t cols,
+                                                     uint32_t line, const float* scale, T* out, uint64_t stride) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t per = line / 4;
+    const uint64_t row = i / per;
+    const uint32_t c = uint32_t(i % per) * 4;
+    if (row >= rows) return;
+    FVec<4> v = 0.f;
+    for (uint32_t s = 0; s < shares; ++s) v += load_any<4>(part + (s * rows + row) * line + c);
+    v *= scale[1];
+    T* to = out + row * stride + c;
+    if (c + 4 <= cols) {
+        store_any<4>(to, from_float<T, 4>(v));
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            if (c + k < cols) to[k] = T(v[k]);
+    }
+}
+
+// A gradient that nothing adds to.
+template <typename T>
+__global__ __launch_bounds__(256) void k_zero_rows(T* out, uint64_t stride, uint64_t rows, uint32_t cols) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i < rows * cols) out[i / cols * stride + i % cols] = T(0.f);
+}
+
+}  // namespace adacomp

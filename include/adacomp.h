@@ -646,6 +646,66 @@ int adacomp_selective_scan_workspace_bytes(const adacomp_ssm_shape* shape, int b
                                            uint64_t* bytes);
 int adacomp_selective_scan_kept_bytes(const adacomp_ssm_shape* shape, uint64_t* bytes);
 
+/* Losses over a vocabulary straight from the hidden states: the logits
+ * z = hidden weight^T are formed in tiles and never kept.  Products of 16-bit
+ * operands are summed in float32; float32 operands are split into three bfloat16
+ * numbers each, which leaves out less than 2^-23 of a product. */
+typedef struct adacomp_head {
+    uint64_t rows;           /* positions; may be 0 */
+    uint32_t width;          /* >= 1 */
+    uint32_t vocabulary;     /* >= 1 */
+    int type;                /* element type of hidden, weight and their gradients */
+    uint64_t hidden_stride;  /* elements from row to row, >= width */
+    uint64_t weight_stride;
+    const void* hidden;      /* [rows, width], aligned to its element */
+    const void* weight;      /* [vocabulary, width], aligned to its element */
+} adacomp_head;
+/* Bytes of ws of the calls below, whatever the strides: of the losses (backward = 0) or of either
+ * direction (1).  hidden and weight are not looked at.  ERR_TOO_LARGE for 2^24 rows, words or strides
+ * and more, a width past 65536 or more than ADACOMP_MAX_PICKS picks. */
+#define ADACOMP_MAX_PICKS 1024u
+int adacomp_head_workspace_bytes(const adacomp_head* head, uint32_t picks, int backward,
+                                 uint64_t* bytes);
+
+/* Softmax cross entropy: lse = log sum_v exp(z_v), loss = lse - z_target.
+ *   targets    device int64[rows]; a row whose target is no word (negative, or past the
+ *              vocabulary) does not count: its loss and gradients are 0.
+ *   loss, lse  [rows] float32 outputs.
+ *   ws         16-byte aligned; no initial contents required. */
+int adacomp_linear_cross_entropy(const adacomp_head* head, const int64_t* targets, float* loss,
+                                 float* lse, void* ws, uint64_t ws_bytes, void* stream);
+
+/* Its gradients, with dz_v = (exp(z_v - lse) - [v = target]) * dloss:
+ *   dhidden = dz weight,  dweight = dz^T hidden
+ * dz rounded once to the type (float32: to 2^-23) after a scaling by a power of two.
+ *   loss, lse  as the forward call wrote them;  dloss  [rows] float32.
+ *   dhidden    nullable [rows, width] output, dhidden_stride elements from row to row.
+ *   dweight    nullable [vocabulary, width] output.
+ * What lies in hidden rows that do not count is not used. */
+int adacomp_linear_cross_entropy_backward(const adacomp_head* head, const int64_t* targets,
+                                          const float* loss, const float* lse, const float* dloss,
+                                          void* dhidden, uint64_t dhidden_stride, void* dweight,
+                                          uint64_t dweight_stride, void* ws, uint64_t ws_bytes,
+                                          void* stream);
+
+/* Distillation from a teacher's top logits, at a temperature > 0: with
+ * p = softmax over the row's picks of teacher / temperature, and z / temperature for z,
+ *   lse = log sum_v exp(z_v),  loss = sum_k p_k * (log p_k - z_(id k) + lse)
+ *   dz_v = (exp(z_v - lse) - sum of the p_k of word v) * dloss / temperature
+ *   ids      device int64[rows, picks]; picks that are no word are left out, and a row without
+ *            any does not count.  A word may be picked more than once.
+ *   teacher  device float32[rows, picks].
+ *   picked   float32[rows, picks] output, z at the ids, for the gradients. */
+int adacomp_linear_distillation(const adacomp_head* head, const int64_t* ids, const float* teacher,
+                                uint32_t picks, float temperature, float* loss, float* lse,
+                                float* picked, void* ws, uint64_t ws_bytes, void* stream);
+int adacomp_linear_distillation_backward(const adacomp_head* head, const int64_t* ids,
+                                         const float* teacher, uint32_t picks, float temperature,
+                                         const float* lse, const float* picked, const float* dloss,
+                                         void* dhidden, uint64_t dhidden_stride, void* dweight,
+                                         uint64_t dweight_stride, void* ws, uint64_t ws_bytes,
+                                         void* stream);
+
 const char* adacomp_status_str(int status);
 
 #ifdef __cplusplus
