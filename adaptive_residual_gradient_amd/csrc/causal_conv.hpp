@@ -21,8 +21,10 @@ namespace adacomp {
 constexpr uint32_t kConvRows = 16, kConvFewRows = 4;
 constexpr uint32_t kConvThreads = 256;
 constexpr uint32_t kConvMaxPartials = 256;   // partial rows of the weight's gradient
-// A thread's channels: 16 bytes; 8 backward with more than 4 taps, whose windows and sums would not fit.
-constexpr uint32_t conv_bytes(bool back, uint32_t taps) { return back && taps > 4 ? 8 : 16; }
+// The filters that kernels are made for: 2, 3 and 4 taps; 8, for every other number too.
+constexpr uint32_t conv_kernel_taps(uint32_t taps) { return taps >= 2 && taps <= 4 ? taps : 8; }
+// A thread's channels: 16 bytes; 8 backward with 8 taps, whose windows and sums would not fit.
+constexpr uint32_t conv_bytes(bool back, uint32_t taps) { return back && conv_kernel_taps(taps) == 8 ? 8 : 16; }
 
 struct ConvArgs {
     ScanView x, y, dy, dx;

@@ -117,7 +117,7 @@ void launch_conv(ConvArgs a, bool silu, hipStream_t s) {
 
 template <typename T, int VW>
 void launch_conv_taps(const ConvArgs& a, bool silu, hipStream_t s) {
-    switch (a.taps) {
+    switch (conv_kernel_taps(a.taps)) {
         case 2: return launch_conv<T, VW, 2>(a, silu, s);
         case 3: return launch_conv<T, VW, 3>(a, silu, s);
         case 4: return launch_conv<T, VW, 4>(a, silu, s);
@@ -134,7 +134,7 @@ void launch_conv_back(const ConvArgs& a, const ConvBackLayout& l, uint32_t vec, 
         if (vec == 1) hipLaunchKernelGGL((k_conv_backward<T, 1, KT>), grid, block, 0, s, a, silu); \
         else hipLaunchKernelGGL((k_conv_backward<T, VW, KT>), grid, block, 0, s, a, silu);         \
     } while (0)
-    switch (a.taps) {
+    switch (conv_kernel_taps(a.taps)) {
         case 2: ADACOMP_CONV_BACK(V, 2); break;
         case 3: ADACOMP_CONV_BACK(V, 3); break;
         case 4: ADACOMP_CONV_BACK(V, 4); break;
