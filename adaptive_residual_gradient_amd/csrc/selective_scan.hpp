@@ -33,7 +33,7 @@ namespace adacomp {
 
 constexpr uint32_t kSsmKeep = 8;        // steps from one kept state to the next; also a block of the kernels
 constexpr uint32_t kSsmBlock = 16;      // states of a wavefront forward (8 where there are no more)
-constexpr uint32_t kSsmBackBlock = 8;   // and backward
+constexpr uint32_t kSsmBackBlock = 4;   // and backward
 constexpr uint32_t kSsmShort = 8;       // longest sequence of the short kernel
 
 struct SsmArgs {
@@ -49,6 +49,7 @@ struct SsmArgs {
     float* rows;             // [batch][length][2][padded]: b and c
     float* ends;             // [batch][chunk][padded][channels]: a chunk's end from 0, then what is carried in
     float* sums;             // [batch][chunk][channels]: sum of s
+    float* steps_of;         // [batch][length][channels]: s, where the sequence is in chunks
     float* part_rows;        // [group of 64 channels][batch][length][2][padded]: db and dc
     float* part_a;           // [batch][chunk][padded + 2][channels]: da, dd, ddt_bias
     uint64_t length;
@@ -56,6 +57,11 @@ struct SsmArgs {
     uint32_t chunks, steps;                     // steps a chunk, a multiple of 8
     uint32_t groups, blocks;                    // wavefronts that cover the channels, and the states
     bool softplus;
+};
+
+template <int N>
+struct Const {
+    static constexpr int value = N;
 };
 
 // log(1 + exp(v)).
@@ -90,10 +96,12 @@ __global__ __launch_bounds__(256) void k_ssm_rows(SsmArgs a) {
 // A wavefront's place in its workgroup, as a number that all its lanes share.
 __device__ __forceinline__ uint32_t wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
-// b and c are the same for all lanes and are not written while a kernel reads them: scalar loads.
-typedef const float __attribute__((address_space(4))) SsmRow;
-__device__ __forceinline__ SsmRow* ssm_row(const float* p) {
-    return reinterpret_cast<SsmRow*>(reinterpret_cast<uintptr_t>(p));
+// b and c are the same for all lanes and are not written while a kernel reads them: scalar loads, of a
+// whole block of states.
+template <int NB>
+__device__ __forceinline__ FVec<NB> ssm_row(const float* p) {
+    typedef const FVec<NB> __attribute__((address_space(4))) Row;
+    return *reinterpret_cast<Row*>(reinterpret_cast<uintptr_t>(p));
 }
 
 // The place of a wavefront.
@@ -126,13 +134,29 @@ __device__ __forceinline__ void ssm_rates(const SsmArgs& a, const SsmPlace& w, f
     }
 }
 
-// Forward.  ENDS: only the states at the chunk's end, from 0.
-template <typename T, int NB, bool ENDS>
+// A sequence's rows of a view, for lanes that each have one channel: a row's address is the same for all
+// lanes, a channel's a 32-bit offset from it.
+template <typename T>
+struct SsmRows {
+    char* p;          // step 0's row
+    uint64_t step;    // bytes
+    __device__ __forceinline__ SsmRows(const ScanView& v, uint32_t b)
+        : p(static_cast<char*>(v.p) + uint64_t(b) * v.bs * sizeof(T)), step(v.ts * sizeof(T)) {}
+    __device__ __forceinline__ T& at(uint64_t t, uint32_t offset) const {
+        return *reinterpret_cast<T*>(p + t * step + offset);
+    }
+};
+
+// Forward.  kSsmEnds: only the states at the chunk's end, from 0, and s, which kSsmChunks takes; kSsmWhole:
+// sequences of one chunk.
+constexpr int kSsmEnds = 0, kSsmChunks = 1, kSsmWhole = 2;
+template <typename T, int NB, int MODE, bool GATED>
 __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
     constexpr int S = kSsmKeep;
+    constexpr bool ENDS = MODE == kSsmEnds, FORMED = MODE == kSsmChunks;
     extern __shared__ float lds[];   // [2][wavefront][S][64], where a channel's states are several blocks
     const SsmPlace w(a);
-    const uint32_t c = w.c, b = w.b;
+    const uint32_t c = w.c, b = w.b, off = c * uint32_t(sizeof(T)), wave = wave_of(), first = wave - w.block;
     const bool mine = w.group < a.groups;
     float a2[NB], h[NB], total = 0.f;
     ssm_rates<NB>(a, w, a2);
@@ -143,75 +167,89 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
         h[n] = 0.f;
         const uint32_t at = w.block * NB + n;
         if (ENDS) continue;
-        if (a.chunks > 1) {
+        if (FORMED) {
             h[n] = a.ends[ends + uint64_t(n) * a.channels];
         } else if (a.h0 != nullptr && at < a.states) {
             h[n] = a.h0[(uint64_t(b) * a.channels + c) * a.states + at];
         }
     }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, d = a.d ? a.d[c] : 0.f;
-    const bool gated = a.z.p != nullptr, soft = a.softplus;
+    const bool soft = a.softplus, keep = !ENDS && a.kept != nullptr && mine;
+    const SsmRows<T> xs(a.x, b), ds(a.dt, b), zs(a.z, b), ys(a.y, b);
+    const uint64_t keeps = (a.length + S - 1) / S;
     uint32_t turn = 0;
-    for (uint64_t t = w.t0; t < end; t += S, turn ^= 1u) {
-        const int left = end - t < uint64_t(S) ? int(end - t) : S;
-        T xr[S], sr[S], zr[S];
+    // U steps from t on
+    auto steps = [&](uint64_t t, auto count) {
+        constexpr int U = decltype(count)::value;
+        T xr[U], zr[U];
+        float s[U], y[U];
+        float* sp = a.steps_of + (uint64_t(b) * a.length + t) * a.channels;
 #pragma unroll
-        for (int u = 0; u < S; ++u) {
-            const uint64_t at = u < left ? t + u : end - 1;
-            xr[u] = *view_at<T>(a.x, b, at, c);
-            sr[u] = *view_at<T>(a.dt, b, at, c);
-            if (!ENDS && gated) zr[u] = *view_at<T>(a.z, b, at, c);
+        for (int u = 0; u < U; ++u) {
+            xr[u] = xs.at(t + u, off);
+            if (FORMED) s[u] = sp[uint64_t(u) * a.channels + c];
+            else s[u] = float(ds.at(t + u, off));
+            if (!ENDS && GATED) zr[u] = zs.at(t + u, off);
         }
-        if (!ENDS && a.kept != nullptr && mine) {
-            float* k = a.kept + ((uint64_t(b) * ((a.length + S - 1) / S) + t / S) * a.padded + w.block * NB) * a.channels + c;
+        if (keep && t % S == 0) {
+            float* k = a.kept + ((uint64_t(b) * keeps + t / S) * a.padded + w.block * NB) * a.channels;
 #pragma unroll
-            for (int n = 0; n < NB; ++n) k[uint64_t(n) * a.channels] = h[n];
+            for (int n = 0; n < NB; ++n) k[uint64_t(n) * a.channels + c] = h[n];
         }
-        float y[S];
-        SsmRow* row = ssm_row(a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB);
+        const float* row = a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB;
 #pragma unroll
-        for (int u = 0; u < S; ++u) {
+        for (int u = 0; u < U; ++u) {
             y[u] = 0.f;
-            if (u >= left) continue;
-            SsmRow* bs = row + uint64_t(u) * 2 * a.padded;
-            float s = float(sr[u]) + bias;
-            if (soft) s = softplus(s);
-            const float v = s * float(xr[u]);
-            if (ENDS) total += s;
+            const FVec<NB> bs = ssm_row<NB>(row + uint64_t(u) * 2 * a.padded);
+            FVec<NB> cs;
+            if (!ENDS) cs = ssm_row<NB>(row + (uint64_t(u) * 2 + 1) * a.padded);
+            if (!FORMED) {
+                s[u] += bias;
+                const float p = softplus(s[u]);
+                s[u] = soft ? p : s[u];
+                if (ENDS) {
+                    total += s[u];
+                    if (w.block == 0 && mine) sp[uint64_t(u) * a.channels + c] = s[u];
+                }
+            }
+            const float v = s[u] * float(xr[u]);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * a2[n]), h[n], v * bs[n]);
-                if (!ENDS) y[u] = __builtin_fmaf(bs[a.padded + n], h[n], y[u]);
+                h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[u] * a2[n]), h[n], v * bs[n]);
+                if (!ENDS) y[u] = __builtin_fmaf(cs[n], h[n], y[u]);
             }
+            __builtin_amdgcn_sched_barrier(0);   // or the rows of all steps are requested at once and spilled
         }
-        if (ENDS) continue;
+        if (ENDS) return;
         auto finish = [&](int u, float sum) {
             sum = __builtin_fmaf(d, float(xr[u]), sum);
-            if (gated) {
+            if (GATED) {
                 const float z = float(zr[u]);
                 sum *= z * logistic(z);
             }
-            if (mine) *view_at<T>(a.y, b, t + u, c) = T(sum);
+            if (mine) ys.at(t + u, off) = T(sum);
         };
         if (a.blocks == 1) {
 #pragma unroll
-            for (int u = 0; u < S; ++u)
-                if (u < left) finish(u, y[u]);
+            for (int u = 0; u < U; ++u) finish(u, y[u]);
         } else {
             float* at = lds + turn * blockDim.x * S;
-            const uint32_t wave = wave_of(), first = wave - w.block;
+            turn ^= 1u;
 #pragma unroll
-            for (int u = 0; u < S; ++u) at[(wave * S + u) * 64 + w.lane] = y[u];
+            for (int u = 0; u < U; ++u) at[(wave * S + u) * 64 + w.lane] = y[u];
             __syncthreads();   // the other half is free again: whoever writes it next has passed this
 #pragma unroll
-            for (int u = 0; u < S; ++u) {
-                if (u >= left || u % a.blocks != w.block) continue;
+            for (int u = 0; u < U; ++u) {
+                if (u % a.blocks != w.block) continue;
                 float sum = 0.f;
                 for (uint32_t j = 0; j < a.blocks; ++j) sum += at[((first + j) * S + u) * 64 + w.lane];
                 finish(u, sum);
             }
         }
-    }
+    };
+    uint64_t t = w.t0;
+    for (; t + S <= end; t += S) steps(t, Const<S>{});
+    for (; t < end; ++t) steps(t, Const<1>{});
     if (!mine) return;
     if (ENDS) {
 #pragma unroll
@@ -219,12 +257,12 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
         if (w.block == 0) a.sums[(uint64_t(b) * a.chunks + w.chunk) * a.channels + c] = total;
         return;
     }
-    if (a.chunks == 1 && a.last != nullptr)
+    if (!FORMED && a.last != nullptr)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
             if (w.block * NB + n < a.states) a.last[(uint64_t(b) * a.channels + c) * a.states + w.block * NB + n] = h[n];
     if (w.block == 0)
-        for (uint64_t t = end > w.t0 ? end : w.t0; t < w.t1; ++t) *view_at<T>(a.y, b, t, c) = T(0.f);
+        for (t = end > w.t0 ? end : w.t0; t < w.t1; ++t) ys.at(t, off) = T(0.f);
 }
 
 // What is carried into each chunk takes the place of its end from 0; backward
@@ -333,59 +371,52 @@ __global__ __launch_bounds__(256) void k_ssm_short(SsmArgs a, uint32_t quads) {
 
 // ---- backward ----
 
-// r = dy silu(z), and what dz needs.
-struct SsmGate {
-    float gate = 1.f, slope = 0.f;   // silu(z) and its derivative
-    __device__ __forceinline__ SsmGate() {}
-    __device__ __forceinline__ explicit SsmGate(float z) {
-        const float q = logistic(z);
-        gate = z * q;
-        slope = __builtin_fmaf(gate, 1.f - q, q);
-    }
-};
-
 // f at each chunk's first step from 0 at its end, and the sum of s.
-template <typename T, int NB>
+template <typename T, int NB, bool GATED>
 __global__ __launch_bounds__(256) void k_ssm_back_ends(SsmArgs a) {
     constexpr int S = kSsmKeep;
     const SsmPlace w(a);
     if (w.group >= a.groups) return;
-    const uint32_t c = w.c, b = w.b;
+    const uint32_t c = w.c, b = w.b, off = c * uint32_t(sizeof(T));
     float a2[NB], f[NB], total = 0.f;
     ssm_rates<NB>(a, w, a2);
 #pragma unroll
     for (int n = 0; n < NB; ++n) f[n] = 0.f;
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-    const bool gated = a.z.p != nullptr, soft = a.softplus;
+    const bool soft = a.softplus;
     const uint64_t end = w.t1 < w.n ? w.t1 : w.n;
-    for (uint64_t t = end; t > w.t0;) {
-        const int left = t - w.t0 < uint64_t(S) ? int(t - w.t0) : S;
-        T dr[S], sr[S], zr[S];
+    const SsmRows<T> rs(a.dy, b), ds(a.dt, b), zs(a.z, b);
+    // U steps from t on, the last one first
+    auto steps = [&](uint64_t t, auto count) {
+        constexpr int U = decltype(count)::value;
+        T rr[U], sr[U], zr[U];
 #pragma unroll
-        for (int u = 0; u < S; ++u) {
-            const uint64_t at = u < left ? t - 1 - u : w.t0;
-            dr[u] = *view_at<T>(a.dy, b, at, c);
-            sr[u] = *view_at<T>(a.dt, b, at, c);
-            if (gated) zr[u] = *view_at<T>(a.z, b, at, c);
+        for (int u = 0; u < U; ++u) {
+            rr[u] = rs.at(t + u, off);
+            sr[u] = ds.at(t + u, off);
+            if (GATED) zr[u] = zs.at(t + u, off);
         }
-        t -= uint32_t(left);
-        SsmRow* row = ssm_row(a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + a.padded + w.block * NB);
+        const float* row = a.rows + ((uint64_t(b) * a.length + t) * 2 + 1) * a.padded + w.block * NB;
 #pragma unroll
-        for (int u = 0; u < S; ++u) {
-            if (u >= left) continue;
-            SsmRow* cs = row + uint64_t(left - 1 - u) * 2 * a.padded;
-            float s = float(sr[u]) + bias;
-            if (soft) s = softplus(s);
+        for (int u = U - 1; u >= 0; --u) {
+            const FVec<NB> cs = ssm_row<NB>(row + uint64_t(u) * 2 * a.padded);
+            const float v = float(sr[u]) + bias, p = softplus(v), s = soft ? p : v;
             total += s;
-            float r = float(dr[u]);
-            if (gated) {
+            float r = float(rr[u]);
+            if (GATED) {
                 const float z = float(zr[u]);
                 r *= z * logistic(z);
             }
 #pragma unroll
             for (int n = 0; n < NB; ++n)
                 f[n] = __builtin_amdgcn_exp2f(s * a2[n]) * __builtin_fmaf(r, cs[n], f[n]);
+            __builtin_amdgcn_sched_barrier(0);   // or the rows of all steps are requested at once and spilled
         }
+    };
+    if (w.t0 < end) {
+        uint64_t t = end;
+        while ((t - w.t0) % S != 0) steps(--t, Const<1>{});
+        while (t > w.t0) steps(t -= S, Const<S>{});
     }
     const uint64_t ends = ((uint64_t(b) * a.chunks + w.chunk) * a.padded + w.block * NB) * a.channels + c;
 #pragma unroll
@@ -393,10 +424,6 @@ __global__ __launch_bounds__(256) void k_ssm_back_ends(SsmArgs a) {
     if (w.block == 0) a.sums[(uint64_t(b) * a.chunks + w.chunk) * a.channels + c] = total;
 }
 
-template <int N>
-struct Const {
-    static constexpr int value = N;
-};
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
     return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false));
@@ -448,15 +475,19 @@ __device__ __forceinline__ float sum_quads(float v0, float v1, float v2, float v
     return (odd ? b : a) + swap1(odd ? a : b);
 }
 
-template <typename T, bool GATED>
-__global__ __launch_bounds__(512) void k_ssm_backward(SsmArgs a) {
+// A workgroup is 64 channels, a wavefront kSsmBackBlock of their states.  Of a block of 8 steps each
+// wavefront prepares OWN (s, u and r, which all of them take from LDS) and finishes the same ones, from the sums
+// over the wavefronts of du, ds and s that lie in LDS then.
+template <typename T, int OWN, bool GATED>
+__global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs a) {
     constexpr int S = kSsmKeep, NB = kSsmBackBlock, V = GATED ? 3 : 2;
-    extern __shared__ float lds[];   // [2][wavefront][V][S][64], where a channel's states are several blocks
+    extern __shared__ float lds[];   // [3][S][64]: s, u, r;  [wavefront][V][S][64]: du, ds, sum
+    float* const ready = lds;
+    float* const parts = lds + 3 * S * 64;
     const SsmPlace w(a);
-    const uint32_t c = w.c, b = w.b, wave = wave_of(), first = wave - w.block;
+    const uint32_t c = w.c, b = w.b, off = c * uint32_t(sizeof(T)), lane = w.lane;
     // a lane past the last channel goes along with it, without a part in the sums over channels
-    const bool mine = w.group < a.groups && w.group * 64 + w.lane < a.channels;
-    const uint32_t group = w.group < a.groups ? w.group : a.groups - 1;
+    const bool mine = w.group * 64 + lane < a.channels;
     float a2[NB], f[NB], da[NB], dd = 0.f, dbias = 0.f;
     ssm_rates<NB>(a, w, a2);
     const uint64_t ends = ((uint64_t(b) * a.chunks + w.chunk) * a.padded + w.block * NB) * a.channels + c;
@@ -470,106 +501,108 @@ __global__ __launch_bounds__(512) void k_ssm_backward(SsmArgs a) {
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, d = a.d ? a.d[c] : 0.f;
     const bool soft = a.softplus;
     const uint64_t end = w.t1 < w.n ? w.t1 : w.n, keeps = (a.length + S - 1) / S;
-    uint32_t turn = 0;
-    for (uint64_t t = w.t0 < end ? (end - 1) / S * S : 0; w.t0 < end; t -= S, turn ^= 1u) {
-        const int left = end - t < uint64_t(S) ? int(end - t) : S;
-        T xr[S], sr[S], dr[S], zr[S];
-        float h[S + 1][NB], e[S][NB], s[S], u_[S], r[S], du[S], ds[S], sum[S];
+    const SsmRows<T> xs(a.x, b), ss(a.dt, b), rs(a.dy, b), zs(a.z, b), dxs(a.dx, b), dss(a.ddt, b), dzs(a.dz, b);
+    for (uint64_t t = w.t0 < end ? (end - 1) / S * S : 0; w.t0 < end; t -= S) {
+        const uint32_t left = end - t < uint64_t(S) ? uint32_t(end - t) : uint32_t(S);
+        // what the wavefront keeps of its own steps
+        float x[OWN], s[OWN], r[OWN], slope[OWN], back[OWN];
+        T xr[OWN], sr[OWN], rr[OWN], zr[OWN];
+        const float* k = a.kept + ((uint64_t(b) * keeps + t / S) * a.padded + w.block * NB) * a.channels;
+        float h[S + 1][NB], e[S][NB];
 #pragma unroll
-        for (int u = 0; u < S; ++u) {
-            const uint64_t at = u < left ? t + u : end - 1;
-            xr[u] = *view_at<T>(a.x, b, at, c);
-            sr[u] = *view_at<T>(a.dt, b, at, c);
-            dr[u] = *view_at<T>(a.dy, b, at, c);
-            if (GATED) zr[u] = *view_at<T>(a.z, b, at, c);
+        for (int i = 0; i < OWN; ++i) {   // past the end the last step again
+            const uint32_t u = min(w.block + a.blocks * i, left - 1);
+            xr[i] = xs.at(t + u, off);
+            sr[i] = ss.at(t + u, off);
+            rr[i] = rs.at(t + u, off);
+            if (GATED) zr[i] = zs.at(t + u, off);
         }
-        const float* k = a.kept + ((uint64_t(b) * keeps + t / S) * a.padded + w.block * NB) * a.channels + c;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) h[0][n] = k[uint64_t(n) * a.channels];
-        SsmRow* row = ssm_row(a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB);
-        // the block's decays and states; behind the sequence's end nothing moves
+        for (int n = 0; n < NB; ++n) h[0][n] = k[uint64_t(n) * a.channels + c];
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const uint32_t u = w.block + a.blocks * i;
+            x[i] = float(xr[i]);
+            const float v = float(sr[i]) + bias, p = softplus(v);
+            s[i] = soft ? p : v;
+            slope[i] = soft ? logistic(v) : 1.f;
+            r[i] = float(rr[i]);
+            if (GATED) {
+                const float z = float(zr[i]), q = logistic(z), g = z * q;
+                back[i] = r[i] * __builtin_fmaf(g, 1.f - q, q);
+                r[i] *= g;
+            }
+            if (u < S) {   // behind the sequence's end nothing moves
+                const bool on = u < left;
+                ready[u * 64 + lane] = on ? s[i] : 0.f;
+                ready[(S + u) * 64 + lane] = on && mine ? s[i] * x[i] : 0.f;
+                ready[(2 * S + u) * 64 + lane] = on && mine ? r[i] : 0.f;
+            }
+        }
+        __syncthreads();
+        // the block's decays and states
+        const float* row = a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB;
+        float* part = parts + (w.block * V * S) * 64 + lane;
 #pragma unroll
         for (int u = 0; u < S; ++u) {
-            SsmRow* bs = row + uint64_t(u < left ? u : 0) * 2 * a.padded;
-            const bool on = u < left;
-            s[u] = float(sr[u]) + bias;
-            if (soft) s[u] = softplus(s[u]);
-            s[u] = on ? s[u] : 0.f;
-            u_[u] = on && mine ? s[u] * float(xr[u]) : 0.f;
-            r[u] = float(dr[u]);
-            if (GATED) {
-                const float z = float(zr[u]);
-                r[u] *= z * logistic(z);
-            }
-            r[u] = on && mine ? r[u] : 0.f;
-            if (GATED) sum[u] = 0.f;
+            const float* at = row + uint64_t(uint32_t(u) < left ? u : 0) * 2 * a.padded;
+            const FVec<NB> bs = ssm_row<NB>(at), cs = ssm_row<NB>(at + a.padded);
+            const float step = ready[u * 64 + lane], in = ready[(S + u) * 64 + lane];
+            float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                e[u][n] = __builtin_amdgcn_exp2f(s[u] * a2[n]);
-                h[u + 1][n] = __builtin_fmaf(e[u][n], h[u][n], u_[u] * bs[n]);
-                if (GATED) sum[u] = __builtin_fmaf(bs[a.padded + n], h[u + 1][n], sum[u]);
+                e[u][n] = __builtin_amdgcn_exp2f(step * a2[n]);
+                h[u + 1][n] = __builtin_fmaf(e[u][n], h[u][n], in * bs[n]);
+                if (GATED) sum = __builtin_fmaf(cs[n], h[u + 1][n], sum);
             }
+            if (GATED) part[(2 * S + u) * 64] = sum;
         }
-        float quad[4];
+        float v[16], quad[S / 2];
 #pragma unroll
         for (int u = S - 1; u >= 0; --u) {
-            SsmRow* bs = row + uint64_t(u < left ? u : 0) * 2 * a.padded;
-            du[u] = ds[u] = 0.f;
-            float v[16];
+            const float* at = row + uint64_t(uint32_t(u) < left ? u : 0) * 2 * a.padded;
+            const FVec<NB> bs = ssm_row<NB>(at), cs = ssm_row<NB>(at + a.padded);
+            const float step = ready[u * 64 + lane], in = ready[(S + u) * 64 + lane], out = ready[(2 * S + u) * 64 + lane];
+            float du = 0.f, ds = 0.f;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const float l = __builtin_fmaf(r[u], bs[a.padded + n], f[n]);
+                const float l = __builtin_fmaf(out, cs[n], f[n]);
                 f[n] = e[u][n] * l;
                 const float q = f[n] * h[u][n];
-                du[u] = __builtin_fmaf(l, bs[n], du[u]);
-                ds[u] = __builtin_fmaf(q, a2[n], ds[u]);
-                da[n] = __builtin_fmaf(q, s[u], da[n]);
-                v[n] = l * u_[u];
-                v[n + 8] = r[u] * h[u + 1][n];
+                du = __builtin_fmaf(l, bs[n], du);
+                ds = __builtin_fmaf(q, a2[n], ds);
+                da[n] = __builtin_fmaf(q, step, da[n]);
+                v[u % 2 * 4 + n] = l * in;
+                v[8 + u % 2 * 4 + n] = out * h[u + 1][n];
             }
-            quad[u % 4] = sum_halves(v);
-            if (u % 4 == 0) {
-                const float total = sum_quads(quad[0], quad[1], quad[2], quad[3], w.lane);
-                const int at = u + int(w.lane % 4);
-                if (at < left && w.group < a.groups)
-                    a.part_rows[(((uint64_t(group) * a.batch + b) * a.length + t + at) * 2 + w.lane / 32) * a.padded +
-                                w.block * NB + w.lane / 4 % 8] = total;
-            }
+            part[u * 64] = du;
+            part[(S + u) * 64] = ds;
+            if (u % 2 == 0) quad[u / 2] = sum_halves(v);
         }
-        auto finish = [&](int u, float du_, float ds_, float sum_) {
-            const float x = float(xr[u]);
-            const float dx = __builtin_fmaf(du_, s[u], d * r[u]);
-            float dv = __builtin_fmaf(ds_, kLn2, du_ * x);   // the rates were in units of log 2
-            if (soft) dv *= logistic(float(sr[u]) + bias);
-            dd = __builtin_fmaf(r[u], x, dd);
+        {   // lane l has the sum of step 2 (l % 4) + l / 16 % 2, state l / 4 % 4, of b or (from lane 32 on) of c
+            const float total = sum_quads(quad[0], quad[1], quad[2], quad[3], lane);
+            const uint32_t u = 2 * (lane % 4) + lane / 16 % 2;
+            if (u < left)
+                a.part_rows[(((uint64_t(w.group) * a.batch + b) * a.length + t + u) * 2 + lane / 32) * a.padded +
+                            w.block * NB + lane / 4 % 4] = total;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const uint32_t u = w.block + a.blocks * i;
+            if (u >= left) continue;
+            float sums[V] = {};
+            for (uint32_t j = 0; j < a.blocks; ++j)
+#pragma unroll
+                for (int q = 0; q < V; ++q) sums[q] += parts[((j * V + q) * S + u) * 64 + lane];
+            const float dx = __builtin_fmaf(sums[0], s[i], d * r[i]);
+            const float dv = slope[i] * __builtin_fmaf(sums[1], kLn2, sums[0] * x[i]);   // the rates were in units of log 2
+            dd = __builtin_fmaf(r[i], x[i], dd);
             dbias += dv;
-            if (!mine) return;
-            *view_at<T>(a.dx, b, t + u, c) = T(dx);
-            *view_at<T>(a.ddt, b, t + u, c) = T(dv);
-            if (GATED) *view_at<T>(a.dz, b, t + u, c) = T(float(dr[u]) * __builtin_fmaf(d, x, sum_) * SsmGate(float(zr[u])).slope);
-        };
-        if (a.blocks == 1) {
-#pragma unroll
-            for (int u = 0; u < S; ++u)
-                if (u < left) finish(u, du[u], ds[u], GATED ? sum[u] : 0.f);
-        } else {
-            float* at = lds + turn * (blockDim.x * V * S);
-#pragma unroll
-            for (int u = 0; u < S; ++u) {
-                at[((wave * V + 0) * S + u) * 64 + w.lane] = du[u];
-                at[((wave * V + 1) * S + u) * 64 + w.lane] = ds[u];
-                if (GATED) at[((wave * V + 2) * S + u) * 64 + w.lane] = sum[u];
-            }
-            __syncthreads();   // the other half is free again: whoever writes it next has passed this
-#pragma unroll
-            for (int u = 0; u < S; ++u) {
-                if (u >= left || u % a.blocks != w.block) continue;
-                float v[3] = {0.f, 0.f, 0.f};
-                for (uint32_t j = 0; j < a.blocks; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] += at[(((first + j) * V + i) * S + u) * 64 + w.lane];
-                finish(u, v[0], v[1], v[2]);
-            }
+            if (!mine) continue;
+            dxs.at(t + u, off) = T(dx);
+            dss.at(t + u, off) = T(dv);
+            if (GATED) dzs.at(t + u, off) = T(back[i] * __builtin_fmaf(d, x[i], sums[V - 1]));
         }
         if (t == w.t0) break;
     }
@@ -578,25 +611,23 @@ __global__ __launch_bounds__(512) void k_ssm_backward(SsmArgs a) {
     if (mine)
 #pragma unroll
         for (int n = 0; n < NB; ++n) part[uint64_t(w.block * NB + n) * a.channels] = da[n];
-    if (a.blocks > 1) {
-        __syncthreads();
-        lds[(wave * 2 + 0) * 64 + w.lane] = dd;
-        lds[(wave * 2 + 1) * 64 + w.lane] = dbias;
-        __syncthreads();
-        dd = dbias = 0.f;
-        for (uint32_t j = 0; j < a.blocks; ++j) {
-            dd += lds[((first + j) * 2 + 0) * 64 + w.lane];
-            dbias += lds[((first + j) * 2 + 1) * 64 + w.lane];
-        }
-    }
+    __syncthreads();
+    lds[(w.block * 2 + 0) * 64 + lane] = dd;
+    lds[(w.block * 2 + 1) * 64 + lane] = dbias;
+    __syncthreads();
     if (!mine) return;
     if (w.block == 0) {
+        dd = dbias = 0.f;
+        for (uint32_t j = 0; j < a.blocks; ++j) {
+            dd += lds[(j * 2 + 0) * 64 + lane];
+            dbias += lds[(j * 2 + 1) * 64 + lane];
+        }
         part[uint64_t(a.padded) * a.channels] = dd;
         part[uint64_t(a.padded + 1) * a.channels] = dbias;
         for (uint64_t t = end > w.t0 ? end : w.t0; t < w.t1; ++t) {
-            *view_at<T>(a.dx, b, t, c) = T(0.f);
-            *view_at<T>(a.ddt, b, t, c) = T(0.f);
-            if (GATED) *view_at<T>(a.dz, b, t, c) = T(0.f);
+            dxs.at(t, off) = T(0.f);
+            dss.at(t, off) = T(0.f);
+            if (GATED) dzs.at(t, off) = T(0.f);
         }
     }
     if (a.chunks == 1 && a.last != nullptr)

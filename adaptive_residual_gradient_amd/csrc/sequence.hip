@@ -147,7 +147,7 @@ void launch_conv_back(const ConvArgs& a, const ConvBackLayout& l, uint32_t vec, 
 
 struct SsmLayout {
     uint32_t padded, nb, groups, chunks, steps;   // nb: states of a forward wavefront
-    uint64_t rows, ends, sums, part_rows, part_a, bytes;   // byte offsets
+    uint64_t rows, ends, sums, steps_of, part_rows, part_a, bytes;   // byte offsets
     bool brief;
 };
 
@@ -165,10 +165,9 @@ SsmLayout ssm_layout(const adacomp_ssm_shape& s, bool back) {
     l.nb = s.states <= 8 ? 8 : kSsmBlock;
     l.padded = (s.states + l.nb - 1) / l.nb * l.nb;
     l.groups = (s.channels + 63) / 64;
-    // Chunks: enough for 4 wavefronts a SIMD (backward 2, more do not fit), of 64 steps or more.
-    const uint64_t waves = std::max<uint64_t>(uint64_t(s.batch) * l.groups * (l.padded / (back ? kSsmBackBlock : l.nb)), 1);
-    const uint64_t want = back ? 2048 : 4096;
-    uint64_t chunks = std::min<uint64_t>((want + waves - 1) / waves, (s.length + 63) / 64);
+    // Chunks: enough for 4 wavefronts a SIMD, of 64 steps or more.
+    const uint64_t waves = std::max<uint64_t>(uint64_t(s.batch) * l.groups * (l.padded / l.nb), 1);
+    uint64_t chunks = std::min<uint64_t>((4096 + waves - 1) / waves, (s.length + 63) / 64);
     chunks = std::max<uint64_t>(chunks, 1);
     const uint64_t steps = ((s.length + chunks - 1) / chunks + kSsmKeep - 1) / kSsmKeep * kSsmKeep;
     l.steps = static_cast<uint32_t>(std::max<uint64_t>(steps, kSsmKeep));
@@ -182,6 +181,7 @@ SsmLayout ssm_layout(const adacomp_ssm_shape& s, bool back) {
     l.rows = place(rows);
     l.ends = place(l.chunks > 1 ? B * l.chunks * l.padded * C : 0);
     l.sums = place(l.chunks > 1 ? B * l.chunks * C : 0);
+    l.steps_of = place(!back && l.chunks > 1 ? B * s.length * C : 0);
     if (back) {
         l.part_rows = place(rows * l.groups);
         l.part_a = place(B * l.chunks * (l.padded + 2) * C);
@@ -196,8 +196,7 @@ uint64_t ssm_kept_bytes(const adacomp_ssm_shape& s) {
 bool ssm_fits(const adacomp_ssm_shape& s, const SsmLayout& l) {
     const uint64_t B = s.batch;
     return B * s.length * 2 * l.padded < kItems && B * l.padded * s.channels < kItems &&
-           B * l.chunks * (l.groups + 4) * (l.padded / kSsmBackBlock) * 64 < kItems &&
-           B * s.channels * 16 < kItems;
+           B * l.chunks * (l.groups + 4) * (l.padded / kSsmBackBlock) * 64 < kItems && B * s.channels * 16 < kItems;
 }
 
 void ssm_args(SsmArgs& a, const adacomp_ssm_shape& s, const adacomp_ssm_inputs& in, const SsmLayout& l, void* ws) {
@@ -223,6 +222,7 @@ void ssm_args(SsmArgs& a, const adacomp_ssm_shape& s, const adacomp_ssm_inputs& 
     a.rows = reinterpret_cast<float*>(p + l.rows);
     a.ends = reinterpret_cast<float*>(p + l.ends);
     a.sums = reinterpret_cast<float*>(p + l.sums);
+    a.steps_of = reinterpret_cast<float*>(p + l.steps_of);
 }
 
 // Workgroups of 4 wavefronts or so: the blocks of one group of channels, of as many groups as fit.
@@ -241,15 +241,22 @@ int launch_ssm(SsmArgs a, hipStream_t s) {
     if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
     a.blocks = a.padded / NB;
     const SsmGrid g(a);
-    if (a.chunks > 1) {
-        hipLaunchKernelGGL((k_ssm_forward<T, NB, true>), g.grid, g.block, 0, s, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        hipLaunchKernelGGL(k_ssm_join<false>, dim3(blocks_of(uint64_t(a.batch) * a.padded * a.channels)), dim3(256), 0, s,
-                           a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-    }
     const uint32_t lds = a.blocks > 1 ? 2 * g.block.x * kSsmKeep * 4 : 0;
-    hipLaunchKernelGGL((k_ssm_forward<T, NB, false>), g.grid, g.block, lds, s, a);
+#define ADACOMP_SSM(MODE)                                                                                          \
+    do {                                                                                                           \
+        if (a.z.p != nullptr) hipLaunchKernelGGL((k_ssm_forward<T, NB, MODE, true>), g.grid, g.block, lds, s, a);  \
+        else hipLaunchKernelGGL((k_ssm_forward<T, NB, MODE, false>), g.grid, g.block, lds, s, a);                  \
+    } while (0)
+    if (a.chunks == 1) {
+        ADACOMP_SSM(kSsmWhole);
+        return launch_status();
+    }
+    hipLaunchKernelGGL((k_ssm_forward<T, NB, kSsmEnds, false>), g.grid, g.block, 0, s, a);
+    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    hipLaunchKernelGGL(k_ssm_join<false>, dim3(blocks_of(uint64_t(a.batch) * a.padded * a.channels)), dim3(256), 0, s, a);
+    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    ADACOMP_SSM(kSsmChunks);
+#undef ADACOMP_SSM
     return launch_status();
 }
 
@@ -265,29 +272,35 @@ int launch_ssm(const SsmArgs& a, uint32_t nb, hipStream_t s) {
     return nb == 8 ? launch_ssm<T, 8>(a, s) : launch_ssm<T, 16>(a, s);
 }
 
+template <typename T, bool GATED>
+int launch_ssm_back(SsmArgs a, uint32_t nb, hipStream_t s) {
+    if (a.chunks > 1) {
+        a.blocks = a.padded / nb;
+        const SsmGrid g(a);
+        if (nb == 8) hipLaunchKernelGGL((k_ssm_back_ends<T, 8, GATED>), g.grid, g.block, 0, s, a);
+        else hipLaunchKernelGGL((k_ssm_back_ends<T, 16, GATED>), g.grid, g.block, 0, s, a);
+        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+        hipLaunchKernelGGL(k_ssm_join<true>, dim3(blocks_of(uint64_t(a.batch) * a.padded * a.channels)), dim3(256), 0, s, a);
+        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    }
+    a.blocks = a.padded / kSsmBackBlock;   // 2, 4, 8, 12 or 16
+    const dim3 grid(a.groups * a.chunks * a.batch), block(64 * a.blocks);
+    const uint32_t lds = (3 + a.blocks * (GATED ? 3 : 2)) * kSsmKeep * 64 * 4;
+    if (a.blocks == 2) hipLaunchKernelGGL((k_ssm_backward<T, 4, GATED>), grid, block, lds, s, a);
+    else if (a.blocks == 4) hipLaunchKernelGGL((k_ssm_backward<T, 2, GATED>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_ssm_backward<T, 1, GATED>), grid, block, lds, s, a);
+    return launch_status();
+}
+
 template <typename T>
-int launch_ssm_back(SsmArgs a, uint32_t nb, const adacomp_ssm_gradients& out, hipStream_t s) {
+int launch_ssm_back(const SsmArgs& a, uint32_t nb, const adacomp_ssm_gradients& out, hipStream_t s) {
     const uint64_t rows = uint64_t(a.batch) * a.length * 2 * a.padded;
     if (rows > 0) {
         hipLaunchKernelGGL(k_ssm_rows<T>, dim3(blocks_of(rows)), dim3(256), 0, s, a);
         if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
     }
-    if (a.chunks > 1) {
-        a.blocks = a.padded / nb;
-        const SsmGrid g(a);
-        if (nb == 8) hipLaunchKernelGGL((k_ssm_back_ends<T, 8>), g.grid, g.block, 0, s, a);
-        else hipLaunchKernelGGL((k_ssm_back_ends<T, 16>), g.grid, g.block, 0, s, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        hipLaunchKernelGGL(k_ssm_join<true>, dim3(blocks_of(uint64_t(a.batch) * a.padded * a.channels)), dim3(256), 0, s, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-    }
-    a.blocks = a.padded / kSsmBackBlock;
-    const SsmGrid g(a);
-    const bool gated = a.z.p != nullptr;
-    const uint32_t lds = a.blocks > 1 ? 2 * g.block.x * (gated ? 3 : 2) * kSsmKeep * 4 : 0;
-    if (gated) hipLaunchKernelGGL((k_ssm_backward<T, true>), g.grid, g.block, lds, s, a);
-    else hipLaunchKernelGGL((k_ssm_backward<T, false>), g.grid, g.block, lds, s, a);
-    if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+    const int st = a.z.p != nullptr ? launch_ssm_back<T, true>(a, nb, s) : launch_ssm_back<T, false>(a, nb, s);
+    if (st != ADACOMP_OK) return st;
     if (rows > 0) {
         hipLaunchKernelGGL(k_ssm_row_grad<T>, dim3(blocks_of(rows)), dim3(256), 0, s, a);
         if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
