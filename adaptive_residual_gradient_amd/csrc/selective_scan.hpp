@@ -134,6 +134,15 @@ __device__ __forceinline__ void ssm_rates(const SsmArgs& a, const SsmPlace& w, f
     }
 }
 
+// The kernel's arguments where the launch left them (they are its first and only ones), read again at each
+// use: kept in scalar registers over a loop they would not fit beside b and c, and be spilled lane by lane.
+typedef const SsmArgs __attribute__((address_space(4))) SsmArgsAt;
+__device__ __forceinline__ SsmArgsAt& ssm_args_again() {
+    SsmArgsAt* p = (SsmArgsAt*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *p;
+}
+
 // A sequence's rows of a view, for lanes that each have one channel: a row's address is the same for all
 // lanes, a channel's a 32-bit offset from it.
 template <typename T>
@@ -141,6 +150,8 @@ struct SsmRows {
     char* p;          // step 0's row
     uint64_t step;    // bytes
     __device__ __forceinline__ SsmRows(const ScanView& v, uint32_t b)
+        : p(static_cast<char*>(v.p) + uint64_t(b) * v.bs * sizeof(T)), step(v.ts * sizeof(T)) {}
+    __device__ __forceinline__ SsmRows(const ScanView __attribute__((address_space(4)))& v, uint32_t b)
         : p(static_cast<char*>(v.p) + uint64_t(b) * v.bs * sizeof(T)), step(v.ts * sizeof(T)) {}
     __device__ __forceinline__ T& at(uint64_t t, uint32_t offset) const {
         return *reinterpret_cast<T*>(p + t * step + offset);
@@ -175,14 +186,23 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
     }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, d = a.d ? a.d[c] : 0.f;
     const bool soft = a.softplus, keep = !ENDS && a.kept != nullptr && mine;
-    const SsmRows<T> xs(a.x, b), ds(a.dt, b), zs(a.z, b), ys(a.y, b);
     const uint64_t keeps = (a.length + S - 1) / S;
     uint32_t turn = 0;
+    // b and c, requested a step ahead
+    const float* const rows = a.rows + uint64_t(b) * a.length * 2 * a.padded + w.block * NB;
+    FVec<NB> bn, cn;
+    auto request = [&](uint64_t t) {
+        const float* row = rows + (t < end ? t : end - 1) * 2 * a.padded;
+        bn = ssm_row<NB>(row);
+        if (!ENDS) cn = ssm_row<NB>(row + a.padded);
+    };
     // U steps from t on
     auto steps = [&](uint64_t t, auto count) {
         constexpr int U = decltype(count)::value;
         T xr[U], zr[U];
         float s[U], y[U];
+        SsmArgsAt& again = ssm_args_again();
+        const SsmRows<T> xs(again.x, b), ds(again.dt, b), zs(again.z, b);
         float* sp = a.steps_of + (uint64_t(b) * a.length + t) * a.channels;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -196,22 +216,25 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
 #pragma unroll
             for (int n = 0; n < NB; ++n) k[uint64_t(n) * a.channels + c] = h[n];
         }
-        const float* row = a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB;
+        if (!FORMED) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            y[u] = 0.f;
-            const FVec<NB> bs = ssm_row<NB>(row + uint64_t(u) * 2 * a.padded);
-            FVec<NB> cs;
-            if (!ENDS) cs = ssm_row<NB>(row + (uint64_t(u) * 2 + 1) * a.padded);
-            if (!FORMED) {
+            for (int u = 0; u < U; ++u) {
                 s[u] += bias;
                 const float p = softplus(s[u]);
                 s[u] = soft ? p : s[u];
-                if (ENDS) {
-                    total += s[u];
-                    if (w.block == 0 && mine) sp[uint64_t(u) * a.channels + c] = s[u];
-                }
+                total += s[u];
             }
+            if (ENDS && w.block == 0 && mine)
+#pragma unroll
+                for (int u = 0; u < U; ++u) sp[uint64_t(u) * a.channels + c] = s[u];
+        }
+        // no branch from here on: the compiler would move all steps' work behind it, and spill their rows
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            y[u] = 0.f;
+            const FVec<NB> bs = bn, cs = cn;
+            request(t + u + 1);
             const float v = s[u] * float(xr[u]);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
@@ -221,6 +244,7 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
             __builtin_amdgcn_sched_barrier(0);   // or the rows of all steps are requested at once and spilled
         }
         if (ENDS) return;
+        const SsmRows<T> ys(ssm_args_again().y, b);
         auto finish = [&](int u, float sum) {
             sum = __builtin_fmaf(d, float(xr[u]), sum);
             if (GATED) {
@@ -248,6 +272,7 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
         }
     };
     uint64_t t = w.t0;
+    if (t < end) request(t);
     for (; t + S <= end; t += S) steps(t, Const<S>{});
     for (; t < end; ++t) steps(t, Const<1>{});
     if (!mine) return;
@@ -262,7 +287,7 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
         for (int n = 0; n < NB; ++n)
             if (w.block * NB + n < a.states) a.last[(uint64_t(b) * a.channels + c) * a.states + w.block * NB + n] = h[n];
     if (w.block == 0)
-        for (t = end > w.t0 ? end : w.t0; t < w.t1; ++t) ys.at(t, off) = T(0.f);
+        for (t = end > w.t0 ? end : w.t0; t < w.t1; ++t) SsmRows<T>(a.y, b).at(t, off) = T(0.f);
 }
 
 // What is carried into each chunk takes the place of its end from 0; backward
@@ -279,7 +304,7 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmArgs a) {
         a2 = a.a[uint64_t(c) * a.states + n] * kLog2e;
         if (a.h0 != nullptr) h = a.h0[place];
     }
-    constexpr uint32_t U = 4;   // chunks requested together
+    constexpr uint32_t U = 16;   // chunks requested together
     for (uint32_t k = 0; k < a.chunks; k += U) {
         float end[U], sum[U];
 #pragma unroll
@@ -479,7 +504,7 @@ __device__ __forceinline__ float sum_quads(float v0, float v1, float v2, float v
 // wavefront prepares OWN (s, u and r, which all of them take from LDS) and finishes the same ones, from the sums
 // over the wavefronts of du, ds and s that lie in LDS then.
 template <typename T, int OWN, bool GATED>
-__global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs a) {
+__global__ __launch_bounds__(OWN == 1 ? 1024 : 256, 4) void k_ssm_backward(SsmArgs a) {
     constexpr int S = kSsmKeep, NB = kSsmBackBlock, V = GATED ? 3 : 2;
     extern __shared__ float lds[];   // [3][S][64]: s, u, r;  [wavefront][V][S][64]: du, ds, sum
     float* const ready = lds;
@@ -501,9 +526,10 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs 
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, d = a.d ? a.d[c] : 0.f;
     const bool soft = a.softplus;
     const uint64_t end = w.t1 < w.n ? w.t1 : w.n, keeps = (a.length + S - 1) / S;
-    const SsmRows<T> xs(a.x, b), ss(a.dt, b), rs(a.dy, b), zs(a.z, b), dxs(a.dx, b), dss(a.ddt, b), dzs(a.dz, b);
     for (uint64_t t = w.t0 < end ? (end - 1) / S * S : 0; w.t0 < end; t -= S) {
         const uint32_t left = end - t < uint64_t(S) ? uint32_t(end - t) : uint32_t(S);
+        SsmArgsAt& again = ssm_args_again();
+        const SsmRows<T> xs(again.x, b), ss(again.dt, b), rs(again.dy, b), zs(again.z, b);
         // what the wavefront keeps of its own steps
         float x[OWN], s[OWN], r[OWN], slope[OWN], back[OWN];
         T xr[OWN], sr[OWN], rr[OWN], zr[OWN];
@@ -519,6 +545,16 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs 
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) h[0][n] = k[uint64_t(n) * a.channels + c];
+        // b and c of the whole block, requested before the barrier
+        const float* row = a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB;
+        FVec<NB> bs[S], cs[S];
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            const float* at = row + uint64_t(uint32_t(u) < left ? u : 0) * 2 * a.padded;
+            bs[u] = ssm_row<NB>(at);
+            cs[u] = ssm_row<NB>(at + a.padded);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             const uint32_t u = w.block + a.blocks * i;
@@ -541,35 +577,31 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs 
         }
         __syncthreads();
         // the block's decays and states
-        const float* row = a.rows + (uint64_t(b) * a.length + t) * 2 * a.padded + w.block * NB;
         float* part = parts + (w.block * V * S) * 64 + lane;
 #pragma unroll
         for (int u = 0; u < S; ++u) {
-            const float* at = row + uint64_t(uint32_t(u) < left ? u : 0) * 2 * a.padded;
-            const FVec<NB> bs = ssm_row<NB>(at), cs = ssm_row<NB>(at + a.padded);
             const float step = ready[u * 64 + lane], in = ready[(S + u) * 64 + lane];
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 e[u][n] = __builtin_amdgcn_exp2f(step * a2[n]);
-                h[u + 1][n] = __builtin_fmaf(e[u][n], h[u][n], in * bs[n]);
-                if (GATED) sum = __builtin_fmaf(cs[n], h[u + 1][n], sum);
+                h[u + 1][n] = __builtin_fmaf(e[u][n], h[u][n], in * bs[u][n]);
+                if (GATED) sum = __builtin_fmaf(cs[u][n], h[u + 1][n], sum);
             }
             if (GATED) part[(2 * S + u) * 64] = sum;
+            __builtin_amdgcn_sched_barrier(0);
         }
         float v[16], quad[S / 2];
 #pragma unroll
         for (int u = S - 1; u >= 0; --u) {
-            const float* at = row + uint64_t(uint32_t(u) < left ? u : 0) * 2 * a.padded;
-            const FVec<NB> bs = ssm_row<NB>(at), cs = ssm_row<NB>(at + a.padded);
             const float step = ready[u * 64 + lane], in = ready[(S + u) * 64 + lane], out = ready[(2 * S + u) * 64 + lane];
             float du = 0.f, ds = 0.f;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const float l = __builtin_fmaf(out, cs[n], f[n]);
+                const float l = __builtin_fmaf(out, cs[u][n], f[n]);
                 f[n] = e[u][n] * l;
                 const float q = f[n] * h[u][n];
-                du = __builtin_fmaf(l, bs[n], du);
+                du = __builtin_fmaf(l, bs[u][n], du);
                 ds = __builtin_fmaf(q, a2[n], ds);
                 da[n] = __builtin_fmaf(q, step, da[n]);
                 v[u % 2 * 4 + n] = l * in;
@@ -577,7 +609,10 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs 
             }
             part[u * 64] = du;
             part[(S + u) * 64] = ds;
-            if (u % 2 == 0) quad[u / 2] = sum_halves(v);
+            if (u % 2 == 0) {
+                quad[u / 2] = sum_halves(v);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         {   // lane l has the sum of step 2 (l % 4) + l / 16 % 2, state l / 4 % 4, of b or (from lane 32 on) of c
             const float total = sum_quads(quad[0], quad[1], quad[2], quad[3], lane);
@@ -587,6 +622,8 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs 
                             w.block * NB + lane / 4 % 4] = total;
         }
         __syncthreads();
+        SsmArgsAt& outs = ssm_args_again();
+        const SsmRows<T> dxs(outs.dx, b), dss(outs.ddt, b), dzs(outs.dz, b);
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             const uint32_t u = w.block + a.blocks * i;
@@ -625,9 +662,9 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256) void k_ssm_backward(SsmArgs 
         part[uint64_t(a.padded) * a.channels] = dd;
         part[uint64_t(a.padded + 1) * a.channels] = dbias;
         for (uint64_t t = end > w.t0 ? end : w.t0; t < w.t1; ++t) {
-            dxs.at(t, off) = T(0.f);
-            dss.at(t, off) = T(0.f);
-            if (GATED) dzs.at(t, off) = T(0.f);
+            SsmRows<T>(a.dx, b).at(t, off) = T(0.f);
+            SsmRows<T>(a.ddt, b).at(t, off) = T(0.f);
+            if (GATED) SsmRows<T>(a.dz, b).at(t, off) = T(0.f);
         }
     }
     if (a.chunks == 1 && a.last != nullptr)
