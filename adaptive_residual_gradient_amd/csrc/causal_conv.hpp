@@ -4,27 +4,33 @@
 //   p_t = bias + sum_k w_k x_(t-K+1+k),  y = p or p sigmoid(p)
 //   g_t = dy_t (p's derivative),  dx_t = sum_k w_k g_(t+K-1-k),  dw_k = sum g_t x_(t-K+1+k)
 //
-// A thread has 16 bytes of channels and goes along the sequence with the last
-// steps in registers: forward kConvRows steps (or kConvFewRows, where that
-// leaves too few threads), backward a longer stretch, so that the steps that
-// two stretches both read, K - 1 of x (and of dy), are few.  The weight's gradient is
-// summed in registers along the stretch, over a workgroup's stretches in LDS,
-// written as one partial row a workgroup and joined in float64 by a second kernel.
+// A thread has 8 bytes of channels and goes along the sequence with the last
+// steps in registers: forward 4 to 32 steps, backward a longer stretch, so that the
+// steps that two stretches both read, K - 1 of x (and of dy), are few.  The
+// weight's gradient is summed in registers along the stretch, over a
+// workgroup's stretches in LDS, written as one partial row a workgroup and
+// joined in float64 by a second kernel.
 //
-// Memory bounds both directions.
+// Memory bounds both directions: 8 x 4096 x 2048 bf16 of 4 taps takes 53 us forward
+// (5.1 TB/s) and 87 us backward (4.6 TB/s) and 6 us for the rows joined.
 #pragma once
 
 #include "sequence.hpp"
 
 namespace adacomp {
 
-constexpr uint32_t kConvRows = 16, kConvFewRows = 4;
+// Steps of a thread forward: the first of them that leaves enough threads (8 x 4096 x 2048 bf16, 4 taps, in us: 8
+// steps 70, 12 63, 16 58, 24 53.5, 32 53).
+constexpr uint32_t kConvRows[3] = {32, 12, 4};
 constexpr uint32_t kConvThreads = 256;
-constexpr uint32_t kConvMaxPartials = 256;   // partial rows of the weight's gradient
+// Partial rows of the weight's gradient: 3 wavefronts a SIMD, which the registers hold (8 x 4096 x 2048 bf16
+// backward and the rows joined: 97 us, with 256 101, with 512 111).
+constexpr uint32_t kConvMaxPartials = 384;
 // The filters that kernels are made for: 2, 3 and 4 taps; 8, for every other number too.
 constexpr uint32_t conv_kernel_taps(uint32_t taps) { return taps >= 2 && taps <= 4 ? taps : 8; }
-// A thread's channels: 16 bytes; 8 backward with 8 taps, whose windows and sums would not fit.
-constexpr uint32_t conv_bytes(bool back, uint32_t taps) { return back && conv_kernel_taps(taps) == 8 ? 8 : 16; }
+// A thread's channels: 8 bytes, for more threads than with 16 (8 x 4096 x 2048 bf16 72 us forward and 109 backward
+// against 98 and 118, before the other steps).
+constexpr uint32_t kConvBytes = 8;
 
 struct ConvArgs {
     ScanView x, y, dy, dx;
@@ -40,11 +46,15 @@ struct ConvArgs {
     uint32_t lanes;          // threads that cover the channels
     uint32_t per;            // backward: threads of one stretch in a workgroup
     uint32_t pieces, rows;   // stretches of a sequence, and (backward) their steps
+    bool past;               // results go past the cache
 };
 
 // p's logistic function.  From -87 down, where exp(-p) would overflow, it stays at 1.6e-38: y is off by
-// less than 1e-35 there.
+// less than 1e-35 there.  Of 16-bit calls, whose results are rounded far coarser, without the corrections of the
+// exponential's argument and of the reciprocal: off by 2^-24 (|p| + 4).
+template <typename T>
 __device__ __forceinline__ float conv_gate(float p) {
+    if (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(p * -kLog2e));
     p = __builtin_elementwise_minimum(__builtin_elementwise_maximum(p, -87.f), 100.f);
     const float d = 1.f + exp_of_minus(p);
     const float r = __builtin_amdgcn_rcpf(d);
@@ -88,11 +98,18 @@ __device__ __forceinline__ FVec<VW> conv_sum(const ConvArgs& a, const FVec<VW> (
     return sum;
 }
 
+// Workgroups go to the 8 chiplets in turn: each chiplet takes a run of them, whose stretches follow each
+// other, so that the steps that two stretches read come from its cache.
+__device__ __forceinline__ uint32_t conv_workgroup() {
+    const uint32_t each = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
+    return xcd * each + min(xcd, rest) + blockIdx.x / 8;
+}
+
 // ROWS steps of one sequence.
 template <typename T, int VW, int KT, int ROWS>
 __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, bool silu) {
     typedef typename Packed<T, VW>::V V;
-    const uint64_t i = uint64_t(blockIdx.x) * kConvThreads + threadIdx.x;
+    const uint64_t i = uint64_t(conv_workgroup()) * kConvThreads + threadIdx.x;
     const uint32_t r = uint32_t(i % a.lanes);
     const uint64_t unit = i / a.lanes;
     const uint32_t piece = uint32_t(unit % a.pieces), b = uint32_t(unit / a.pieces);
@@ -132,8 +149,11 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, bool silu) {
             FVec<VW> s = conv_sum<KT, VW>(a, w, x + u, bias);
             if (silu)
 #pragma unroll
-                for (int v = 0; v < VW; ++v) s[v] *= conv_gate(s[v]);
-            if (u < live) store_any<VW>(y, from_float<T, VW>(s));
+                for (int v = 0; v < VW; ++v) s[v] *= conv_gate<T>(s[v]);
+            if (u < live) {
+                if (a.past) stream_store<VW>(y, from_float<T, VW>(s));
+                else store_any<VW>(y, from_float<T, VW>(s));
+            }
             y += a.y.ts;
         }
     }
@@ -156,7 +176,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, bool silu) {
 template <typename T, int VW, int KT>
 __global__ __launch_bounds__(kConvThreads) void k_conv_backward(ConvArgs a, bool silu) {
     typedef typename Packed<T, VW>::V V;
-    constexpr int U = 4;   // steps requested together
+    constexpr int U = 8;   // steps requested together
     constexpr uint32_t HALO = KT - 1;
     __shared__ float sums[kConvThreads * VW];   // [stretch][channel of a thread][thread of the stretch]
     const uint32_t per = a.per, subs = kConvThreads / per, sub = threadIdx.x / per, lane = threadIdx.x % per;
@@ -210,7 +230,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(ConvArgs a, bool
                     const FVec<VW> p = conv_sum<KT, VW>(a, w, xw, bias);
 #pragma unroll
                     for (int v = 0; v < VW; ++v) {
-                        const float q = conv_gate(p[v]);
+                        const float q = conv_gate<T>(p[v]);
                         g[v] *= __builtin_fmaf(p[v] * q, 1.f - q, q);
                     }
                 }
@@ -235,7 +255,9 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(ConvArgs a, bool
                     for (int v = 0; v < VW; ++v) d[v] = __builtin_fmaf(w[k][v], gw[KT - 1 - k][v], d[v]);
                 }
                 if (s >= HALO) {
-                    store_any<VW>(view_at<T>(a.dx, b, s - HALO, c), from_float<T, VW>(d));
+                    T* at = view_at<T>(a.dx, b, s - HALO, c);
+                    if (a.past) stream_store<VW>(at, from_float<T, VW>(d));
+                    else store_any<VW>(at, from_float<T, VW>(d));
                 } else if (a.dstate != nullptr && HALO - s < a.taps) {   // so many steps before step 0
                     store_any<VW>(static_cast<T*>(a.dstate) +
                                       (uint64_t(b) * (a.taps - 1) + (a.taps - 1 - uint32_t(HALO - s))) * a.channels + c,
@@ -269,19 +291,20 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(ConvArgs a, bool
     }
 }
 
-// Partial rows joined: dweight [channels][taps] and dbias.  A thread sums one element.
-__global__ __launch_bounds__(256) void k_conv_weight_grad(const float* partial, uint32_t rows, uint32_t taps,
-                                                          uint32_t channels, float* dweight, float* dbias) {
-    __shared__ double part[16][17];
+// Partial rows joined: dweight [channels][taps] and dbias.  64 threads an element.
+__global__ __launch_bounds__(1024) void k_conv_weight_grad(const float* partial, uint32_t rows, uint32_t taps,
+                                                           uint32_t channels, float* dweight, float* dbias) {
+    __shared__ double part[64][17];
     const uint32_t lane = threadIdx.x % 16, sub = threadIdx.x / 16;
     const uint32_t c = blockIdx.x * 16 + lane, k = blockIdx.y;
     double s = 0.0;
     if (c < channels)
-        for (uint32_t i = sub; i < rows; i += 16) s += partial[(uint64_t(i) * (taps + 1) + k) * channels + c];
+#pragma unroll 4
+        for (uint32_t i = sub; i < rows; i += 64) s += partial[(uint64_t(i) * (taps + 1) + k) * channels + c];
     part[sub][lane] = s;
     __syncthreads();
     if (sub != 0 || c >= channels) return;
-    for (uint32_t j = 1; j < 16; ++j) s += part[j][lane];
+    for (uint32_t j = 1; j < 64; ++j) s += part[j][lane];
     if (k < taps) dweight[uint64_t(c) * taps + k] = float(s);
     else if (dbias != nullptr) dbias[c] = float(s);
 }

@@ -74,14 +74,14 @@ int check_conv(const adacomp_conv_shape* s) {
         return ADACOMP_ERR_INVALID_ARGUMENT;
     const int st = check_sizes(s->length, s->batch, s->channels);
     if (st != ADACOMP_OK) return st;
-    const uint64_t vec = 16 / type_size(s->type), lanes = (s->channels + vec - 1) / vec;
-    if (s->batch * lanes * ((s->length + kConvFewRows - 1) / kConvFewRows + 1) >= kItems) return ADACOMP_ERR_TOO_LARGE;
+    const uint64_t vec = kConvBytes / type_size(s->type), lanes = (s->channels + vec - 1) / vec;
+    if (s->batch * lanes * ((s->length + kConvRows[2] - 1) / kConvRows[2] + 1) >= kItems) return ADACOMP_ERR_TOO_LARGE;
     return ADACOMP_OK;
 }
 
 // Channels of a thread: a vector, or one where there are fewer channels than it has.
-uint32_t conv_vec(const adacomp_conv_shape& s, bool back) {
-    const uint32_t vec = conv_bytes(back, s.taps) / uint32_t(type_size(s.type));
+uint32_t conv_vec(const adacomp_conv_shape& s) {
+    const uint32_t vec = kConvBytes / uint32_t(type_size(s.type));
     return s.channels < vec ? 1 : vec;
 }
 
@@ -91,7 +91,7 @@ struct ConvBackLayout {
 // Stretches: as many as workgroups of kConvMaxPartials partial rows hold, of 32 steps or more.
 ConvBackLayout conv_back_layout(const adacomp_conv_shape& s) {
     ConvBackLayout l{};
-    const uint32_t vec = conv_vec(s, true);
+    const uint32_t vec = conv_vec(s);
     l.lanes = (s.channels + vec - 1) / vec;
     l.groups = (l.lanes + kConvThreads - 1) / kConvThreads;
     l.per = (l.lanes + l.groups - 1) / l.groups;
@@ -106,13 +106,14 @@ ConvBackLayout conv_back_layout(const adacomp_conv_shape& s) {
 
 template <typename T, int VW, int KT>
 void launch_conv(ConvArgs a, bool silu, hipStream_t s) {
-    // few rows a thread where more would leave fewer than 8 wavefronts a CU
-    const bool few = a.batch * uint64_t(a.lanes) * ((a.length + kConvRows - 1) / kConvRows) < 256 * 8 * 64;
-    const uint32_t rows = few ? kConvFewRows : kConvRows;
-    a.pieces = static_cast<uint32_t>(std::max<uint64_t>((a.length + rows - 1) / rows, 1));
+    // at least 2 wavefronts a SIMD
+    const auto threads = [&](uint32_t rows) { return a.batch * uint64_t(a.lanes) * ((a.length + rows - 1) / rows); };
+    const int pick = threads(kConvRows[0]) >= 2 * 1024 * 64 ? 0 : threads(kConvRows[1]) >= 2 * 1024 * 64 ? 1 : 2;
+    a.pieces = static_cast<uint32_t>(std::max<uint64_t>((a.length + kConvRows[pick] - 1) / kConvRows[pick], 1));
     const dim3 grid(blocks_of(uint64_t(a.batch) * a.lanes * a.pieces)), block(kConvThreads);
-    if (few) hipLaunchKernelGGL((k_conv<T, VW, KT, kConvFewRows>), grid, block, 0, s, a, silu);
-    else hipLaunchKernelGGL((k_conv<T, VW, KT, kConvRows>), grid, block, 0, s, a, silu);
+    if (pick == 0) hipLaunchKernelGGL((k_conv<T, VW, KT, kConvRows[0]>), grid, block, 0, s, a, silu);
+    else if (pick == 1) hipLaunchKernelGGL((k_conv<T, VW, KT, kConvRows[1]>), grid, block, 0, s, a, silu);
+    else hipLaunchKernelGGL((k_conv<T, VW, KT, kConvRows[2]>), grid, block, 0, s, a, silu);
 }
 
 template <typename T, int VW>
@@ -127,7 +128,7 @@ void launch_conv_taps(const ConvArgs& a, bool silu, hipStream_t s) {
 
 template <typename T>
 void launch_conv_back(const ConvArgs& a, const ConvBackLayout& l, uint32_t vec, bool silu, hipStream_t s) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = kConvBytes / sizeof(T);
     const dim3 grid(l.parts * l.groups), block(kConvThreads);
 #define ADACOMP_CONV_BACK(VW, KT)                                                        \
     do {                                                                                 \
@@ -138,7 +139,7 @@ void launch_conv_back(const ConvArgs& a, const ConvBackLayout& l, uint32_t vec, 
         case 2: ADACOMP_CONV_BACK(V, 2); break;
         case 3: ADACOMP_CONV_BACK(V, 3); break;
         case 4: ADACOMP_CONV_BACK(V, 4); break;
-        default: ADACOMP_CONV_BACK(V / 2, 8);
+        default: ADACOMP_CONV_BACK(V, 8);
     }
 #undef ADACOMP_CONV_BACK
 }
@@ -352,13 +353,14 @@ int adacomp_causal_conv(const adacomp_conv_shape* shape, const adacomp_view* x, 
     a.batch = s.batch;
     a.channels = s.channels;
     a.taps = s.taps;
-    const uint32_t vec = conv_vec(s, false);
+    a.past = s.batch * s.length * s.channels * size > kKeepBytes;
+    const uint32_t vec = conv_vec(s);
     a.lanes = (s.channels + vec - 1) / vec;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const bool silu = s.silu != 0;
-    if (s.type == ADACOMP_FLOAT) vec == 1 ? launch_conv_taps<float, 1>(a, silu, hs) : launch_conv_taps<float, 4>(a, silu, hs);
-    else if (s.type == ADACOMP_BFLOAT) vec == 1 ? launch_conv_taps<bf16, 1>(a, silu, hs) : launch_conv_taps<bf16, 8>(a, silu, hs);
-    else vec == 1 ? launch_conv_taps<f16, 1>(a, silu, hs) : launch_conv_taps<f16, 8>(a, silu, hs);
+    if (s.type == ADACOMP_FLOAT) vec == 1 ? launch_conv_taps<float, 1>(a, silu, hs) : launch_conv_taps<float, 2>(a, silu, hs);
+    else if (s.type == ADACOMP_BFLOAT) vec == 1 ? launch_conv_taps<bf16, 1>(a, silu, hs) : launch_conv_taps<bf16, 4>(a, silu, hs);
+    else vec == 1 ? launch_conv_taps<f16, 1>(a, silu, hs) : launch_conv_taps<f16, 4>(a, silu, hs);
     return launch_status();
 }
 
@@ -410,18 +412,19 @@ int adacomp_causal_conv_backward(const adacomp_conv_shape* shape, const adacomp_
     a.batch = s.batch;
     a.channels = s.channels;
     a.taps = s.taps;
+    a.past = s.batch * s.length * s.channels * size > kKeepBytes;
     a.lanes = l.lanes;
     a.per = l.per;
     a.pieces = l.pieces;
     a.rows = l.rows;
     if (s.batch > 0) {
-        const uint32_t vec = conv_vec(s, true);
+        const uint32_t vec = conv_vec(s);
         if (s.type == ADACOMP_FLOAT) launch_conv_back<float>(a, l, vec, s.silu != 0, hs);
         else if (s.type == ADACOMP_BFLOAT) launch_conv_back<bf16>(a, l, vec, s.silu != 0, hs);
         else launch_conv_back<f16>(a, l, vec, s.silu != 0, hs);
         if ((st = launch_status()) != ADACOMP_OK) return st;
     }
-    hipLaunchKernelGGL(k_conv_weight_grad, dim3((s.channels + 15) / 16, s.taps + 1), dim3(256), 0, hs, a.partial, l.parts,
+    hipLaunchKernelGGL(k_conv_weight_grad, dim3((s.channels + 15) / 16, s.taps + 1), dim3(1024), 0, hs, a.partial, l.parts,
                        s.taps, s.channels, dweight, dbias);
     return launch_status();
 }

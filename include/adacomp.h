@@ -540,7 +540,7 @@ int adacomp_gated_scan_workspace_bytes(const adacomp_scan_shape* shape, uint64_t
  * in float32 whatever the type, y rounded once.  x at the taps - 1 steps
  * before step 0 is `state` (zero without it).  ERR_TOO_LARGE: as for the gated
  * scan's sizes and strides, or 2^32 work-items and more (one for each 4 steps
- * of 16 bytes of channels). */
+ * of 8 bytes of channels). */
 #define ADACOMP_CONV_MAX_TAPS 8u
 typedef struct adacomp_conv_shape {
     uint64_t length;      /* steps, n_b <= length; may be 0 */
