@@ -38,10 +38,38 @@ __device__ __forceinline__ f32x16 mfma(Eight<f16> a, Eight<f16> b, f32x16 c) {
 }
 #define ADACOMP_LDS __attribute__((address_space(3)))
 #define ADACOMP_GLOBAL __attribute__((address_space(1)))
-template <typename E>
-__device__ __forceinline__ Four<E> read_transposed(const E* p) {
-    typedef short V __attribute__((ext_vector_type(4)));
-    return __builtin_bit_cast(Four<E>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ADACOMP_LDS V*)p));
+// Transposing LDS reads of N blocks of 32 rows: two of each block, the second 4 lines behind the first, whose
+// 4 + 4 elements along k are the lane's 8.  at: the blocks' LDS addresses; LOW: bytes from there to the lines.  The
+// builtin waits for every copy into LDS that is still under way, also into the other buffer; these wait for
+// themselves alone, in the same statement.
+typedef short Half8 __attribute__((ext_vector_type(4)));
+template <int LOW, int HIGH>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[1], Half8 (&v)[2]) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %2 offset:%3\n\tds_read_b64_tr_b16 %1, %2 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1])
+        : "v"(at[0]), "n"(LOW), "n"(HIGH)
+        : "memory");
+}
+template <int LOW, int HIGH>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[2], Half8 (&v)[4]) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%6\n\tds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+        "ds_read_b64_tr_b16 %2, %5 offset:%6\n\tds_read_b64_tr_b16 %3, %5 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at[0]), "v"(at[1]), "n"(LOW), "n"(HIGH)
+        : "memory");
+}
+template <int LOW, int HIGH>
+__device__ __forceinline__ void read_transposed(const uint32_t (&at)[4], Half8 (&v)[8]) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(LOW), "n"(HIGH)
+        : "memory");
 }
 
 // A matrix, 16-byte aligned, whose lines are 16-byte aligned too.
@@ -103,20 +131,50 @@ struct TileLoader {
                                              16, 0, 0);
         }
     }
-    // A wavefront's 32 rows from m on, elements k .. k + 15 of the step.
-    static __device__ __forceinline__ Eight<E> read(const E* tile, uint32_t m, uint32_t k) {
-        const uint32_t lane = threadIdx.x % 64;
-        if (!OUTER) {
-            const uint32_t line = m + lane % 32;
-            return *reinterpret_cast<const Eight<E>*>(tile + line * kTileK + place(line, k / 8 + lane / 32) * 8);
+    // A wavefront's BLOCKS of 32 rows from m on: where its lanes read them.
+    template <int BLOCKS>
+    struct Reader {
+        uint32_t at[BLOCKS];   // LDS addresses in bytes, from the tile's first
+        __device__ __forceinline__ explicit Reader(uint32_t m) {
+            const uint32_t lane = threadIdx.x % 64;
+#pragma unroll
+            for (int i = 0; i < BLOCKS; ++i) {
+                if (OUTER) {
+                    // lanes 16 g .. 16 g + 15: the columns from 16 (g % 2) on and k from 8 (g / 2) on, in two halves.
+                    // Lines 4 and 16 apart have their pieces in the same places.
+                    const uint32_t g = lane / 16, column = m + i * 32 + 16 * (g % 2) + lane % 4 * 4;
+                    const uint32_t line = 8 * (g / 2) + lane % 16 / 4;
+                    at[i] = (line * ROWS + place(line, column / 8) * 8 + column % 8) * 2;
+                } else {
+                    at[i] = (m + i * 32 + lane % 32) * kTileK * 2;
+                }
+            }
         }
-        // lanes 16 g .. 16 g + 15: the columns from m + 16 (g % 2) on and k from 8 (g / 2) on, in two halves
-        const uint32_t g = lane / 16, i = lane % 16;
-        const uint32_t column = m + 16 * (g % 2) + i % 4 * 4, line = k + 8 * (g / 2) + i / 4;
-        const Four<E> low = read_transposed(tile + line * ROWS + place(line, column / 8) * 8 + column % 8);
-        const Four<E> high = read_transposed(tile + (line + 4) * ROWS + place(line + 4, column / 8) * 8 + column % 8);
-        return __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
+        // Elements K .. K + 15 of the step.
+        template <int K>
+        __device__ __forceinline__ void read(const E* tile, Eight<E> (&v)[BLOCKS]) const {
+            if constexpr (OUTER) {
+                const uint32_t base = uint32_t(uintptr_t((ADACOMP_LDS const E*)tile));
+                uint32_t where[BLOCKS];
+                Half8 half[2 * BLOCKS];
+#pragma unroll
+                for (int i = 0; i < BLOCKS; ++i) where[i] = base + at[i];
+                read_transposed<K * ROWS * 2, (K + 4) * ROWS * 2>(where, half);
+#pragma unroll
+                for (int i = 0; i < BLOCKS; ++i)
+                    v[i] = __builtin_bit_cast(Eight<E>, __builtin_shufflevector(half[2 * i], half[2 * i + 1], 0, 1, 2, 3, 4, 5,
+                                                                                6, 7));
+            } else {
+                const uint32_t lane = threadIdx.x % 64;
+#pragma unroll
+                for (int i = 0; i < BLOCKS; ++i) {
+                    // rows 32 apart have their pieces in the same places
+                    const char* p = reinterpret_cast<const char*>(tile) + at[i] + place(lane % 32, K / 8 + lane / 32) * 16;
+                    v[i] = *reinterpret_cast<const Eight<E>*>(p);
+                }
+            }
+        }
+    };
 };
 
 template <typename E_, int WM_, int WN_, int MT_, int NT_, bool AOUTER, bool BOUTER>
@@ -137,6 +195,18 @@ struct TileProduct {
     // Row of register i of a block; the lane's column is lane % 32.
     __device__ static __forceinline__ uint32_t block_row(int i) {
         return 8 * (i / 4) + i % 4 + 4 * (threadIdx.x % 64 / 32);
+    }
+
+    // 16 elements of the inner axis.
+    template <int K, typename RA, typename RB>
+    __device__ __forceinline__ void part(const RA& ra, const RB& rb, const E* ta, const E* tb) {
+        Eight<E> av[MT], bv[NT];
+        ra.template read<K>(ta, av);
+        rb.template read<K>(tb, bv);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = mfma(av[i], bv[j], acc[i][j]);
     }
 
     // The sum over k in [kbegin, kend) of every pair of planes.
@@ -163,7 +233,8 @@ struct TileProduct {
             }
         };
         if (total > 0) request(lds);
-        const uint32_t r = row(), c = column();
+        const typename LoadA::template Reader<MT> ra(row());
+        const typename LoadB::template Reader<NT> rb(column());
         for (uint32_t step = 0; step < total; ++step) {
             // this step's elements are there, and the other buffer has been read
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -171,18 +242,10 @@ struct TileProduct {
             const E* ta = lds + (step & 1u) * STEP;
             const E* tb = ta + TM * kTileK;
             if (step + 1 < total) request(lds + (~step & 1u) * STEP);
-#pragma unroll
-            for (uint32_t kk = 0; kk < kTileK; kk += 16) {
-                Eight<E> av[MT], bv[NT];
-#pragma unroll
-                for (int i = 0; i < MT; ++i) av[i] = LoadA::read(ta, r + i * 32, kk);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) bv[j] = LoadB::read(tb, c + j * 32, kk);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[i][j] = mfma(av[i], bv[j], acc[i][j]);
-            }
+            part<0>(ra, rb, ta, tb);
+            part<16>(ra, rb, ta, tb);
+            part<32>(ra, rb, ta, tb);
+            part<48>(ra, rb, ta, tb);
         }
         __syncthreads();   // the buffers are free
     }
