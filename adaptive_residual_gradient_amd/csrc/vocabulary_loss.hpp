@@ -48,7 +48,7 @@ struct LossArgs {
     const float* dloss;
     float* factor;              // [rows]: dloss / temperature of the rows that count, times the scale
     float* scale;               // [2]: the scale and its reciprocal
-    float2* part;               // [tile of the vocabulary][rows]
+    float2* part;               // [tile of the vocabulary][rows]: largest logit in units of log 2, sum
     uint32_t rows, width, words, picks;
     float sharp;                // 1 / temperature
 };
@@ -101,31 +101,34 @@ __global__ __launch_bounds__(256) void k_pack(const T* from, uint64_t stride, ui
 
 // ---- forward ----
 
-// The rows' largest logits and sums of exponentials over a tile's words.
-template <typename P>
-__device__ __forceinline__ void leave_sums(const P& p, const LossArgs& a, uint32_t word0, uint32_t m0, uint32_t n0, uint32_t tile,
-                                           float2* lds) {
+// The rows' largest logits and sums of exponentials over a tile's words, in units of log 2: an exponential is
+// one multiply-add before it.  WHOLE: every word of the tile is there.
+template <bool WHOLE, typename P>
+__device__ __forceinline__ void leave_sums(const P& p, const LossArgs& a, uint32_t word0, uint32_t m0, uint32_t n0,
+                                           uint32_t tile, float2* lds) {
     const uint32_t lane = threadIdx.x % 64;
+    const float k = a.sharp * kLog2e;
+    auto there = [&](int i, int q) { return WHOLE || word0 + m0 + p.row() + i * 32 + p.block_row(q) < a.words; };
 #pragma unroll
     for (int j = 0; j < P::NT; ++j) {
         float most = -__builtin_inff(), sum = 0.f;
 #pragma unroll
         for (int i = 0; i < P::MT; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                if (word0 + m0 + p.row() + i * 32 + p.block_row(q) < a.words) most = fmaxf(most, p.acc[i][j][q]);
+            for (int q = 0; q < 16; ++q) most = fmaxf(most, there(i, q) ? p.acc[i][j][q] : -__builtin_inff());
+        most *= k;
         // exponentials from a finite number on, also where every logit is -infinity
-        const float from = most == -__builtin_inff() ? 0.f : most * a.sharp;
+        const float from = most == -__builtin_inff() ? 0.f : most;
 #pragma unroll
         for (int i = 0; i < P::MT; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                if (word0 + m0 + p.row() + i * 32 + p.block_row(q) < a.words)
-                    sum += __builtin_amdgcn_exp2f((p.acc[i][j][q] * a.sharp - from) * kLog2e);
-        most *= a.sharp;
+            for (int q = 0; q < 16; ++q) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][q], k, -from));
+                sum += there(i, q) ? e : 0.f;
+            }
         const float other = __shfl_xor(most, 32), theirs = __shfl_xor(sum, 32), top = fmaxf(most, other);
         const float f0 = top == -__builtin_inff() ? 0.f : top;
-        sum = sum * __builtin_amdgcn_exp2f((most - f0) * kLog2e) + theirs * __builtin_amdgcn_exp2f((other - f0) * kLog2e);
+        sum = sum * __builtin_amdgcn_exp2f(most - f0) + theirs * __builtin_amdgcn_exp2f(other - f0);
         if (lane < 32) lds[(p.wave() % P::WM) * P::TN + p.column() + j * 32 + lane] = make_float2(top, sum);
     }
     __syncthreads();
@@ -135,41 +138,60 @@ __device__ __forceinline__ void leave_sums(const P& p, const LossArgs& a, uint32
         for (int w = 1; w < P::WM; ++w) {
             const float2 t = lds[w * P::TN + n];
             const float top = fmaxf(s.x, t.x), f0 = top == -__builtin_inff() ? 0.f : top;
-            s.y = s.y * __builtin_amdgcn_exp2f((s.x - f0) * kLog2e) + t.y * __builtin_amdgcn_exp2f((t.x - f0) * kLog2e);
+            s.y = s.y * __builtin_amdgcn_exp2f(s.x - f0) + t.y * __builtin_amdgcn_exp2f(t.x - f0);
             s.x = top;
         }
         a.part[uint64_t(tile) * a.rows + n0 + n] = s;
     }
 }
 
+// Two groups of 4 consecutive rows of a tile's block that a lane and the lane 32 before or behind it have (rows 0 to
+// 3 and 8 to 11, or 4 to 7 and 12 to 15) become 8 consecutive ones: 0 to 7 of the lower lane, 8 to 15 of the upper.
+template <typename E>
+__device__ __forceinline__ Eight<E> eight_rows(Four<E> low, Four<E> high) {
+    typedef unsigned int Pair __attribute__((ext_vector_type(2)));
+    typedef unsigned int Quad __attribute__((ext_vector_type(4)));
+    const Pair l = __builtin_bit_cast(Pair, low), h = __builtin_bit_cast(Pair, high);
+    const auto x = __builtin_amdgcn_permlane32_swap(l[0], h[0], false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(l[1], h[1], false, false);
+    return __builtin_bit_cast(Eight<E>, Quad{x[0], y[0], x[1], y[1]});
+}
+
 // dz of a tile, scaled, into [plane][rows][line]: columns from the piece's first word on, zeros behind the last.
-template <typename P>
+// One plane's exponentials take one multiply-add before them, whose rounding is far below the type's; three planes'
+// are float32's own.  A row that does not count, whose lse may be anything, gives exp(0) times 0.
+template <bool WHOLE, typename P>
 __device__ __forceinline__ void leave_dz(const P& p, const LossArgs& a, uint32_t word0, uint32_t m0, uint32_t n0,
                                          const Operand& dz, uint32_t planes) {
     typedef typename P::E E;
     const uint32_t lane = threadIdx.x % 64;
+    const float k = a.sharp * kLog2e;
 #pragma unroll
     for (int j = 0; j < P::NT; ++j) {
         const uint32_t row = n0 + p.column() + j * 32 + lane % 32;
-        if (row >= a.rows) continue;
-        const float lse = a.lse[row], f = a.factor[row];
-        E* out = static_cast<E*>(const_cast<void*>(dz.p)) + uint64_t(row) * dz.line;
+        const bool on = row < a.rows;   // the lane 32 away has the same row
+        const float f = on ? a.factor[row] : 0.f, lse = f != 0.f ? a.lse[row] : 0.f, from = lse * kLog2e;
+        E* out = static_cast<E*>(const_cast<void*>(dz.p)) + uint64_t(on ? row : 0) * dz.line;
 #pragma unroll
         for (int i = 0; i < P::MT; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; q += 4) {
-                const uint32_t m = m0 + p.row() + i * 32 + p.block_row(q);
-                FVec<4> v;
+            for (int q = 0; q < 16; q += 8) {
+                const uint32_t m = m0 + p.row() + i * 32 + p.block_row(q);   // and 8 rows on
+                FVec<8> v;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float e = exp_of_minus(__builtin_elementwise_minimum(lse - p.acc[i][j][q + k] * a.sharp, 200.f));
-                    // a row that does not count stays out of it, whatever it holds
-                    v[k] = f != 0.f && word0 + m + k < a.words ? e * f : 0.f;
+                for (int t = 0; t < 8; ++t) {
+                    const float z = p.acc[i][j][q + t];
+                    const float e = planes == 1 ? __builtin_amdgcn_exp2f(__builtin_fmaf(z, k, -from))
+                                                : exp_of_minus(__builtin_elementwise_minimum(lse - z * a.sharp, 200.f));
+                    v[t] = WHOLE || word0 + m + t % 4 + t / 4 * 8 < a.words ? e * f : 0.f;
                 }
+                const uint32_t at = m0 + p.row() + i * 32 + q * 2 + lane / 32 * 8;
                 for (uint32_t plane = 0; plane < planes; ++plane) {
-                    const Four<E> part = __builtin_convertvector(v, Four<E>);
-                    *reinterpret_cast<Four<E>*>(out + plane * dz.plane + m) = part;
-                    v -= __builtin_convertvector(part, FVec<4>);
+                    const Eight<E> part = __builtin_convertvector(v, Eight<E>);
+                    const Eight<E> out8 = eight_rows<E>(__builtin_shufflevector(part, part, 0, 1, 2, 3),
+                                                        __builtin_shufflevector(part, part, 4, 5, 6, 7));
+                    if (on) *reinterpret_cast<Eight<E>*>(out + plane * dz.plane + at) = out8;
+                    if (planes > 1) v -= __builtin_convertvector(part, FVec<8>);
                 }
             }
     }
@@ -184,8 +206,15 @@ __global__ __launch_bounds__(P::THREADS) void k_logits(LossArgs a, Operand w, ui
     const TilePlace t(blockIdx.x, tiles_m, tiles_n);
     const uint32_t m0 = t.m * P::TM, n0 = t.n * P::TN;
     p.run(w, a.x, m0, n0, 0, w.inner, planes, reinterpret_cast<typename P::E*>(lds));
-    if (BACK) leave_dz(p, a, word0, m0, n0, dz, planes);
-    else leave_sums(p, a, word0, m0, n0, tile0 + t.m, reinterpret_cast<float2*>(lds));
+    const bool whole = word0 + m0 + P::TM <= a.words;
+    if (BACK) {
+        if (whole) leave_dz<true>(p, a, word0, m0, n0, dz, planes);
+        else leave_dz<false>(p, a, word0, m0, n0, dz, planes);
+    } else {
+        float2* sums = reinterpret_cast<float2*>(lds);
+        if (whole) leave_sums<true>(p, a, word0, m0, n0, tile0 + t.m, sums);
+        else leave_sums<false>(p, a, word0, m0, n0, tile0 + t.m, sums);
+    }
 }
 
 // z at the picks: a wavefront a pick.
@@ -238,7 +267,7 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, uint32_t tiles) {
     float most = -__builtin_inff(), sum = 0.f;
     auto join = [&](float m, float s) {
         const float top = fmaxf(most, m), f0 = top == -__builtin_inff() ? 0.f : top;
-        sum = sum * expf(most - f0) + s * expf(m - f0);
+        sum = sum * exp2f(most - f0) + s * exp2f(m - f0);
         most = top;
     };
     for (uint32_t t = lane; t < tiles; t += 64) {
@@ -246,7 +275,7 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, uint32_t tiles) {
         join(s.x, s.y);
     }
     for (int m = 32; m > 0; m /= 2) join(__shfl_xor(most, m), __shfl_xor(sum, m));
-    const float lse = most + logf(sum);
+    const float lse = __builtin_fmaf(most, kLn2, __builtin_fmaf(most, kLn2Low, logf(sum)));   // most in units of log 2
     if (lane == 0) a.lse[row] = lse;
     float loss = 0.f;
     if (a.teacher == nullptr) {
@@ -347,6 +376,19 @@ struct ProductOut {
     bool add;             // partial sums: to what is there
 };
 
+// N columns of a row from m on, as far as they are there.
+template <typename T, int N>
+__device__ __forceinline__ void put_columns(T* row, uint32_t m, uint32_t cols, bool on, typename Packed<T, N>::V v) {
+    if (!on) return;
+    if (m + N <= cols) {
+        store_any<N>(row + m, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (m + k < cols) row[m + k] = v[k];
+    }
+}
+
 // One product from dz: [n, m] = sum over k; shares of the inner axis where PARTIAL.
 template <typename P, typename T, bool PARTIAL>
 __global__ __launch_bounds__(P::THREADS) void k_product(Operand x, Operand y, uint32_t inner, uint32_t planes,
@@ -364,23 +406,32 @@ __global__ __launch_bounds__(P::THREADS) void k_product(Operand x, Operand y, ui
 #pragma unroll
     for (int j = 0; j < P::NT; ++j) {
         const uint32_t n = n0 + p.column() + j * 32 + lane % 32;
-        if (n >= out.rows) continue;
-        T* row = static_cast<T*>(out.p) + (PARTIAL ? uint64_t(share) * out.rows * out.stride : 0) + n * out.stride;
+        const bool on = n < out.rows;   // the lane 32 away has the same row
+        T* row = static_cast<T*>(out.p) + (PARTIAL ? uint64_t(share) * out.rows * out.stride : 0) +
+                 uint64_t(on ? n : 0) * out.stride;
 #pragma unroll
         for (int i = 0; i < P::MT; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; q += 4) {
-                const uint32_t m = m0 + p.row() + i * 32 + p.block_row(q);
-                FVec<4> v;
+            for (int q = 0; q < 16; q += 8) {
+                const uint32_t first = m0 + p.row() + i * 32 + q * 2;
+                if constexpr (sizeof(T) == 2) {
+                    FVec<8> v;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = p.acc[i][j][q + k] * factor;
-                if (m + 4 <= out.cols) {
-                    if (PARTIAL && out.add) v += to_float<4, T>(load_any<4>(row + m));
-                    store_any<4>(row + m, from_float<T, 4>(v));
+                    for (int k = 0; k < 8; ++k) v[k] = p.acc[i][j][q + k] * factor;
+                    const Eight<T> part = __builtin_convertvector(v, Eight<T>);
+                    const Eight<T> whole = eight_rows<T>(__builtin_shufflevector(part, part, 0, 1, 2, 3),
+                                                         __builtin_shufflevector(part, part, 4, 5, 6, 7));
+                    put_columns<T, 8>(row, first + lane / 32 * 8, out.cols, on, whole);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (m + k < out.cols) row[m + k] = T(PARTIAL && out.add ? v[k] + float(row[m + k]) : v[k]);
+                    for (int h = 0; h < 8; h += 4) {
+                        const uint32_t m = first + h * 2 + lane / 32 * 4;
+                        FVec<4> v;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = p.acc[i][j][q + h + k] * factor;
+                        if (PARTIAL && out.add && on && m < out.cols) v += load_any<4>(row + m);   // rows of whole 8 columns
+                        put_columns<T, 4>(row, m, out.cols, on, v);
+                    }
                 }
             }
     }
