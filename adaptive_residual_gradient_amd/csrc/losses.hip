@@ -15,25 +15,31 @@ using namespace adacomp;
 namespace {
 
 constexpr uint32_t kWord = 256;            // words of a tile of the vocabulary, at most
-constexpr uint64_t kPieceBytes = 512u << 20;   // dz of a piece
-constexpr uint32_t kPieceMost = 32768, kPieceLeast = 2048, kPackMost = 16384;   // words of a piece, backward and forward
+constexpr uint64_t kPieceBytes = 1u << 30;     // dz of a piece
+constexpr uint32_t kPieceMost = 65536, kPieceLeast = 2048, kPackMost = 16384;   // words of a piece, backward and forward
+constexpr uint32_t kCus = 256;
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 uint32_t share_of(uint64_t n, uint32_t each) { return static_cast<uint32_t>((n + each - 1) / each); }
 uint32_t blocks_of(uint64_t items) { return static_cast<uint32_t>((items + 255) / 256); }
 
-// Tiles of the products: 256 x 256 by 8 wavefronts; 128 x 128 by 4, where the large ones would be fewer
-// than the CUs; 128 x 64 for few rows.
-enum { kBig, kMid, kSmall };
-constexpr uint32_t kTileM[3] = {256, 128, 128};   // words, or columns of a gradient
-int tile_of(uint64_t m, uint64_t n, uint64_t shares) {
-    if (n <= 64) return kSmall;
-    return up(m, 256) / 256 * (up(n, 256) / 256) * shares >= 192 ? kBig : kMid;
+// Tiles of the products: 256 x 256 by 8 wavefronts where they give most CUs one; else 128 x 128 by 4, two of which a
+// CU holds; for few rows, or where these leave half of the CUs without one, 64 x 64 by 2.
+enum { kBig, kMid, kTiny };
+constexpr uint32_t kTileM[3] = {256, 128, 64};   // words, or columns of a gradient
+uint64_t tiles(uint64_t m, uint64_t n, uint64_t side) { return (m + side - 1) / side * ((n + side - 1) / side); }
+int tile_of(uint64_t m, uint64_t n, uint64_t shares = 1) {
+    if (n <= 64) return kTiny;
+    if (tiles(m, n, 256) * shares >= kCus * 3 / 4) return kBig;
+    return tiles(m, n, 128) * shares >= kCus / 2 ? kMid : kTiny;
 }
-// Shares of the inner axis of a product into partial sums.
-uint32_t shares_of(uint64_t m, uint64_t n, uint64_t k) {
-    const uint64_t tiles = n <= 64 ? up(m, 128) / 128 : up(m, 256) / 256 * (up(n, 256) / 256);
-    return static_cast<uint32_t>(std::max<uint64_t>(std::min<uint64_t>({(384 + tiles - 1) / tiles, up(k, 512) / 512, 16}), 1));
+// Shares of the inner axis of a product into partial sums: for one tile a CU where 256 x 256 tiles are enough for a
+// quarter of them, else for two of 128 x 128.
+uint32_t shares_of(uint64_t m, uint64_t n, uint64_t k, uint32_t planes) {
+    const uint64_t big = tiles(m, n, 256), small = std::max<uint64_t>(tiles(m, n, n <= 64 ? 64 : 128), 1);
+    const uint64_t want = big >= kCus / 4 ? (kCus + big - 1) / big : (2 * kCus + small - 1) / small;
+    const uint64_t most = (k + 255) / 256 * (planes == 3 ? 4 : 1);   // 256 of the inner axis, or as much work in planes
+    return static_cast<uint32_t>(std::max<uint64_t>(std::min<uint64_t>({want, most, 64}), 1));
 }
 
 struct HeadLayout {
@@ -57,8 +63,14 @@ HeadLayout head_layout(const adacomp_head& h, bool back) {
     const uint64_t R = h.rows, V = h.vocabulary;
     if (back) {
         const uint64_t words = kPieceBytes / std::max<uint64_t>(2 * l.planes * R, 1) / kWord * kWord;
-        l.piece = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(std::min<uint64_t>(words, kPieceMost), kPieceLeast),
-                                                           up(V, kWord)));
+        // The tiles of a piece's dweight are whole turns of the CUs, or all of the vocabulary's where their last turn
+        // is half full; where it is not, the rest of the vocabulary is a piece of its own (8192 x 2048 over 49999
+        // words: 49152 and 847).
+        const uint64_t across = (h.width + 255) / 256, turn = up(kCus, across) / across * kWord, all = up(V, kWord);
+        uint64_t piece = std::min<uint64_t>(std::max<uint64_t>(std::min<uint64_t>(words, kPieceMost), kPieceLeast), all);
+        const uint64_t last = across * (all / kWord) % kCus;
+        if (piece > turn && (piece < all || (last > 0 && last < kCus / 2))) piece = piece / turn * turn;
+        l.piece = static_cast<uint32_t>(piece);
     } else {
         l.piece = static_cast<uint32_t>(std::min<uint64_t>(kPackMost, up(V, kWord)));
     }
@@ -69,13 +81,13 @@ HeadLayout head_layout(const adacomp_head& h, bool back) {
     };
     l.x = place(R * l.line * 2 * l.planes);
     l.w = place(uint64_t(l.piece) * l.line * 2 * l.planes);
-    l.part = place(back ? 0 : R * (up(V, 128) / 128) * 8);
+    l.part = place(back ? 0 : R * (up(V, kTileM[kTiny]) / kTileM[kTiny]) * 8);
     l.picked = place(back ? 0 : R * 4);
     if (back) {
         l.factor = place(R * 4);
         l.scale = place(8);
         l.dz = place(R * l.piece * 2 * l.planes);
-        l.shares = shares_of(h.width, R, l.piece);
+        l.shares = shares_of(h.width, R, l.piece, l.planes);
         l.dx = place(uint64_t(l.shares) * R * l.line * 4);
     }
     return l;
@@ -155,7 +167,7 @@ struct Loss {
         switch (tile) {
             case kBig: return logits<TileProduct<E, 2, 4, 4, 2, false, false>, BACK>(w, word0, dz, tile0);
             case kMid: return logits<TileProduct<E, 2, 2, 2, 2, false, false>, BACK>(w, word0, dz, tile0);
-            default: return logits<TileProduct<E, 4, 1, 1, 2, false, false>, BACK>(w, word0, dz, tile0);
+            default: return logits<TileProduct<E, 2, 1, 1, 2, false, false>, BACK>(w, word0, dz, tile0);
         }
     }
     template <typename P, typename O, bool PARTIAL>
@@ -169,7 +181,7 @@ struct Loss {
         switch (tile) {
             case kBig: return product<TileProduct<E, 2, 4, 4, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
             case kMid: return product<TileProduct<E, 2, 2, 2, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
-            default: return product<TileProduct<E, 4, 1, 1, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
+            default: return product<TileProduct<E, 2, 1, 1, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
         }
     }
 
@@ -182,7 +194,7 @@ struct Loss {
         }
         const bool whole = direct<T>(a.weight.p, a.weight.stride, a.width);
         const uint32_t piece = whole ? a.words : l.piece;
-        const int tile = tile_of(piece, a.rows, 1);
+        const int tile = tile_of(piece, a.rows);
         uint32_t tiles = 0;
         for (uint32_t word0 = 0; word0 < a.words; word0 += piece) {
             const Operand w = weight(word0, std::min(piece, a.words - word0));
@@ -206,7 +218,7 @@ struct Loss {
             const uint32_t words = std::min(l.piece, a.words - word0);
             const Operand w = weight(word0, words);
             const Operand dz{ws + l.dz, l.piece, uint64_t(a.rows) * l.piece, a.rows, words};
-            logits<true>(tile_of(words, a.rows, 1), w, word0, dz, 0);
+            logits<true>(tile_of(words, a.rows), w, word0, dz, 0);
             if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
             if (c.distil)
                 hipLaunchKernelGGL(k_pick_grad<E>, dim3(share_of(a.rows, 4)), dim3(256), 0, c.stream, a, word0, words, dz,
@@ -224,7 +236,7 @@ struct Loss {
             if (c.dweight != nullptr) {
                 const ProductOut out{static_cast<T*>(c.dweight) + uint64_t(word0) * c.dweight_stride, c.dweight_stride, words,
                                      a.width, a.scale, false};
-                product<T, false, true>(tile_of(a.width, words, 1), turned(a.x, l.line, a.rows),
+                product<T, false, true>(tile_of(a.width, words), turned(a.x, l.line, a.rows),
                                         turned(dz, uint32_t(up(words, 8)), a.rows), a.rows, 1, out);
                 if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
             }
@@ -286,7 +298,7 @@ int run_loss(const LossCall& c) {
     // work-items of the launches that go over whole matrices, and of a wavefront a pick
     constexpr uint64_t items = uint64_t(1) << 32;
     if (R * (l.line / 4) >= items || uint64_t(l.piece) * (l.line / 8) >= items || R * c.picks * 64 >= items ||
-        up(h.vocabulary, 128) / 128 * (up(R, 64) / 64) * 512 >= items)
+        up(h.vocabulary, 64) / 64 * (up(R, 64) / 64) * 512 >= items)
         return ADACOMP_ERR_TOO_LARGE;
     const uint64_t rows4 = R * 4, picks4 = rows4 * c.picks;
     const Range r[12] = {range_of(c.back ? nullptr : c.loss, c.back || !c.loss ? 0 : rows4),

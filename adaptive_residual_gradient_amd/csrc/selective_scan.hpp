@@ -64,13 +64,13 @@ struct Const {
     static constexpr int value = N;
 };
 
-// log(1 + exp(v)).
-__device__ __forceinline__ float softplus(float v) {
+// log(1 + exp(v)), and its derivative 1 / (1 + exp(-v)) from the same exponential.
+__device__ __forceinline__ float softplus(float v, float* slope = nullptr) {
     const float e = exp_of_minus(__builtin_elementwise_minimum(__builtin_fabsf(v), 100.f));
-    const float w = 1.f + e;
+    const float w = 1.f + e, r = __builtin_amdgcn_rcpf(w);
     // what the rounding of 1 + e leaves out, relative to it
-    const float low = (e - (w - 1.f)) * __builtin_amdgcn_rcpf(w);
-    const float l = __builtin_fmaf(__builtin_amdgcn_logf(w), kLn2, low);
+    const float l = __builtin_fmaf(__builtin_amdgcn_logf(w), kLn2, (e - (w - 1.f)) * r);
+    if (slope) *slope = (v < 0.f ? e : 1.f) * __builtin_fmaf(r, __builtin_fmaf(-w, r, 1.f), r);
     return __builtin_elementwise_maximum(v, 0.f) + l;
 }
 // 1 / (1 + exp(-v)); from -87 down it stays at 1.6e-38.
@@ -559,9 +559,9 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256, 4) void k_ssm_backward(SsmAr
         for (int i = 0; i < OWN; ++i) {
             const uint32_t u = w.block + a.blocks * i;
             x[i] = float(xr[i]);
-            const float v = float(sr[i]) + bias, p = softplus(v);
+            const float v = float(sr[i]) + bias, p = softplus(v, &slope[i]);
             s[i] = soft ? p : v;
-            slope[i] = soft ? logistic(v) : 1.f;
+            slope[i] = soft ? slope[i] : 1.f;
             r[i] = float(rr[i]);
             if (GATED) {
                 const float z = float(zr[i]), q = logistic(z), g = z * q;

@@ -447,6 +447,7 @@ __global__ __launch_bounds__(256) void k_join_shares(const float* part, uint32_t
     const uint32_t c = uint32_t(i % per) * 4;
     if (row >= rows) return;
     FVec<4> v = 0.f;
+#pragma unroll 8
     for (uint32_t s = 0; s < shares; ++s) v += load_any<4>(part + (s * rows + row) * line + c);
     v *= scale[1];
     T* to = out + row * stride + c;
