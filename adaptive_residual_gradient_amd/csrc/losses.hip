@@ -38,12 +38,12 @@ int tile_of(uint64_t m, uint64_t n, uint64_t shares = 1) {
 uint32_t shares_of(uint64_t m, uint64_t n, uint64_t k, uint32_t planes) {
     const uint64_t big = tiles(m, n, 256), small = std::max<uint64_t>(tiles(m, n, n <= 64 ? 64 : 128), 1);
     const uint64_t want = big >= kCus / 4 ? (kCus + big - 1) / big : (2 * kCus + small - 1) / small;
-    const uint64_t most = (k + 255) / 256 * (planes == 3 ? 4 : 1);   // 256 of the inner axis, or as much work in planes
+    const uint64_t most = (k + 255) / 256 * (planes == 3 ? 4 : planes);   // 256 of the inner axis, or as much work in planes
     return static_cast<uint32_t>(std::max<uint64_t>(std::min<uint64_t>({want, most, 64}), 1));
 }
 
 struct HeadLayout {
-    uint32_t line, planes, piece, shares;   // line: a packed row's elements
+    uint32_t line, planes, dz_planes, piece, shares;   // line: a packed row's elements
     uint64_t x, w, part, picked, factor, scale, dz, dx, bytes;   // byte offsets
 };
 
@@ -59,10 +59,11 @@ int check_head(const adacomp_head* h, uint32_t picks) {
 HeadLayout head_layout(const adacomp_head& h, bool back) {
     HeadLayout l{};
     l.line = static_cast<uint32_t>(up(h.width, 8));
-    l.planes = h.type == ADACOMP_FLOAT ? 3 : 1;
     const uint64_t R = h.rows, V = h.vocabulary;
+    l.planes = h.type == ADACOMP_FLOAT ? 3 : 1;
+    l.dz_planes = l.planes == 3 ? 3 : R <= kLossFewRows ? 2 : 1;
     if (back) {
-        const uint64_t words = kPieceBytes / std::max<uint64_t>(2 * l.planes * R, 1) / kWord * kWord;
+        const uint64_t words = kPieceBytes / std::max<uint64_t>(2 * l.dz_planes * R, 1) / kWord * kWord;
         // The tiles of a piece's dweight are whole turns of the CUs, or all of the vocabulary's where their last turn
         // is half full; where it is not, the rest of the vocabulary is a piece of its own (8192 x 2048 over 49999
         // words: 49152 and 847).
@@ -85,9 +86,9 @@ HeadLayout head_layout(const adacomp_head& h, bool back) {
     l.picked = place(back ? 0 : R * 4);
     if (back) {
         l.factor = place(R * 4);
-        l.scale = place(8);
-        l.dz = place(R * l.piece * 2 * l.planes);
-        l.shares = shares_of(h.width, R, l.piece, l.planes);
+            l.scale = place(4);
+        l.dz = place(R * l.piece * 2 * l.dz_planes);
+        l.shares = shares_of(h.width, R, l.piece, l.dz_planes);
         l.dx = place(uint64_t(l.shares) * R * l.line * 4);
     }
     return l;
@@ -160,7 +161,7 @@ struct Loss {
     void logits(const Operand& w, uint32_t word0, const Operand& dz, uint32_t tile0) const {
         const uint32_t tm = share_of(w.extent, P::TM), tn = share_of(a.rows, P::TN);
         hipLaunchKernelGGL((k_logits<P, BACK>), dim3(tm * tn), dim3(P::THREADS), P::LDS_BYTES, c.stream, a, w, word0, tm, tn,
-                           uint32_t(PLANES), dz, tile0);
+                           PLANES == 3 ? kThreeByThree : kOneByOne, dz, l.dz_planes, tile0);
     }
     template <bool BACK>
     void logits(int tile, const Operand& w, uint32_t word0, const Operand& dz, uint32_t tile0) const {
@@ -174,7 +175,8 @@ struct Loss {
     void product(const Operand& x, const Operand& y, uint32_t inner, uint32_t shares, const ProductOut& out) const {
         const uint32_t tm = share_of(out.cols, P::TM), tn = share_of(out.rows, P::TN);
         hipLaunchKernelGGL((k_product<P, O, PARTIAL>), dim3(tm * tn * shares), dim3(P::THREADS), P::LDS_BYTES, c.stream, x,
-                           y, inner, uint32_t(PLANES), tm, tn, shares, out);
+                           y, inner, PLANES == 3 ? kThreeByThree : l.dz_planes == 2 ? kOneByTwo : kOneByOne, tm, tn, shares,
+                           out);
     }
     template <typename O, bool PARTIAL, bool YOUTER>
     void product(int tile, const Operand& x, const Operand& y, uint32_t inner, uint32_t shares, const ProductOut& out) const {
@@ -222,10 +224,10 @@ struct Loss {
             if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
             if (c.distil)
                 hipLaunchKernelGGL(k_pick_grad<E>, dim3(share_of(a.rows, 4)), dim3(256), 0, c.stream, a, word0, words, dz,
-                                   uint32_t(PLANES));
+                                   l.dz_planes);
             else
                 hipLaunchKernelGGL(k_target_grad<E>, dim3(blocks_of(a.rows)), dim3(256), 0, c.stream, a, word0, words, dz,
-                                   uint32_t(PLANES));
+                                   l.dz_planes);
             if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
             if (c.dhidden != nullptr) {
                 const ProductOut out{ws + l.dx, l.line, a.rows, l.line, a.scale, word0 > 0};

@@ -12,9 +12,11 @@
 // outer: the tile lies as 64 rows along m (or n), 64-byte pieces change places
 // by the row, and the transposing LDS read hands each lane its 4 elements along k.
 //
-// Wide operands: float32 matrices are split into three bfloat16 planes whose
-// sum they are to 2^-24, and the product is the sum of the six products of
-// planes that are not below that (`planes` = 3).
+// Wide operands: a matrix is the sum of planes of 16 bits each.  Float32 matrices
+// are split into three bfloat16 planes whose sum they are to 2^-24, and the
+// product is the sum of the six products of planes that are not below that
+// (kThreeByThree).  Or B alone has a second plane, of what the first leaves out
+// (kOneByTwo).
 #pragma once
 
 #include "elements.hpp"
@@ -22,7 +24,11 @@
 namespace adacomp {
 
 constexpr uint32_t kTileK = 64;      // the inner axis in LDS
-constexpr int kPlanePairs = 6;
+// Pairs of planes of a product: how many, and the planes of A and B, 4 bits each, smallest products first.
+struct PlanePairs {
+    uint32_t count, a, b;
+};
+constexpr PlanePairs kOneByOne{1, 0x0, 0x0}, kOneByTwo{2, 0x00, 0x10}, kThreeByThree{6, 0x021010, 0x201100};
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <typename E>
@@ -211,25 +217,22 @@ struct TileProduct {
 
     // The sum over k in [kbegin, kend) of every pair of planes.
     __device__ __forceinline__ void run(const Operand& a, const Operand& b, uint32_t m0, uint32_t n0, uint32_t kbegin,
-                                        uint32_t kend, uint32_t planes, E* lds) {
+                                        uint32_t kend, PlanePairs pairs, E* lds) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[i][j] = 0.f;
         const LoadA la(a, m0);
         const LoadB lb(b, n0);
-        const uint32_t steps = (kend - kbegin + kTileK - 1) / kTileK, total = planes == 3 ? steps * kPlanePairs : steps;
-        uint32_t k = kbegin, pair = 0;
+        const uint32_t total = (kend - kbegin + kTileK - 1) / kTileK * pairs.count;
+        uint32_t k = kbegin, left = 4 * (pairs.count - 1);
         auto request = [&](E* to) {
-            // smallest products first: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0)
-            const uint32_t pa = planes == 3 ? 0x021010u >> (4 * (5 - pair)) & 3u : 0;
-            const uint32_t pb = planes == 3 ? 0x201100u >> (4 * (5 - pair)) & 3u : 0;
-            la.request(a, pa, m0, k, kend, to);
-            lb.request(b, pb, n0, k, kend, to + TM * kTileK);
+            la.request(a, pairs.a >> left & 15u, m0, k, kend, to);
+            lb.request(b, pairs.b >> left & 15u, n0, k, kend, to + TM * kTileK);
             k += kTileK;
-            if (k >= kend) {
+            if (k >= kend) {   // the next pair; after the last one nothing is requested
                 k = kbegin;
-                ++pair;
+                left = left >= 4 ? left - 4 : 0;
             }
         };
         if (total > 0) request(lds);

@@ -16,12 +16,14 @@
 // products from dz (k_product).  A pass is three products for the gradients and
 // one for the loss, bound by the matrix cores.
 //
-// dz is rounded to the operands' 16 bits, as they are, for the matrix cores take no
-// wider ones: each term of the gradients' sums is off by at most half a step
-// of its type.  It is scaled by a power of two that brings the largest row
-// factor up to 2^14: half's smallest numbers would not hold a probability over the number
-// of rows.  float32 calls split every operand, dz too, into three bfloat16
-// planes (tile_product.hpp), and their products are as exact as float32's own.
+// dz is rounded to the operands' 16 bits, for the matrix cores take no wider
+// ones: each term of the gradients' sums is off by at most half a step of its
+// type, as the rounded results are, which many rows' errors add to like random ones.
+// Of few rows, where they need not, dz has a second plane of what the first leaves
+// out.  The rows' factors are divided by the largest of them and brought up to 2^14:
+// half's smallest numbers would not hold a probability over the number of rows, and equal
+// factors are exact.  float32 calls split every operand, dz too, into three
+// bfloat16 planes (tile_product.hpp), and their products are as exact as float32's own.
 #pragma once
 
 #include "sequence.hpp"
@@ -30,6 +32,7 @@
 namespace adacomp {
 
 constexpr uint32_t kLossMaxPicks = 1024;
+constexpr uint32_t kLossFewRows = 512;   // most rows whose dz has a second plane
 
 // Where a matrix of the caller's lies; T elements.
 struct LossMatrix {
@@ -46,8 +49,8 @@ struct LossArgs {
     float* lse;
     float* picked;              // [rows][picks]: z at the ids
     const float* dloss;
-    float* factor;              // [rows]: dloss / temperature of the rows that count, times the scale
-    float* scale;               // [2]: the scale and its reciprocal
+    float* factor;              // [rows]: dloss / temperature of the rows that count, over the largest, times 2^14
+    float* scale;               // [1]: what a result from dz has to be multiplied by
     float2* part;               // [tile of the vocabulary][rows]: largest logit in units of log 2, sum
     uint32_t rows, width, words, picks;
     float sharp;                // 1 / temperature
@@ -200,12 +203,13 @@ __device__ __forceinline__ void leave_dz(const P& p, const LossArgs& a, uint32_t
 // A piece of the vocabulary from word0 on; w is its operand.
 template <typename P, bool BACK>
 __global__ __launch_bounds__(P::THREADS) void k_logits(LossArgs a, Operand w, uint32_t word0, uint32_t tiles_m,
-                                                       uint32_t tiles_n, uint32_t planes, Operand dz, uint32_t tile0) {
+                                                       uint32_t tiles_n, PlanePairs pairs, Operand dz, uint32_t planes,
+                                                       uint32_t tile0) {
     extern __shared__ uint4 lds[];
     P p;
     const TilePlace t(blockIdx.x, tiles_m, tiles_n);
     const uint32_t m0 = t.m * P::TM, n0 = t.n * P::TN;
-    p.run(w, a.x, m0, n0, 0, w.inner, planes, reinterpret_cast<typename P::E*>(lds));
+    p.run(w, a.x, m0, n0, 0, w.inner, pairs, reinterpret_cast<typename P::E*>(lds));
     const bool whole = word0 + m0 + P::TM <= a.words;
     if (BACK) {
         if (whole) leave_dz<true>(p, a, word0, m0, n0, dz, planes);
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, uint32_t tiles) {
 
 // ---- backward ----
 
-// The scale, a power of two: 2^14 over the largest factor's own, from the rows that count.  One workgroup.
+// The rows' factors: 0 of those that do not count.  An infinite one leaves them all as they are.  One workgroup.
 __global__ __launch_bounds__(1024) void k_loss_scale(LossArgs a) {
     __shared__ float most[16];
     float m = 0.f;
@@ -308,14 +312,10 @@ __global__ __launch_bounds__(1024) void k_loss_scale(LossArgs a) {
     if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = m;
     __syncthreads();
     for (int i = 0; i < 16; ++i) m = fmaxf(m, most[i]);
-    int e = 0;
-    if (m > 0.f && m < __builtin_inff()) e = min(max(14 - ilogbf(m), -100), 100);
-    const float scale = ldexpf(1.f, e);
-    for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) a.factor[row] *= scale;
-    if (threadIdx.x == 0) {
-        a.scale[0] = scale;
-        a.scale[1] = ldexpf(1.f, -e);
-    }
+    const bool scaled = m > 0.f && m < __builtin_inff();
+    if (scaled)
+        for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) a.factor[row] = a.factor[row] / m * 16384.f;
+    if (threadIdx.x == 0) a.scale[0] = scaled ? m / 16384.f : 1.f;
 }
 
 // One element of dz in all planes.
@@ -372,7 +372,7 @@ struct ProductOut {
     void* p;              // [n][m], of T, or float32 partial sums [share][n][m]
     uint64_t stride;
     uint32_t rows, cols;  // n and m that are there
-    const float* scale;   // scale[1] is a factor of the result
+    const float* scale;   // a factor of the result
     bool add;             // partial sums: to what is there
 };
 
@@ -391,7 +391,7 @@ __device__ __forceinline__ void put_columns(T* row, uint32_t m, uint32_t cols, b
 
 // One product from dz: [n, m] = sum over k; shares of the inner axis where PARTIAL.
 template <typename P, typename T, bool PARTIAL>
-__global__ __launch_bounds__(P::THREADS) void k_product(Operand x, Operand y, uint32_t inner, uint32_t planes,
+__global__ __launch_bounds__(P::THREADS) void k_product(Operand x, Operand y, uint32_t inner, PlanePairs pairs,
                                                         uint32_t tiles_m, uint32_t tiles_n, uint32_t shares, ProductOut out) {
     extern __shared__ uint4 lds[];
     P p;
@@ -400,8 +400,8 @@ __global__ __launch_bounds__(P::THREADS) void k_product(Operand x, Operand y, ui
     const uint32_t m0 = t.m * P::TM, n0 = t.n * P::TN;
     const uint32_t each = (inner + shares * kTileK - 1) / (shares * kTileK) * kTileK;
     const uint32_t begin = min(share * each, inner), end = min(begin + each, inner);
-    p.run(x, y, m0, n0, begin, end, planes, reinterpret_cast<typename P::E*>(lds));
-    const float factor = PARTIAL ? 1.f : out.scale[1];
+    p.run(x, y, m0, n0, begin, end, pairs, reinterpret_cast<typename P::E*>(lds));
+    const float factor = PARTIAL ? 1.f : out.scale[0];
     const uint32_t lane = threadIdx.x % 64;
 #pragma unroll
     for (int j = 0; j < P::NT; ++j) {
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(256) void k_join_shares(const float* part, uint32_t
     FVec<4> v = 0.f;
 #pragma unroll 8
     for (uint32_t s = 0; s < shares; ++s) v += load_any<4>(part + (s * rows + row) * line + c);
-    v *= scale[1];
+    v *= scale[0];
     T* to = out + row * stride + c;
     if (c + 4 <= cols) {
         store_any<4>(to, from_float<T, 4>(v));
