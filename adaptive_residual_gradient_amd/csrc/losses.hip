@@ -82,7 +82,13 @@ HeadLayout head_layout(const adacomp_head& h, bool back) {
     };
     l.x = place(R * l.line * 2 * l.planes);
     l.w = place(uint64_t(l.piece) * l.line * 2 * l.planes);
-    l.part = place(back ? 0 : R * (up(V, kTileM[kTiny]) / kTileM[kTiny]) * 8);
+    uint64_t parts = 0;   // whether the weight is taken as it lies, in one piece, or copied
+    if (!back)
+        for (const uint64_t piece : {V, uint64_t(l.piece)}) {
+            const uint64_t side = kTileM[tile_of(piece, R)];
+            parts = std::max(parts, V / piece * up(piece, side) / side + up(V % piece, side) / side);
+        }
+    l.part = place(R * parts * 8);
     l.picked = place(back ? 0 : R * 4);
     if (back) {
         l.factor = place(R * 4);

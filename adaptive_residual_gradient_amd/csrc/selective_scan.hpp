@@ -318,7 +318,11 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmArgs a) {
             if (k + u >= a.chunks) continue;
             const uint32_t chunk = BACK ? a.chunks - 1 - (k + u) : k + u;
             a.ends[((b * a.chunks + chunk) * a.padded + n) * a.channels + c] = h;
-            h = __builtin_fmaf(__builtin_amdgcn_exp2f(sum[u] * a2), h, end[u]);
+            // not 0 and not infinite where the steps' own decays were neither: an infinite state times 0, or none
+            // times infinity, would be NaN
+            const float decay = __builtin_elementwise_minimum(
+                __builtin_elementwise_maximum(__builtin_amdgcn_exp2f(sum[u] * a2), __uint_as_float(1u)), 3.40282347e38f);
+            h = __builtin_fmaf(decay, h, end[u]);
         }
     }
     if (a.last != nullptr && n < a.states) a.last[place] = h;
