@@ -172,9 +172,9 @@ struct Loss {
     template <bool BACK>
     void logits(int tile, const Operand& w, uint32_t word0, const Operand& dz, uint32_t tile0) const {
         switch (tile) {
-            case kBig: return logits<TileProduct<E, 2, 4, 4, 2, false, false>, BACK>(w, word0, dz, tile0);
-            case kMid: return logits<TileProduct<E, 2, 2, 2, 2, false, false>, BACK>(w, word0, dz, tile0);
-            default: return logits<TileProduct<E, 2, 1, 1, 2, false, false>, BACK>(w, word0, dz, tile0);
+            case kBig: return logits<TileProduct<E, 2, 4, 4, 2, 2, false, false>, BACK>(w, word0, dz, tile0);
+            case kMid: return logits<TileProduct<E, 2, 2, 2, 2, 2, false, false>, BACK>(w, word0, dz, tile0);
+            default: return logits<TileProduct<E, 2, 1, 1, 2, 4, false, false>, BACK>(w, word0, dz, tile0);
         }
     }
     template <typename P, typename O, bool PARTIAL>
@@ -187,9 +187,9 @@ struct Loss {
     template <typename O, bool PARTIAL, bool YOUTER>
     void product(int tile, const Operand& x, const Operand& y, uint32_t inner, uint32_t shares, const ProductOut& out) const {
         switch (tile) {
-            case kBig: return product<TileProduct<E, 2, 4, 4, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
-            case kMid: return product<TileProduct<E, 2, 2, 2, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
-            default: return product<TileProduct<E, 2, 1, 1, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
+            case kBig: return product<TileProduct<E, 2, 4, 4, 2, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
+            case kMid: return product<TileProduct<E, 2, 2, 2, 2, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
+            default: return product<TileProduct<E, 2, 1, 1, 2, 4, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
         }
     }
 

@@ -2,9 +2,9 @@
 // A[m, k] B[n, k] in float32, of bfloat16 or half operands.
 //
 // A workgroup of WM x WN wavefronts forms TM x TN results, a wavefront MT x NT
-// blocks of 32 x 32 of them, in registers.  Steps of 64 of the inner axis lie in
-// two LDS buffers: while one is read, the next step's elements go straight from
-// memory into the other.
+// blocks of 32 x 32 of them, in registers.  Steps of 64 of the inner axis lie in LDS
+// buffers, one of which is read while the next steps' elements go straight
+// from memory into the others.
 //
 // An operand is read in either order.  K inner (rows of the inner axis): its
 // tile lies in LDS as rows of 64 elements, whose 16-byte pieces change places by
@@ -183,7 +183,9 @@ struct TileLoader {
     };
 };
 
-template <typename E_, int WM_, int WN_, int MT_, int NT_, bool AOUTER, bool BOUTER>
+// BUFFERS, a power of two: 2 of the large tiles; 4 of small ones, whose steps are over before the next one's
+// elements arrive.
+template <typename E_, int WM_, int WN_, int MT_, int NT_, int BUFFERS, bool AOUTER, bool BOUTER>
 struct TileProduct {
     typedef E_ E;
     static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
@@ -191,7 +193,8 @@ struct TileProduct {
     typedef TileLoader<E, AOUTER, TM, THREADS> LoadA;
     typedef TileLoader<E, BOUTER, TN, THREADS> LoadB;
     static constexpr uint32_t STEP = (TM + TN) * kTileK;   // elements of one buffer
-    static constexpr uint32_t LDS_BYTES = 2 * STEP * 2;
+    static constexpr uint32_t LDS_BYTES = BUFFERS * STEP * 2;
+    static constexpr int REQUESTS = LoadA::N + LoadB::N;   // a thread's, a step
 
     f32x16 acc[MT][NT];
     // the wavefront's first row and column of the tile
@@ -235,16 +238,21 @@ struct TileProduct {
                 left = left >= 4 ? left - 4 : 0;
             }
         };
-        if (total > 0) request(lds);
+        for (uint32_t step = 0; step + 1 < BUFFERS && step < total; ++step) request(lds + step * STEP);
         const typename LoadA::template Reader<MT> ra(row());
         const typename LoadB::template Reader<NT> rb(column());
         for (uint32_t step = 0; step < total; ++step) {
-            // this step's elements are there, and the other buffer has been read
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-            const E* ta = lds + (step & 1u) * STEP;
+            // This step's elements are there: of the later requests, those of BUFFERS - 2 steps, none has to be.  And
+            // the buffer before this one has been read, by every wavefront's own wait for its reads before the
+            // barrier.  (A fence would wait for every request.)
+            if (step + BUFFERS - 1 <= total)
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((BUFFERS - 2) * REQUESTS) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            const E* ta = lds + (step & (BUFFERS - 1)) * STEP;
             const E* tb = ta + TM * kTileK;
-            if (step + 1 < total) request(lds + (~step & 1u) * STEP);
+            if (step + BUFFERS - 1 < total) request(lds + ((step + BUFFERS - 1) & (BUFFERS - 1)) * STEP);
             part<0>(ra, rb, ta, tb);
             part<16>(ra, rb, ta, tb);
             part<32>(ra, rb, ta, tb);
