@@ -44,7 +44,7 @@ uint32_t shares_of(uint64_t m, uint64_t n, uint64_t k, uint32_t planes) {
 
 struct HeadLayout {
     uint32_t line, planes, dz_planes, piece, shares;   // line: a packed row's elements
-    uint64_t x, w, part, picked, factor, scale, dz, dx, bytes;   // byte offsets
+    uint64_t x, w, part, factor, scale, dz, dx, bytes;   // byte offsets
 };
 
 int check_head(const adacomp_head* h, uint32_t picks) {
@@ -89,7 +89,6 @@ HeadLayout head_layout(const adacomp_head& h, bool back) {
             parts = std::max(parts, V / piece * up(piece, side) / side + up(V % piece, side) / side);
         }
     l.part = place(R * parts * 8);
-    l.picked = place(back ? 0 : R * 4);
     if (back) {
         l.factor = place(R * 4);
             l.scale = place(4);
@@ -128,10 +127,9 @@ struct LossCall {
 };
 
 template <typename T, typename E, int PLANES>
-void pack(const void* from, uint64_t stride, uint64_t rows, const LossArgs& a, uint32_t line, const float* live, void* to,
-          hipStream_t s) {
+void pack(const void* from, uint64_t stride, uint64_t rows, const LossArgs& a, uint32_t line, void* to, hipStream_t s) {
     hipLaunchKernelGGL((k_pack<T, E, PLANES>), dim3(blocks_of(rows * (line / 8))), dim3(256), 0, s,
-                       static_cast<const T*>(from), stride, uint32_t(rows), a.width, line, live, static_cast<E*>(to));
+                       static_cast<const T*>(from), stride, uint32_t(rows), a.width, line, static_cast<E*>(to));
 }
 
 // An operand needs no copy where its rows are 16-byte aligned and end with a whole 16 bytes.
@@ -155,7 +153,7 @@ struct Loss {
     Operand weight(uint32_t word0, uint32_t words) const {
         const T* p = static_cast<const T*>(a.weight.p) + uint64_t(word0) * a.weight.stride;
         if (direct<T>(p, a.weight.stride, a.width)) return operand(p, a.weight.stride, words);
-        pack<T, E, PLANES>(p, a.weight.stride, words, a, l.line, nullptr, ws + l.w, c.stream);
+        pack<T, E, PLANES>(p, a.weight.stride, words, a, l.line, ws + l.w, c.stream);
         return operand(ws + l.w, l.line, words);
     }
     // Lines become the inner axis.
@@ -197,7 +195,7 @@ struct Loss {
         if (direct<T>(a.hidden.p, a.hidden.stride, a.width)) {
             a.x = operand(a.hidden.p, a.hidden.stride, a.rows);
         } else {
-            pack<T, E, PLANES>(a.hidden.p, a.hidden.stride, a.rows, a, l.line, nullptr, ws + l.x, c.stream);
+            pack<T, E, PLANES>(a.hidden.p, a.hidden.stride, a.rows, a, l.line, ws + l.x, c.stream);
             a.x = operand(ws + l.x, l.line, a.rows);
         }
         const bool whole = direct<T>(a.weight.p, a.weight.stride, a.width);
@@ -210,16 +208,17 @@ struct Loss {
             if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
             tiles += share_of(w.extent, kTileM[tile]);
         }
-        hipLaunchKernelGGL(k_picks<T>, dim3(share_of(uint64_t(a.rows) * a.picks, 4)), dim3(256), 0, c.stream, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        hipLaunchKernelGGL(k_loss, dim3(share_of(a.rows, 4)), dim3(256), 0, c.stream, a, tiles);
+        if (c.distil) {
+            hipLaunchKernelGGL(k_picks<T>, dim3(share_of(uint64_t(a.rows) * a.picks, 4)), dim3(256), 0, c.stream, a);
+            if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+        }
+        hipLaunchKernelGGL(k_loss<T>, dim3(share_of(a.rows, 4)), dim3(256), 0, c.stream, a, tiles);
         return launch_status();
     }
 
     int backward() {
-        hipLaunchKernelGGL(k_loss_scale, dim3(1), dim3(1024), 0, c.stream, a);
-        if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-        pack<T, E, PLANES>(a.hidden.p, a.hidden.stride, a.rows, a, l.line, a.factor, ws + l.x, c.stream);
+        hipLaunchKernelGGL((k_loss_start<T, E, PLANES>), dim3(1 + share_of(uint64_t(a.rows) * (l.line / 8), 1024)), dim3(1024), 0,
+                           c.stream, a, l.line, reinterpret_cast<E*>(ws + l.x));
         if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
         a.x = operand(ws + l.x, l.line, a.rows);
         for (uint32_t word0 = 0; word0 < a.words; word0 += l.piece) {
@@ -228,13 +227,11 @@ struct Loss {
             const Operand dz{ws + l.dz, l.piece, uint64_t(a.rows) * l.piece, a.rows, words};
             logits<true>(tile_of(words, a.rows), w, word0, dz, 0);
             if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
-            if (c.distil)
+            if (c.distil) {
                 hipLaunchKernelGGL(k_pick_grad<E>, dim3(share_of(a.rows, 4)), dim3(256), 0, c.stream, a, word0, words, dz,
                                    l.dz_planes);
-            else
-                hipLaunchKernelGGL(k_target_grad<E>, dim3(blocks_of(a.rows)), dim3(256), 0, c.stream, a, word0, words, dz,
-                                   l.dz_planes);
-            if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+                if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+            }
             if (c.dhidden != nullptr) {
                 const ProductOut out{ws + l.dx, l.line, a.rows, l.line, a.scale, word0 > 0};
                 product<float, true, false>(tile_of(l.line, a.rows, l.shares), turned(w, l.line, words), dz, words, l.shares,
@@ -268,7 +265,7 @@ int launch_loss(const LossCall& c, const HeadLayout& l) {
     a.teacher = c.teacher;
     a.loss = c.loss;
     a.lse = c.lse;
-    a.picked = c.distil ? c.picked : reinterpret_cast<float*>(ws + l.picked);
+    a.picked = c.picked;
     a.dloss = c.dloss;
     a.factor = reinterpret_cast<float*>(ws + l.factor);
     a.scale = reinterpret_cast<float*>(ws + l.scale);

@@ -9,10 +9,10 @@
 //
 // Forward is one product: a tile of 256 words leaves each row's largest logit and
 // sum of exponentials (k_logits<false>), which k_loss joins; the logits at the
-// targets or picks are dot products of their own (k_picks).  Backward takes a
+// targets or picks are dot products of their own (k_loss, k_picks).  Backward takes a
 // piece of the vocabulary at a time: the product again, whose tiles leave dz in
 // 16 bits (k_logits<true>), the target's or picks' elements put right from the
-// forward call's float32 values (k_target_grad, k_pick_grad), and the two
+// forward call's float32 values (put_targets, k_pick_grad), and the two
 // products from dz (k_product).  A pass is three products for the gradients and
 // one for the loss, bound by the matrix cores.
 //
@@ -67,18 +67,13 @@ __device__ __forceinline__ bool row_counts(const LossArgs& a, uint32_t row) {
 
 // ---- operands ----
 
-// A matrix as bfloat16 planes or padded rows: to [plane][rows][line], zeros behind the columns and,
-// where `live` says so, in whole rows.
+// Eight elements of a matrix as planes, or as a padded row: to [plane][rows][line], zeros behind the columns and,
+// of rows that are not live, everywhere.
 template <typename T, typename E, int PLANES>
-__global__ __launch_bounds__(256) void k_pack(const T* from, uint64_t stride, uint32_t rows, uint32_t cols, uint32_t line,
-                                              const float* live, E* to) {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-    const uint32_t per = line / 8;
-    const uint64_t row = i / per;
-    const uint32_t c = uint32_t(i % per) * 8;
-    if (row >= rows) return;
+__device__ __forceinline__ void pack_eight(const T* from, uint64_t stride, uint32_t rows, uint32_t cols, uint32_t line,
+                                           uint64_t row, uint32_t c, bool live, E* to) {
     FVec<8> v = 0.f;
-    if (live == nullptr || live[row] != 0.f) {
+    if (live) {
         const T* p = from + row * stride + c;
         if (c + 8 <= cols) {
             v = to_float<8, T>(load_any<8>(p));
@@ -100,6 +95,48 @@ __global__ __launch_bounds__(256) void k_pack(const T* from, uint64_t stride, ui
             v[k] = __builtin_isfinite(float(part[k])) ? rest : 0.f;   // an infinity is whole in the first plane
         }
     }
+}
+template <typename T, typename E, int PLANES>
+__global__ __launch_bounds__(256) void k_pack(const T* from, uint64_t stride, uint32_t rows, uint32_t cols, uint32_t line,
+                                              E* to) {
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t per = line / 8;
+    if (i / per < rows) pack_eight<T, E, PLANES>(from, stride, rows, cols, line, i / per, uint32_t(i % per) * 8, true, to);
+}
+
+// The rows' factors: 0 of those that do not count.  An infinite one leaves them all as they are.  One workgroup.
+__device__ __forceinline__ void row_factors(const LossArgs& a) {
+    __shared__ float most[16];
+    float m = 0.f;
+    for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) {
+        const float f = row_counts(a, row) ? a.dloss[row] * a.sharp : 0.f;
+        a.factor[row] = f;
+        m = fmaxf(m, fabsf(f));
+    }
+    for (int s = 32; s > 0; s /= 2) m = fmaxf(m, __shfl_xor(m, s));
+    if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = m;
+    __syncthreads();
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, most[i]);
+    const bool scaled = m > 0.f && m < __builtin_inff();
+    if (scaled)
+        for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) a.factor[row] = a.factor[row] / m * 16384.f;
+    if (threadIdx.x == 0) a.scale[0] = scaled ? m / 16384.f : 1.f;
+}
+
+// What the gradients start from: the factors, by the first workgroup, and the hidden states' rows that count, by the
+// others.
+template <typename T, typename E, int PLANES>
+__global__ __launch_bounds__(1024) void k_loss_start(LossArgs a, uint32_t line, E* to) {
+    if (blockIdx.x == 0) {
+        row_factors(a);
+        return;
+    }
+    const uint64_t i = uint64_t(blockIdx.x - 1) * 1024 + threadIdx.x;
+    const uint32_t per = line / 8;
+    const uint64_t row = i / per;
+    if (row >= a.rows) return;
+    pack_eight<T, E, PLANES>(static_cast<const T*>(a.hidden.p), a.hidden.stride, a.rows, a.width, line, row,
+                             uint32_t(i % per) * 8, row_counts(a, uint32_t(row)), to);
 }
 
 // ---- forward ----
@@ -200,6 +237,34 @@ __device__ __forceinline__ void leave_dz(const P& p, const LossArgs& a, uint32_t
     }
 }
 
+// One element of dz in all planes.
+template <typename E>
+__device__ __forceinline__ void put_dz(const Operand& dz, uint32_t planes, uint32_t row, uint32_t column, float v) {
+    E* out = static_cast<E*>(const_cast<void*>(dz.p)) + uint64_t(row) * dz.line + column;
+    for (uint32_t plane = 0; plane < planes; ++plane) {
+        const E part = E(v);
+        out[plane * dz.plane] = part;
+        v -= float(part);
+    }
+}
+
+// dz at the targets that are words of a tile, behind the tile's own stores: exp(z_t - lse) - 1 without the
+// difference of two numbers near 1.
+template <typename P>
+__device__ __forceinline__ void put_targets(const LossArgs& a, uint32_t word0, uint32_t m0, uint32_t n0, const Operand& dz,
+                                            uint32_t planes) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    for (uint32_t n = threadIdx.x; n < P::TN; n += P::THREADS) {
+        const uint32_t row = n0 + n;
+        if (row >= a.rows) continue;
+        const int64_t id = a.ids[row];
+        const float f = a.factor[row];
+        if (is_word(id, a.words) && uint64_t(id) - word0 - m0 < P::TM && f != 0.f)
+            put_dz<typename P::E>(dz, planes, row, uint32_t(id) - word0, expm1f(-a.loss[row]) * f);
+    }
+}
+
 // A piece of the vocabulary from word0 on; w is its operand.
 template <typename P, bool BACK>
 __global__ __launch_bounds__(P::THREADS) void k_logits(LossArgs a, Operand w, uint32_t word0, uint32_t tiles_m,
@@ -214,6 +279,7 @@ __global__ __launch_bounds__(P::THREADS) void k_logits(LossArgs a, Operand w, ui
     if (BACK) {
         if (whole) leave_dz<true>(p, a, word0, m0, n0, dz, planes);
         else leave_dz<false>(p, a, word0, m0, n0, dz, planes);
+        if (a.teacher == nullptr) put_targets<P>(a, word0, m0, n0, dz, planes);
     } else {
         float2* sums = reinterpret_cast<float2*>(lds);
         if (whole) leave_sums<true>(p, a, word0, m0, n0, tile0 + t.m, sums);
@@ -221,18 +287,10 @@ __global__ __launch_bounds__(P::THREADS) void k_logits(LossArgs a, Operand w, ui
     }
 }
 
-// z at the picks: a wavefront a pick.
+// z of one row at a word, by a wavefront.
 template <typename T>
-__global__ __launch_bounds__(256) void k_picks(LossArgs a) {
-    const uint64_t i = uint64_t(blockIdx.x) * 4 + threadIdx.x / 64;
-    if (i >= uint64_t(a.rows) * a.picks) return;
-    const uint32_t lane = threadIdx.x % 64;
-    const int64_t id = a.ids[i];
-    if (!is_word(id, a.words)) {
-        if (lane == 0) a.picked[i] = 0.f;
-        return;
-    }
-    const T* x = static_cast<const T*>(a.hidden.p) + i / a.picks * a.hidden.stride;
+__device__ __forceinline__ float logit_at(const LossArgs& a, uint64_t row, int64_t id, uint32_t lane) {
+    const T* x = static_cast<const T*>(a.hidden.p) + row * a.hidden.stride;
     const T* w = static_cast<const T*>(a.weight.p) + uint64_t(id) * a.weight.stride;
     constexpr int V = 16 / sizeof(T);
     float s = 0.f;
@@ -244,7 +302,18 @@ __global__ __launch_bounds__(256) void k_picks(LossArgs a) {
     }
     for (; c < a.width; ++c) s = __builtin_fmaf(float(x[c]), float(w[c]), s);   // the one lane at the rows' end
     for (int m = 32; m > 0; m /= 2) s += __shfl_xor(s, m);
-    if (lane == 0) a.picked[i] = s * a.sharp;
+    return s * a.sharp;
+}
+
+// z at the picks: a wavefront a pick.
+template <typename T>
+__global__ __launch_bounds__(256) void k_picks(LossArgs a) {
+    const uint64_t i = uint64_t(blockIdx.x) * 4 + threadIdx.x / 64;
+    if (i >= uint64_t(a.rows) * a.picks) return;
+    const uint32_t lane = threadIdx.x % 64;
+    const int64_t id = a.ids[i];
+    const float z = is_word(id, a.words) ? logit_at<T>(a, i / a.picks, id, lane) : 0.f;
+    if (lane == 0) a.picked[i] = z;
 }
 
 // p of a row's picks by one wavefront: the largest teacher logit and the sum of exponentials.
@@ -265,25 +334,34 @@ struct Teacher {
 };
 
 // A wavefront a row: the tiles' sums joined, and the loss.
+template <typename T>
 __global__ __launch_bounds__(256) void k_loss(LossArgs a, uint32_t tiles) {
     const uint32_t row = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
     if (row >= a.rows) return;
+    float target = 0.f;
+    const bool scored = a.teacher == nullptr && is_word(a.ids[row], a.words);
+    if (scored) target = logit_at<T>(a, row, a.ids[row], lane);
     float most = -__builtin_inff(), sum = 0.f;
     auto join = [&](float m, float s) {
         const float top = fmaxf(most, m), f0 = top == -__builtin_inff() ? 0.f : top;
         sum = sum * exp2f(most - f0) + s * exp2f(m - f0);
         most = top;
     };
-    for (uint32_t t = lane; t < tiles; t += 64) {
-        const float2 s = a.part[uint64_t(t) * a.rows + row];
-        join(s.x, s.y);
+    constexpr uint32_t U = 4;   // requested together
+    for (uint32_t t = lane; t < tiles; t += 64 * U) {
+        float2 s[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) s[u] = a.part[uint64_t(min(t + 64 * u, tiles - 1)) * a.rows + row];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u)
+            if (t + 64 * u < tiles) join(s[u].x, s[u].y);
     }
     for (int m = 32; m > 0; m /= 2) join(__shfl_xor(most, m), __shfl_xor(sum, m));
     const float lse = __builtin_fmaf(most, kLn2, __builtin_fmaf(most, kLn2Low, logf(sum)));   // most in units of log 2
     if (lane == 0) a.lse[row] = lse;
     float loss = 0.f;
     if (a.teacher == nullptr) {
-        if (is_word(a.ids[row], a.words)) loss = lse - a.picked[row];
+        if (scored) loss = lse - target;
     } else {
         const Teacher p(a, row, lane);
         for (uint32_t k = lane; k < a.picks; k += 64) {
@@ -298,46 +376,6 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, uint32_t tiles) {
 }
 
 // ---- backward ----
-
-// The rows' factors: 0 of those that do not count.  An infinite one leaves them all as they are.  One workgroup.
-__global__ __launch_bounds__(1024) void k_loss_scale(LossArgs a) {
-    __shared__ float most[16];
-    float m = 0.f;
-    for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) {
-        const float f = row_counts(a, row) ? a.dloss[row] * a.sharp : 0.f;
-        a.factor[row] = f;
-        m = fmaxf(m, fabsf(f));
-    }
-    for (int s = 32; s > 0; s /= 2) m = fmaxf(m, __shfl_xor(m, s));
-    if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = m;
-    __syncthreads();
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, most[i]);
-    const bool scaled = m > 0.f && m < __builtin_inff();
-    if (scaled)
-        for (uint32_t row = threadIdx.x; row < a.rows; row += 1024) a.factor[row] = a.factor[row] / m * 16384.f;
-    if (threadIdx.x == 0) a.scale[0] = scaled ? m / 16384.f : 1.f;
-}
-
-// One element of dz in all planes.
-template <typename E>
-__device__ __forceinline__ void put_dz(const Operand& dz, uint32_t planes, uint32_t row, uint32_t column, float v) {
-    E* out = static_cast<E*>(const_cast<void*>(dz.p)) + uint64_t(row) * dz.line + column;
-    for (uint32_t plane = 0; plane < planes; ++plane) {
-        const E part = E(v);
-        out[plane * dz.plane] = part;
-        v -= float(part);
-    }
-}
-
-// dz at the targets of a piece: exp(z_t - lse) - 1 without the difference of two numbers near 1.
-template <typename E>
-__global__ __launch_bounds__(256) void k_target_grad(LossArgs a, uint32_t word0, uint32_t words, Operand dz, uint32_t planes) {
-    const uint32_t row = blockIdx.x * 256 + threadIdx.x;
-    if (row >= a.rows) return;
-    const int64_t id = a.ids[row];
-    if (!is_word(id, a.words) || uint64_t(id) - word0 >= words || a.factor[row] == 0.f) return;
-    put_dz<E>(dz, planes, row, uint32_t(id) - word0, expm1f(-a.loss[row]) * a.factor[row]);
-}
 
 // dz at the picks of a piece, a wavefront a row.  A word that was picked twice has both its shares of p, from every
 // one of its picks.
