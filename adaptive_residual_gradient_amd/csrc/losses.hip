@@ -23,20 +23,22 @@ uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 uint32_t share_of(uint64_t n, uint32_t each) { return static_cast<uint32_t>((n + each - 1) / each); }
 uint32_t blocks_of(uint64_t items) { return static_cast<uint32_t>((items + 255) / 256); }
 
-// Tiles of the products: 256 x 256 by 8 wavefronts where they give most CUs one; else 128 x 128 by 4, two of which a
-// CU holds; for few rows, or where these leave half of the CUs without one, 64 x 64 by 2.
-enum { kBig, kMid, kTiny };
-constexpr uint32_t kTileM[3] = {256, 128, 64};   // words, or columns of a gradient
+// Tiles of the products, each by 8 wavefronts (small ones by fewer keep too few requests under way: 300 x 256
+// float32 over 4999 words 106 us forward and backward, by 4 wavefronts 114, by 2 with 64 x 64 tiles 122): 256 x 256
+// where they give most CUs one; else 128 x 128; for few rows, or where these leave half of the CUs without one,
+// 128 x 64.
+enum { kBig, kMid, kSmall };
+constexpr uint32_t kTileM[3] = {256, 128, 128};   // words, or columns of a gradient
 uint64_t tiles(uint64_t m, uint64_t n, uint64_t side) { return (m + side - 1) / side * ((n + side - 1) / side); }
 int tile_of(uint64_t m, uint64_t n, uint64_t shares = 1) {
-    if (n <= 64) return kTiny;
+    if (n <= 64) return kSmall;
     if (tiles(m, n, 256) * shares >= kCus * 3 / 4) return kBig;
-    return tiles(m, n, 128) * shares >= kCus / 2 ? kMid : kTiny;
+    return tiles(m, n, 128) * shares >= kCus / 2 ? kMid : kSmall;
 }
 // Shares of the inner axis of a product into partial sums: for one tile a CU where 256 x 256 tiles are enough for a
 // quarter of them, else for two of 128 x 128.
 uint32_t shares_of(uint64_t m, uint64_t n, uint64_t k, uint32_t planes) {
-    const uint64_t big = tiles(m, n, 256), small = std::max<uint64_t>(tiles(m, n, n <= 64 ? 64 : 128), 1);
+    const uint64_t big = tiles(m, n, 256), small = std::max<uint64_t>(tiles(m, n, 128), 1);
     const uint64_t want = big >= kCus / 4 ? (kCus + big - 1) / big : (2 * kCus + small - 1) / small;
     const uint64_t most = (k + 255) / 256 * (planes == 3 ? 4 : planes);   // 256 of the inner axis, or as much work in planes
     return static_cast<uint32_t>(std::max<uint64_t>(std::min<uint64_t>({want, most, 64}), 1));
@@ -171,8 +173,8 @@ struct Loss {
     void logits(int tile, const Operand& w, uint32_t word0, const Operand& dz, uint32_t tile0) const {
         switch (tile) {
             case kBig: return logits<TileProduct<E, 2, 4, 4, 2, 2, false, false>, BACK>(w, word0, dz, tile0);
-            case kMid: return logits<TileProduct<E, 2, 2, 2, 2, 2, false, false>, BACK>(w, word0, dz, tile0);
-            default: return logits<TileProduct<E, 2, 1, 1, 2, 4, false, false>, BACK>(w, word0, dz, tile0);
+            case kMid: return logits<TileProduct<E, 4, 2, 1, 2, 2, false, false>, BACK>(w, word0, dz, tile0);
+            default: return logits<TileProduct<E, 4, 2, 1, 1, 4, false, false>, BACK>(w, word0, dz, tile0);
         }
     }
     template <typename P, typename O, bool PARTIAL>
@@ -186,8 +188,8 @@ struct Loss {
     void product(int tile, const Operand& x, const Operand& y, uint32_t inner, uint32_t shares, const ProductOut& out) const {
         switch (tile) {
             case kBig: return product<TileProduct<E, 2, 4, 4, 2, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
-            case kMid: return product<TileProduct<E, 2, 2, 2, 2, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
-            default: return product<TileProduct<E, 2, 1, 1, 2, 4, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
+            case kMid: return product<TileProduct<E, 4, 2, 1, 2, 2, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
+            default: return product<TileProduct<E, 4, 2, 1, 1, 4, true, YOUTER>, O, PARTIAL>(x, y, inner, shares, out);
         }
     }
 
