@@ -166,10 +166,16 @@ SsmLayout ssm_layout(const adacomp_ssm_shape& s, bool back) {
     l.nb = s.states <= 8 ? 8 : kSsmBlock;
     l.padded = (s.states + l.nb - 1) / l.nb * l.nb;
     l.groups = (s.channels + 63) / 64;
-    // Chunks: enough for 4 wavefronts a SIMD, of 64 steps or more.
+    // Chunks: for 4 wavefronts a SIMD, of 32 steps or more; where these leave less than 2, for 2, of 16 or more; where
+    // these leave less than 1, for 1, of 8 or more (forward of 1 x 2048 x 2048: 77 us, of 64 steps or more 105, of 16 83;
+    // of 2 x 300 x 1024: 37 us, of 32 or more 53).
     const uint64_t waves = std::max<uint64_t>(uint64_t(s.batch) * l.groups * (l.padded / l.nb), 1);
-    uint64_t chunks = std::min<uint64_t>((4096 + waves - 1) / waves, (s.length + 63) / 64);
-    chunks = std::max<uint64_t>(chunks, 1);
+    uint64_t chunks = 1;
+    for (const uint64_t least : {32, 16, 8}) {
+        const uint64_t want = 128 * least;   // 4, 2 and 1 a SIMD
+        chunks = std::max<uint64_t>(std::min<uint64_t>((want + waves - 1) / waves, (s.length + least - 1) / least), chunks);
+        if (chunks * waves >= want / 2) break;
+    }
     const uint64_t steps = ((s.length + chunks - 1) / chunks + kSsmKeep - 1) / kSsmKeep * kSsmKeep;
     l.steps = static_cast<uint32_t>(std::max<uint64_t>(steps, kSsmKeep));
     l.chunks = static_cast<uint32_t>(std::max<uint64_t>((s.length + l.steps - 1) / l.steps, 1));
