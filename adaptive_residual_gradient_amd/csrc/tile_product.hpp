@@ -8,7 +8,7 @@
 //
 // An operand is read in either order.  K inner (rows of the inner axis): its
 // tile lies in LDS as rows of 64 elements, whose 16-byte pieces change places by
-// the row, so that the 8 lanes of a cycle find 8 different bank groups.  K
+// the row, so that the 16 lanes of a cycle find 16 different bank groups.  K
 // outer: the tile lies as 64 rows along m (or n), 64-byte pieces change places
 // by the row, and the transposing LDS read hands each lane its 4 elements along k.
 //
@@ -100,7 +100,7 @@ struct TileLoader {
     uint32_t k[N];        // the piece's place on the inner axis
     // Where piece c of a line lies.
     static __device__ __forceinline__ uint32_t place(uint32_t line, uint32_t c) {
-        if (!OUTER) return c ^ (line & 7u);
+        if (!OUTER) return c ^ (line >> 1 & 7u);   // 16 lines' pieces lie in the 64 banks once
         const uint32_t turn = ROWS >= 256 ? (line & 3u) | (line >> 1 & 4u) : ROWS >= 128 ? line & 3u : line >> 1 & 1u;
         return c ^ turn << 2;
     }

@@ -58,10 +58,15 @@ struct LossArgs {
 
 __device__ __forceinline__ bool is_word(int64_t id, uint32_t words) { return uint64_t(id) < words; }
 
-// Whether a row has a word of the vocabulary among its picks.
+// Whether a row has a word of the vocabulary among its picks, which are requested 8 together.
 __device__ __forceinline__ bool row_counts(const LossArgs& a, uint32_t row) {
-    for (uint32_t k = 0; k < a.picks; ++k)
-        if (is_word(a.ids[uint64_t(row) * a.picks + k], a.words)) return true;
+    const int64_t* ids = a.ids + uint64_t(row) * a.picks;
+    for (uint32_t k = 0; k < a.picks; k += 8) {
+        bool any = false;
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u) any |= is_word(ids[min(k + u, a.picks - 1)], a.words);
+        if (any) return true;
+    }
     return false;
 }
 
