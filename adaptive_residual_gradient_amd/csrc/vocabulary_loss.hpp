@@ -204,7 +204,7 @@ __device__ __forceinline__ Eight<E> eight_rows(Four<E> low, Four<E> high) {
 
 // dz of a tile, scaled, into [plane][rows][line]: columns from the piece's first word on, zeros behind the last.
 // One plane's exponentials take one multiply-add before them, whose rounding is far below the type's; three planes'
-// are float32's own.  A row that does not count, whose lse may be anything, gives exp(0) times 0.
+// are float32's own.  A row whose factor is 0, whose lse may be anything, gives 0 times 0.
 template <bool WHOLE, typename P>
 __device__ __forceinline__ void leave_dz(const P& p, const LossArgs& a, uint32_t word0, uint32_t m0, uint32_t n0,
                                          const Operand& dz, uint32_t planes) {
@@ -215,7 +215,7 @@ __device__ __forceinline__ void leave_dz(const P& p, const LossArgs& a, uint32_t
     for (int j = 0; j < P::NT; ++j) {
         const uint32_t row = n0 + p.column() + j * 32 + lane % 32;
         const bool on = row < a.rows;   // the lane 32 away has the same row
-        const float f = on ? a.factor[row] : 0.f, lse = f != 0.f ? a.lse[row] : 0.f, from = lse * kLog2e;
+        const float f = on ? a.factor[row] : 0.f, lse = f != 0.f ? a.lse[row] : 1e30f, from = lse * kLog2e;
         E* out = static_cast<E*>(const_cast<void*>(dz.p)) + uint64_t(on ? row : 0) * dz.line;
 #pragma unroll
         for (int i = 0; i < P::MT; ++i)

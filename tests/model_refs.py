@@ -255,8 +255,13 @@ def loss(hidden, weight, ids, teacher=None, temperature=1.0, dloss=None, dtype=t
     edz = edz + (dz.abs() + edz) * half + 4 * U * dz.abs()
     dz = dz * f[:, None]
     # what is below the smallest number of the scaled dz
-    edz = edz * f.abs()[:, None] + (f.abs().max() * 2.0 ** -38 if dtype == torch.float16 else 0.0)
+    most = f.abs().max()
+    edz = edz * f.abs()[:, None] + (most * 2.0 ** -38 if dtype == torch.float16 else 0.0)
+    # and of float32's: an exponential below 2^-126 may be taken for 0, which leaves out |f| 2^-126 of dz; so may the
+    # planes of dz, and the products and sums of terms, which are formed of dz / most 2^14, so 2^-126 2^-14 most each
+    tiny = most * 2.0 ** -140
+    edz = edz + f.abs()[:, None] * 2.0 ** -126 + 3 * tiny
     edz = torch.where(used[:, None], edz, zero)
-    out["dhidden"] = (dz @ weight, edz @ weight.abs() + (terms(V) + 20 * U) * (dz.abs() @ weight.abs()))
-    out["dweight"] = (dz.t() @ x, edz.t() @ x.abs() + (terms(R) + 20 * U) * (dz.abs().t() @ x.abs()))
+    out["dhidden"] = (dz @ weight, edz @ weight.abs() + (terms(V) + 20 * U) * (dz.abs() @ weight.abs()) + 12 * V * tiny)
+    out["dweight"] = (dz.t() @ x, edz.t() @ x.abs() + (terms(R) + 20 * U) * (dz.abs().t() @ x.abs()) + 12 * R * tiny)
     return out

@@ -150,6 +150,16 @@ def test_sharp_rows(dtype):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("picks", [0, 3])
+def test_rows_of_weight_zero(picks, dtype):
+    """Rows that count in the loss and whose gradient is 0, among logits whose exponentials overflow: a loss mask."""
+    c = Case(90, 64, 600, TYPES[dtype], picks=picks, scale=100.0)
+    c.dloss[::2] = 0
+    c.check()
+    assert not c.dh[::2].any()
+
+
 def test_teacher_without_probability():
     """Teacher logits of -infinity have no part."""
     c = Case(40, 40, 300, torch.float32, picks=6)
