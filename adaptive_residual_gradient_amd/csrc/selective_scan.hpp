@@ -6,12 +6,12 @@
 //   dc_n = sum r h_n,  db_n = sum l_n u  (over channels),  du = sum_n l_n b_n,
 //   q_n = f_n h_n(before),  ds = sum_n q_n a_n + du x,  da_n = sum q_n s,  dx = du s + d r
 //
-// The exponentials and the states' updates bound it, not the memory: forward 5
-// instructions for every step, channel and state, one of them an exponential,
-// and backward 17.  So a lane has one channel and a block of its states in
-// registers, nothing is reduced across lanes on the way to y, and b and c, which
-// all channels share, come through scalar registers: a kernel before lays them
-// out as float32 rows (k_ssm_rows).
+// The exponentials and the states' updates bound it, not the memory: forward takes
+// an exponential and four multiplies and adds for every step, channel and state,
+// backward an exponential and about 16.  So a lane has one channel and a block of
+// its states in registers, nothing is reduced across lanes on the way to y, and b
+// and c, which all channels share, come through scalar registers: a kernel before
+// lays them out as float32 rows (k_ssm_rows).
 //
 // A long sequence is cut into chunks, for there are too few channels to fill the
 // chip.  A first pass forms each chunk's states from 0 (k_ssm_forward, ENDS), a
@@ -19,12 +19,18 @@
 // Then the chunks run on their own.  Backward does the same with f.
 //
 // Backward needs the states of every step.  Forward keeps every 8th, and a
-// block of 8 steps is formed again in registers: 8 states a wavefront, whose
-// decays and states of 8 steps just fit, so the states' blocks of one channel
-// are different wavefronts, which add up du and the like through LDS.  The sums over
-// channels of db and dc are formed by exchanging halves of the values with
-// halves of the lanes: 16 values of 64 lanes take 33 instructions a step, not
-// the 192 of 16 reductions.
+// block of 8 steps is formed again in registers: 4 states a wavefront, whose
+// decays and states of 8 steps leave room for several wavefronts a SIMD.  A
+// workgroup is 64 channels and all their states' blocks, which share s, u and r
+// and add up du, ds and y through LDS.  The sums over channels of db and dc are
+// formed by exchanging halves of the values with halves of the lanes, until
+// each of the 64 lanes has one of the 64 sums of a block of 8 steps.
+//
+// 8 x 2048 x 2048 bf16, 16 states, gated: forward 148 us for the chunks' ends,
+// 12 to join them and 166 for y; backward 148, 11 and 479, and 29 us for
+// the joined sums of db, dc, da and dd.  y takes 42 cycles of a SIMD for a
+// wavefront's step and state at 2.1 GHz, of which its instructions issue in 28;
+// the memory's share, 0.5 GB forward, would be 90 us.
 #pragma once
 
 #include "sequence.hpp"

@@ -17,6 +17,13 @@
 // product is the sum of the six products of planes that are not below that
 // (kThreeByThree).  Or B alone has a second plane, of what the first leaves out
 // (kOneByTwo).
+//
+// The clock under load bounds the large tiles: 8192 x 50176 x 2048 bf16 with the
+// losses' epilogue takes 1560 to 1670 us (1.08 to 1.01 PFLOP/s); the library's plain product of
+// such sizes reaches 1.36.  Neither LDS, whose reads have no bank conflicts, nor the waits
+// show: 4 wavefronts of 4 x 4 blocks, which read a third less of LDS, with each part's
+// elements read during the products of the part before, take 1% less
+// there and 2 to 4% more where the inner axis is 1024, for nothing runs beside their epilogue.
 #pragma once
 
 #include "elements.hpp"

@@ -586,9 +586,12 @@ int adacomp_causal_conv_workspace_bytes(const adacomp_conv_shape* shape, uint64_
  *   h_n <- exp(s_t * a_n) * h_n + s_t * x_t * b_t,n
  *   y_t = (sum_n c_t,n * h_n + d * x_t) * (z_t / (1 + exp(-z_t)) with z, else 1)
  * in float32 whatever the type, y rounded once.  Long sequences are cut into
- * chunks whose decays exp(a_n * sum s_t) are formed from the sum.
- * ERR_TOO_LARGE: as for the gated scan's sizes and strides, or states past
- * ADACOMP_SCAN_MAX_STATES. */
+ * chunks whose decays exp(a_n * sum s_t) are formed from the sum.  (Where a state
+ * is infinite they are taken into 2^-149 .. the largest float32 number: a product of 0 and
+ * infinity then comes from a step's own decay alone.)
+ * ERR_TOO_LARGE: as for the gated scan's sizes and strides, states past
+ * ADACOMP_SCAN_MAX_STATES, or 2^32 work-items and more (one for each step and state of b
+ * and c, and one for each channel, state and sequence among them). */
 #define ADACOMP_SCAN_MAX_STATES 64u
 #define ADACOMP_SCAN_KEEP 8u   /* a state of every so many steps is kept for the gradients */
 typedef struct adacomp_ssm_shape {
@@ -670,14 +673,15 @@ int adacomp_head_workspace_bytes(const adacomp_head* head, uint32_t picks, int b
 /* Softmax cross entropy: lse = log sum_v exp(z_v), loss = lse - z_target.
  *   targets    device int64[rows]; a row whose target is no word (negative, or past the
  *              vocabulary) does not count: its loss and gradients are 0.
- *   loss, lse  [rows] float32 outputs.
+ *   loss, lse  [rows] float32 outputs; lse also of rows that do not count, whatever they hold.
  *   ws         16-byte aligned; no initial contents required. */
 int adacomp_linear_cross_entropy(const adacomp_head* head, const int64_t* targets, float* loss,
                                  float* lse, void* ws, uint64_t ws_bytes, void* stream);
 
 /* Its gradients, with dz_v = (exp(z_v - lse) - [v = target]) * dloss:
  *   dhidden = dz weight,  dweight = dz^T hidden
- * dz rounded once to the type (float32: to 2^-23) after a scaling by a power of two.
+ * dz is divided by the largest |dloss| and rounded once to the type; float32, and 16 bits of at
+ * most 512 rows, have further numbers of what that leaves out (float32: 2^-23 of dz).
  *   loss, lse  as the forward call wrote them;  dloss  [rows] float32.
  *   dhidden    nullable [rows, width] output, dhidden_stride elements from row to row.
  *   dweight    nullable [vocabulary, width] output.
