@@ -46,7 +46,7 @@ uint32_t shares_of(uint64_t m, uint64_t n, uint64_t k, uint32_t planes) {
 
 struct HeadLayout {
     uint32_t line, planes, dz_planes, piece, shares;   // line: a packed row's elements
-    uint64_t x, w, part, factor, scale, dz, dx, bytes;   // byte offsets
+    uint64_t x, w, part, factor, scale, counts, dz, dx, bytes;   // byte offsets
 };
 
 int check_head(const adacomp_head* h, uint32_t picks) {
@@ -93,7 +93,8 @@ HeadLayout head_layout(const adacomp_head& h, bool back) {
     l.part = place(R * parts * 8);
     if (back) {
         l.factor = place(R * 4);
-            l.scale = place(4);
+        l.scale = place(4);
+        l.counts = place(R * 4);
         l.dz = place(R * l.piece * 2 * l.dz_planes);
         l.shares = shares_of(h.width, R, l.piece, l.dz_planes);
         l.dx = place(uint64_t(l.shares) * R * l.line * 4);
@@ -219,6 +220,10 @@ struct Loss {
     }
 
     int backward() {
+        if (c.distil) {
+            hipLaunchKernelGGL(k_row_counts, dim3(share_of(a.rows, 4)), dim3(256), 0, c.stream, a);
+            if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
+        }
         hipLaunchKernelGGL((k_loss_start<T, E, PLANES>), dim3(1 + share_of(uint64_t(a.rows) * (l.line / 8), 1024)), dim3(1024), 0,
                            c.stream, a, l.line, reinterpret_cast<E*>(ws + l.x));
         if (launch_status() != ADACOMP_OK) return ADACOMP_ERR_HIP;
@@ -271,6 +276,7 @@ int launch_loss(const LossCall& c, const HeadLayout& l) {
     a.dloss = c.dloss;
     a.factor = reinterpret_cast<float*>(ws + l.factor);
     a.scale = reinterpret_cast<float*>(ws + l.scale);
+    a.counts = reinterpret_cast<uint32_t*>(ws + l.counts);
     a.part = reinterpret_cast<float2*>(ws + l.part);
     a.rows = uint32_t(h.rows);
     a.width = h.width;

@@ -51,6 +51,7 @@ struct LossArgs {
     const float* dloss;
     float* factor;              // [rows]: dloss / temperature of the rows that count, over the largest, times 2^14
     float* scale;               // [1]: what a result from dz has to be multiplied by
+    uint32_t* counts;           // [rows], backward of the distillation: whether a row counts
     float2* part;               // [tile of the vocabulary][rows]: largest logit in units of log 2, sum
     uint32_t rows, width, words, picks;
     float sharp;                // 1 / temperature
@@ -58,16 +59,19 @@ struct LossArgs {
 
 __device__ __forceinline__ bool is_word(int64_t id, uint32_t words) { return uint64_t(id) < words; }
 
-// Whether a row has a word of the vocabulary among its picks, which are requested 8 together.
+// Whether a row's target is a word, or any of its picks.
 __device__ __forceinline__ bool row_counts(const LossArgs& a, uint32_t row) {
-    const int64_t* ids = a.ids + uint64_t(row) * a.picks;
-    for (uint32_t k = 0; k < a.picks; k += 8) {
-        bool any = false;
-#pragma unroll
-        for (uint32_t u = 0; u < 8; ++u) any |= is_word(ids[min(k + u, a.picks - 1)], a.words);
-        if (any) return true;
-    }
-    return false;
+    return a.teacher ? a.counts[row] != 0 : is_word(a.ids[row], a.words);
+}
+// The picks' part of that, a wavefront a row.  (By the one workgroup that needs it of every row: 4096 rows of 64 picks
+// 50 us.)
+__global__ __launch_bounds__(256) void k_row_counts(LossArgs a) {
+    const uint32_t row = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
+    if (row >= a.rows) return;
+    bool any = false;
+    for (uint32_t k = lane; k < a.picks; k += 64) any |= is_word(a.ids[uint64_t(row) * a.picks + k], a.words);
+    const bool counts = __any(any);
+    if (lane == 0) a.counts[row] = counts;
 }
 
 // ---- operands ----
