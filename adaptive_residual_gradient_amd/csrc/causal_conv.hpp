@@ -11,9 +11,10 @@
 // workgroup's stretches in LDS, written as one partial row a workgroup and
 // joined in float64 by a second kernel.
 //
-// Memory bounds both directions: 8 x 4096 x 2048 bf16 of 4 taps takes 53 to 58 us
-// forward (5.1 to 4.7 TB/s), 87 to 98 us backward (4.6 to 4.1 TB/s) and 7 us for the
-// rows joined; a copy of 1 GB reaches 5.1 TB/s.
+// Memory bounds both directions: 8 x 4096 x 2048 bf16 of 4 taps takes 48 us
+// forward (5.6 TB/s), 94 us backward (4.3 TB/s) and 7 us for the rows joined.  64 x 2048
+// of one step take 4.4 us, most of it the round trips to the memory: all loads
+// are requested together, the kept steps' among them (6.1 us with those behind the results).
 #pragma once
 
 #include "sequence.hpp"
@@ -21,7 +22,7 @@
 namespace adacomp {
 
 // Steps of a thread forward: the first of them that leaves enough threads (8 x 4096 x 2048 bf16, 4 taps, in us: 8
-// steps 70, 12 63, 16 58, 24 53.5, 32 53).
+// steps 70, 12 63, 16 58, 24 53.5, 32 53, before the weights came in whole vectors).
 constexpr uint32_t kConvRows[3] = {32, 12, 4};
 constexpr uint32_t kConvThreads = 256;
 // Partial rows of the weight's gradient: 3 wavefronts a SIMD, which the registers hold (8 x 4096 x 2048 bf16
@@ -65,6 +66,16 @@ __device__ __forceinline__ float conv_gate(float p) {
 // The weights of a thread's channels by tap, those of the KT - taps taps that are not there 0.
 template <int KT, int VW>
 __device__ __forceinline__ void conv_weights(const ConvArgs& a, uint32_t c, FVec<VW> (&w)[KT]) {
+    if (KT <= 4) {   // their own kernels: KT taps of VW channels, which lie together
+        FVec<VW> all[KT];
+#pragma unroll
+        for (int k = 0; k < KT; ++k) all[k] = load_any<VW>(a.weight + uint64_t(c) * KT + k * VW);
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int v = 0; v < VW; ++v) w[k][v] = all[(v * KT + k) / VW][(v * KT + k) % VW];
+        return;
+    }
     const uint32_t skip = KT - a.taps;
 #pragma unroll
     for (int k = 0; k < KT; ++k)
@@ -110,15 +121,24 @@ __device__ __forceinline__ uint32_t conv_workgroup() {
 template <typename T, int VW, int KT, int ROWS>
 __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, bool silu) {
     typedef typename Packed<T, VW>::V V;
-    const uint64_t i = uint64_t(conv_workgroup()) * kConvThreads + threadIdx.x;
-    const uint32_t r = uint32_t(i % a.lanes);
-    const uint64_t unit = i / a.lanes;
-    const uint32_t piece = uint32_t(unit % a.pieces), b = uint32_t(unit / a.pieces);
+    const uint32_t i = conv_workgroup() * kConvThreads + threadIdx.x;   // fewer than 2^32
+    const uint32_t r = i % a.lanes, unit = i / a.lanes, piece = unit % a.pieces, b = unit / a.pieces;
     if (b >= a.batch) return;
     const uint32_t c = min(r * VW, a.channels - VW);
     const uint64_t n = steps_of(a.lengths, a.length, b), t0 = uint64_t(piece) * ROWS;
     const int steps = int(t0 + ROWS < a.length ? ROWS : a.length - t0);   // of the tensor
     const int live = t0 < n ? int(n - t0 < uint64_t(ROWS) ? n - t0 : ROWS) : 0;   // of the sequence
+    // the steps before step n, requested with the others; [j]: KT - 1 - j steps before it
+    const bool keeps = piece == 0 && a.state_out != nullptr;
+    V kept[KT > 1 ? KT - 1 : 1];
+    if (keeps)
+#pragma unroll
+        for (int j = 0; j < KT - 1; ++j) {
+            const uint32_t back = KT - 1 - j;
+            if (back >= a.taps) continue;
+            if (n >= back) kept[j] = load_any<VW>(view_at<T>(a.x, b, n - back, c));
+            else kept[j] = conv_before<T, VW>(a, b, c, uint32_t(back - n));
+        }
     if (live > 0) {
         V raw[KT - 1 + ROWS];
         const T* p = view_at<T>(a.x, b, t0, c);
@@ -159,15 +179,11 @@ __global__ __launch_bounds__(kConvThreads) void k_conv(ConvArgs a, bool silu) {
         }
     }
     for (int u = live; u < steps; ++u) store_any<VW>(view_at<T>(a.y, b, t0 + u, c), V{});
-    if (piece == 0 && a.state_out != nullptr) {
+    if (keeps) {
         T* out = static_cast<T*>(a.state_out) + uint64_t(b) * (a.taps - 1) * a.channels + c;
-        for (uint32_t j = 1; j < a.taps; ++j) {   // the step `back` before step n
-            const uint32_t back = a.taps - j;
-            V v;
-            if (n >= back) v = load_any<VW>(view_at<T>(a.x, b, n - back, c));
-            else v = conv_before<T, VW>(a, b, c, uint32_t(back - n));
-            store_any<VW>(out + uint64_t(j - 1) * a.channels, v);
-        }
+#pragma unroll
+        for (int j = 0; j < KT - 1; ++j)
+            if (uint32_t(j) >= KT - a.taps) store_any<VW>(out + uint64_t(j - (KT - a.taps)) * a.channels, kept[j]);
     }
 }
 

@@ -27,7 +27,7 @@
 // each of the 64 lanes has one of the 64 sums of a block of 8 steps.
 //
 // 8 x 2048 x 2048 bf16, 16 states, gated: forward 148 us for the chunks' ends,
-// 12 to join them and 166 for y; backward 148, 11 and 479, and 29 us for
+// 12 to join them and 166 for y; backward 148, 11 and 479, and 25 us for
 // the joined sums of db, dc, da and dd.  The vector units are busy 63% of the
 // forward ends' time, 69% of y's, 73% of the backward ends' and 88% of the
 // gradients', which take 26 vector instructions a step and state.
@@ -89,13 +89,12 @@ __device__ __forceinline__ float logistic(float v) {
 // b and c as float32 rows of whole blocks, zeros behind the states.
 template <typename T>
 __global__ __launch_bounds__(256) void k_ssm_rows(SsmArgs a) {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-    const uint32_t n = uint32_t(i % a.padded), which = uint32_t(i / a.padded) & 1u;
-    const uint64_t row = i / (2 * a.padded), b = row / a.length, t = row % a.length;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x;   // fewer than 2^32, as in the kernels below
+    const uint32_t n = i % a.padded, which = i / a.padded & 1u;
+    const uint32_t row = i / (2 * a.padded), b = row / uint32_t(a.length), t = row % uint32_t(a.length);
     if (b >= a.batch) return;
     float v = 0.f;
-    if (n < a.states && t < steps_of(a.lengths, a.length, uint32_t(b)))
-        v = float(*view_at<T>(which ? a.c : a.b, uint32_t(b), t, n));
+    if (n < a.states && t < steps_of(a.lengths, a.length, b)) v = float(*view_at<T>(which ? a.c : a.b, b, t, n));
     a.rows[i] = v;
 }
 
@@ -310,25 +309,38 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmArgs a) {
         a2 = a.a[uint64_t(c) * a.states + n] * kLog2e;
         if (a.h0 != nullptr) h = a.h0[place];
     }
-    constexpr uint32_t U = 16;   // chunks requested together
-    for (uint32_t k = 0; k < a.chunks; k += U) {
-        float end[U], sum[U];
+    constexpr uint32_t U = 16;   // chunks requested together, while the ones before are joined
+    float* const ends = a.ends + (b * a.chunks * a.padded + n) * a.channels + c;
+    const float* const sums = a.sums + b * a.chunks * a.channels + c;
+    const uint64_t step = uint64_t(a.padded) * a.channels;
+    float end[U], sum[U];
+    auto request = [&](uint32_t k) {
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) {
             const uint32_t at = min(k + u, a.chunks - 1), chunk = BACK ? a.chunks - 1 - at : at;
-            end[u] = a.ends[((b * a.chunks + chunk) * a.padded + n) * a.channels + c];
-            sum[u] = a.sums[(b * a.chunks + chunk) * a.channels + c];
+            end[u] = ends[chunk * step];
+            sum[u] = sums[uint64_t(chunk) * a.channels];
         }
+    };
+    request(0);
+    for (uint32_t k = 0; k < a.chunks; k += U) {
+        float now[U], s[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            now[u] = end[u];
+            s[u] = sum[u];
+        }
+        if (k + U < a.chunks) request(k + U);
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) {
             if (k + u >= a.chunks) continue;
             const uint32_t chunk = BACK ? a.chunks - 1 - (k + u) : k + u;
-            a.ends[((b * a.chunks + chunk) * a.padded + n) * a.channels + c] = h;
+            ends[chunk * step] = h;
             // not 0 and not infinite where the steps' own decays were neither: an infinite state times 0, or none
             // times infinity, would be NaN
             const float decay = __builtin_elementwise_minimum(
-                __builtin_elementwise_maximum(__builtin_amdgcn_exp2f(sum[u] * a2), __uint_as_float(1u)), 3.40282347e38f);
-            h = __builtin_fmaf(decay, h, end[u]);
+                __builtin_elementwise_maximum(__builtin_amdgcn_exp2f(s[u] * a2), __uint_as_float(1u)), 3.40282347e38f);
+            h = __builtin_fmaf(decay, h, now[u]);
         }
     }
     if (a.last != nullptr && n < a.states) a.last[place] = h;
@@ -337,17 +349,14 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmArgs a) {
 // Sequences of at most kSsmShort steps: `quads` lanes a channel with 4 states each.
 template <typename T>
 __global__ __launch_bounds__(256) void k_ssm_short(SsmArgs a, uint32_t quads) {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-    const uint32_t q = uint32_t(i % quads);
-    const uint64_t unit = i / quads;
-    const bool mine = unit < uint64_t(a.batch) * a.channels;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, q = i % quads, unit = i / quads, units = a.batch * a.channels;
+    const bool mine = unit < units;
     // lanes past the end go along with the last channel: the sum over the quads takes all lanes
-    const uint64_t at = mine ? unit : uint64_t(a.batch) * a.channels - 1;
-    const uint32_t c = uint32_t(at % a.channels), b = uint32_t(at / a.channels);
+    const uint32_t at = mine ? unit : units - 1, c = at % a.channels, b = at / a.channels;
     const uint32_t n0 = q * 4, left = n0 < a.states ? min(a.states - n0, 4u) : 0;
     const uint32_t n = uint32_t(steps_of(a.lengths, a.length, b));
     FVec<4> h = 0.f, a2 = 0.f;
-    const uint64_t place = at * a.states + n0;
+    const uint64_t place = uint64_t(at) * a.states + n0;
     if (left == 4) {
         a2 = load_any<4>(a.a + uint64_t(c) * a.states + n0);
         if (a.h0) h = load_any<4>(a.h0 + place);
@@ -376,6 +385,7 @@ __global__ __launch_bounds__(256) void k_ssm_short(SsmArgs a, uint32_t quads) {
             }
         }
         const float x = float(*view_at<T>(a.x, b, t, c));
+        const float z = a.z.p ? float(*view_at<T>(a.z, b, t, c)) : 0.f;
         float s = float(*view_at<T>(a.dt, b, t, c)) + bias, y = 0.f;
         if (a.softplus) s = softplus(s);
 #pragma unroll
@@ -385,10 +395,7 @@ __global__ __launch_bounds__(256) void k_ssm_short(SsmArgs a, uint32_t quads) {
         }
         for (uint32_t m = 1; m < quads; m *= 2) y += __shfl_xor(y, int(m));
         y = __builtin_fmaf(d, x, y);
-        if (a.z.p != nullptr) {
-            const float z = float(*view_at<T>(a.z, b, t, c));
-            y *= z * logistic(z);
-        }
+        if (a.z.p != nullptr) y *= z * logistic(z);
         if (mine && q == 0) *view_at<T>(a.y, b, t, c) = T(y);
     }
     if (!mine) return;
@@ -686,16 +693,17 @@ __global__ __launch_bounds__(OWN == 1 ? 1024 : 256, 4) void k_ssm_backward(SsmAr
 // db and dc: the groups' sums over their channels joined.
 template <typename T>
 __global__ __launch_bounds__(256) void k_ssm_row_grad(SsmArgs a) {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-    const uint32_t n = uint32_t(i % a.padded), which = uint32_t(i / a.padded) & 1u;
-    const uint64_t row = i / (2 * a.padded), b = row / a.length, t = row % a.length;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x;   // fewer than 2^32, as in the kernels below
+    const uint32_t n = i % a.padded, which = i / a.padded & 1u;
+    const uint32_t row = i / (2 * a.padded), b = row / uint32_t(a.length), t = row % uint32_t(a.length);
     if (b >= a.batch || n >= a.states) return;
     float s = 0.f;
-    if (t < steps_of(a.lengths, a.length, uint32_t(b))) {
+    if (t < steps_of(a.lengths, a.length, b)) {
         const uint64_t stride = uint64_t(a.batch) * a.length * 2 * a.padded;
+#pragma unroll 8
         for (uint32_t g = 0; g < a.groups; ++g) s += a.part_rows[g * stride + i];
     }
-    *view_at<T>(which ? a.dc : a.db, uint32_t(b), t, n) = T(s);
+    *view_at<T>(which ? a.dc : a.db, b, t, n) = T(s);
 }
 
 // da, dd and ddt_bias: the chunks' sums over their steps joined.
@@ -707,6 +715,7 @@ __global__ __launch_bounds__(256) void k_ssm_channel_grad(const float* part, uin
     const uint32_t c = blockIdx.x * 16 + lane, n = blockIdx.y;
     double s = 0.0;
     if (c < channels)
+#pragma unroll 8
         for (uint32_t i = sub; i < rows; i += 16) s += part[(uint64_t(i) * (padded + 2) + n) * channels + c];
     sums[sub][lane] = s;
     __syncthreads();

@@ -108,9 +108,8 @@ __device__ __forceinline__ void pack_eight(const T* from, uint64_t stride, uint3
 template <typename T, typename E, int PLANES>
 __global__ __launch_bounds__(256) void k_pack(const T* from, uint64_t stride, uint32_t rows, uint32_t cols, uint32_t line,
                                               E* to) {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-    const uint32_t per = line / 8;
-    if (i / per < rows) pack_eight<T, E, PLANES>(from, stride, rows, cols, line, i / per, uint32_t(i % per) * 8, true, to);
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, per = line / 8;   // fewer than 2^32, as in the kernels below
+    if (i / per < rows) pack_eight<T, E, PLANES>(from, stride, rows, cols, line, i / per, i % per * 8, true, to);
 }
 
 // The rows' factors: 0 of those that do not count.  An infinite one leaves them all as they are.  One workgroup.
@@ -140,12 +139,12 @@ __global__ __launch_bounds__(1024) void k_loss_start(LossArgs a, uint32_t line, 
         row_factors(a);
         return;
     }
-    const uint64_t i = uint64_t(blockIdx.x - 1) * 1024 + threadIdx.x;
+    const uint32_t i = (blockIdx.x - 1) * 1024 + threadIdx.x;
     const uint32_t per = line / 8;
-    const uint64_t row = i / per;
+    const uint32_t row = i / per;
     if (row >= a.rows) return;
     pack_eight<T, E, PLANES>(static_cast<const T*>(a.hidden.p), a.hidden.stride, a.rows, a.width, line, row,
-                             uint32_t(i % per) * 8, row_counts(a, uint32_t(row)), to);
+                             i % per * 8, row_counts(a, row), to);
 }
 
 // ---- forward ----
@@ -488,10 +487,8 @@ __global__ __launch_bounds__(P::THREADS) void k_product(Operand x, Operand y, ui
 template <typename T>
 __global__ __launch_bounds__(256) void k_join_shares(const float* part, uint32_t shares, uint64_t rows, uint32_t cols,
                                                      uint32_t line, const float* scale, T* out, uint64_t stride) {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-    const uint32_t per = line / 4;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, per = line / 4, c = i % per * 4;
     const uint64_t row = i / per;
-    const uint32_t c = uint32_t(i % per) * 4;
     if (row >= rows) return;
     FVec<4> v = 0.f;
 #pragma unroll 8
