@@ -127,21 +127,26 @@ struct TileLoader {
             }
         }
     }
-    // Step [k0, k0 + 64) of a plane; past the end zeros.
-    __device__ __forceinline__ void request(const Operand& x, uint32_t plane, uint32_t m0, uint32_t k0, uint32_t kend,
-                                            E* tile) const {
-        const E* first = static_cast<const E*>(x.p) + plane * x.plane;
-        first += OUTER ? uint64_t(k0) * x.line + m0 : uint64_t(m0) * x.line + k0;
-        const char* base = reinterpret_cast<const char*>(first);
+    // The tile's first element of a plane at k0, and the bytes from there to the next step's.
+    static __device__ __forceinline__ const char* first(const Operand& x, uint32_t plane, uint32_t m0, uint32_t k0) {
+        const E* p = static_cast<const E*>(x.p) + plane * x.plane;
+        return reinterpret_cast<const char*>(p + (OUTER ? uint64_t(k0) * x.line + m0 : uint64_t(m0) * x.line + k0));
+    }
+    static __device__ __forceinline__ uint64_t advance(const Operand& x) { return (OUTER ? x.line : 1) * kTileK * 2; }
+    // Step [k0, k0 + 64), whose first element is `base`; from `end` on zeros.
+    __device__ __forceinline__ void request(const char* base, uint32_t k0, uint32_t end, E* tile) const {
         char* to = reinterpret_cast<char*>(tile) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * 1024;
-        const uint32_t end = min(kend, x.inner);
-        const bool whole = k0 + kTileK <= end;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const char* from = base + offset[i];
-            if (!whole) from = k0 + k[i] < end ? from : reinterpret_cast<const char*>(&kTileZeros);
+        auto copy = [&](int i, const char* from) {
             __builtin_amdgcn_global_load_lds((ADACOMP_GLOBAL const void*)from, (ADACOMP_LDS void*)(to + i * THREADS * 16),
                                              16, 0, 0);
+        };
+        if (k0 + kTileK <= end) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) copy(i, base + offset[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                copy(i, k0 + k[i] < end ? base + offset[i] : reinterpret_cast<const char*>(&kTileZeros));
         }
     }
     // A wavefront's BLOCKS of 32 rows from m on: where its lanes read them.
@@ -236,13 +241,20 @@ struct TileProduct {
         const LoadB lb(b, n0);
         const uint32_t total = (kend - kbegin + kTileK - 1) / kTileK * pairs.count;
         uint32_t k = kbegin, left = 4 * (pairs.count - 1);
+        const char *pa = LoadA::first(a, pairs.a >> left & 15u, m0, k), *pb = LoadB::first(b, pairs.b >> left & 15u, n0, k);
+        const uint64_t sa = LoadA::advance(a), sb = LoadB::advance(b);
+        const uint32_t enda = min(kend, a.inner), endb = min(kend, b.inner);
         auto request = [&](E* to) {
-            la.request(a, pairs.a >> left & 15u, m0, k, kend, to);
-            lb.request(b, pairs.b >> left & 15u, n0, k, kend, to + TM * kTileK);
+            la.request(pa, k, enda, to);
+            lb.request(pb, k, endb, to + TM * kTileK);
             k += kTileK;
+            pa += sa;
+            pb += sb;
             if (k >= kend) {   // the next pair; after the last one nothing is requested
                 k = kbegin;
                 left = left >= 4 ? left - 4 : 0;
+                pa = LoadA::first(a, pairs.a >> left & 15u, m0, k);
+                pb = LoadB::first(b, pairs.b >> left & 15u, n0, k);
             }
         };
         for (uint32_t step = 0; step + 1 < BUFFERS && step < total; ++step) request(lds + step * STEP);
