@@ -18,12 +18,13 @@
 // (kThreeByThree).  Or B alone has a second plane, of what the first leaves out
 // (kOneByTwo).
 //
-// The clock under load bounds the large tiles: 8192 x 50176 x 2048 bf16 with the
-// losses' epilogue takes 1560 to 1670 us (1.08 to 1.01 PFLOP/s); the library's plain product of
-// such sizes reaches 1.36.  Neither LDS, whose reads have no bank conflicts, nor the waits
-// show: 4 wavefronts of 4 x 4 blocks, which read a third less of LDS, with each part's
-// elements read during the products of the part before, take 1% less
-// there and 2 to 4% more where the inner axis is 1024, for nothing runs beside their epilogue.
+// Where both operands are K inner, each part's elements are read during the products of the
+// part before, across the steps' barrier too; the compiler's own order is a read, its
+// wait and two products (8192 x 65536 x 2048 bf16 with the losses' sums 1780 us against 1967: the
+// matrix cores busy 63% of the cycles against 52%, at a clock that goes down from 2.1 to
+// 1.95 GHz).  Transposing reads, which have to wait in their own statement, leave the overlap
+// to the other wavefront of the SIMD.  LDS does not show: its reads have no bank conflicts, and took the same
+// time when half of their cycles were.
 #pragma once
 
 #include "elements.hpp"
@@ -206,6 +207,8 @@ struct TileProduct {
     typedef TileLoader<E, BOUTER, TN, THREADS> LoadB;
     static constexpr uint32_t STEP = (TM + TN) * kTileK;   // elements of one buffer
     static constexpr uint32_t LDS_BYTES = BUFFERS * STEP * 2;
+    // Whether parts are read ahead.
+    static constexpr bool AHEAD = !AOUTER && !BOUTER && BUFFERS == 2;
     static constexpr int REQUESTS = LoadA::N + LoadB::N;   // a thread's, a step
 
     f32x16 acc[MT][NT];
@@ -228,6 +231,31 @@ struct TileProduct {
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[i][j] = mfma(av[i], bv[j], acc[i][j]);
+    }
+
+    // The products of one part's elements, and the next part's read meanwhile: a read behind each product but the
+    // first, which waits for the ones before.
+    template <int K, typename RA, typename RB>
+    __device__ __forceinline__ void part_ahead(const RA& ra, const RB& rb, const E* ta, const E* tb, Eight<E> (&av)[MT],
+                                               Eight<E> (&bv)[NT]) {
+        Eight<E> an[MT], bn[NT];
+        ra.template read<K>(ta, an);
+        rb.template read<K>(tb, bn);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = mfma(av[i], bv[j], acc[i][j]);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+        for (int i = 0; i < MT + NT; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) av[i] = an[i];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) bv[i] = bn[i];
     }
 
     // The sum over k in [kbegin, kend) of every pair of planes.
@@ -260,6 +288,31 @@ struct TileProduct {
         for (uint32_t step = 0; step + 1 < BUFFERS && step < total; ++step) request(lds + step * STEP);
         const typename LoadA::template Reader<MT> ra(row());
         const typename LoadB::template Reader<NT> rb(column());
+        if constexpr (AHEAD) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // step 0 is there
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (1 < total) request(lds + STEP);
+            Eight<E> av[MT], bv[NT];
+            ra.template read<0>(lds, av);
+            rb.template read<0>(lds + TM * kTileK, bv);
+            for (uint32_t step = 0; step < total; ++step) {
+                const E* ta = lds + (step & 1) * STEP;
+                const E* tb = ta + TM * kTileK;
+                part_ahead<16>(ra, rb, ta, tb, av, bv);
+                part_ahead<32>(ra, rb, ta, tb, av, bv);
+                part_ahead<48>(ra, rb, ta, tb, av, bv);
+                // The next step's elements are there, and this buffer has been read.
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                if (step + 2 < total) request(lds + (step & 1) * STEP);
+                const E* na = lds + (~step & 1) * STEP;
+                part_ahead<0>(ra, rb, na, na + TM * kTileK, av, bv);   // behind the last step read and not used
+            }
+            __syncthreads();   // the buffers are free
+            return;
+        }
         for (uint32_t step = 0; step < total; ++step) {
             // This step's elements are there: of the later requests, those of BUFFERS - 2 steps, none has to be.  And
             // the buffer before this one has been read, by every wavefront's own wait for its reads before the
