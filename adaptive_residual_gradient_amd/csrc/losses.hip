@@ -24,7 +24,8 @@ uint32_t share_of(uint64_t n, uint32_t each) { return static_cast<uint32_t>((n +
 uint32_t blocks_of(uint64_t items) { return static_cast<uint32_t>((items + 255) / 256); }
 
 // Tiles of the products, each by 8 wavefronts (small ones by fewer keep too few requests under way: 300 x 256
-// float32 over 4999 words 106 us forward and backward, by 4 wavefronts 114, by 2 with 64 x 64 tiles 122): 256 x 256
+// float32 over 4999 words 106 us forward and backward, by 4 wavefronts 114, by 2 with 64 x 64 tiles 122, all before
+// addresses went on from step to step, 92 since): 256 x 256
 // where they give most CUs one; else 128 x 128; for few rows, or where these leave half of the CUs without one,
 // 128 x 64.
 enum { kBig, kMid, kSmall };
