@@ -51,16 +51,16 @@ struct ConvArgs {
     bool past;               // results go past the cache
 };
 
-// p's logistic function.  From -87 down, where exp(-p) would overflow, it stays at 1.6e-38: y is off by
-// less than 1e-35 there.  Of 16-bit calls, whose results are rounded far coarser, without the corrections of the
-// exponential's argument and of the reciprocal: off by 2^-24 (|p| + 4).
+// p's logistic function.  Below -87, where exp(-p) comes to overflow, it is 0: a gate of the type's lowest value lets
+// nothing pass, and p times it is off by less than 1.5e-36.  Of 16-bit calls, whose results are rounded far coarser,
+// without the corrections of the exponential's argument and of the reciprocal: off by 2^-24 (|p| + 4).
 template <typename T>
 __device__ __forceinline__ float conv_gate(float p) {
     if (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(p * -kLog2e));
-    p = __builtin_elementwise_minimum(__builtin_elementwise_maximum(p, -87.f), 100.f);
-    const float d = 1.f + exp_of_minus(p);
+    const float v = __builtin_elementwise_minimum(__builtin_elementwise_maximum(p, -87.f), 100.f);
+    const float d = 1.f + exp_of_minus(v);
     const float r = __builtin_amdgcn_rcpf(d);
-    return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.f), r);
+    return p < -87.f ? 0.f : __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.f), r);
 }
 
 // The weights of a thread's channels by tap, those of the KT - taps taps that are not there 0.
