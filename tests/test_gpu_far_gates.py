@@ -4,6 +4,7 @@ import torch
 
 import model_refs as M
 import test_gpu_causal_conv as conv
+import test_gpu_selective_scan as scan
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,45 @@ def test_convolution(T, K, dtype):
         eg = torch.where(x < -200.0, torch.zeros(()).double(), eg)
         err = (eg * x.abs()).sum((0, 1)) + (T + 260) * M.U * (g * x).abs().sum((0, 1))
         M.assert_within(c.dw, ((g * x).sum((0, 1))[:, None], err[:, None]), "dweight")
+
+
+class Scan(scan.Case):
+    def check(self):
+        """As its own check, with what a sigmoid that is 0 leaves out of dz: the gate's slope at z below -87 is
+        s (1 + z (1 - s)) with s < exp(-87) = 1.65e-38 and |z| s < 1.43e-36, so less than NOTHING times dy and what the
+        gate multiplies."""
+        form, ins = M.scan, {k: M.f64(v) for k, v in self.i.items()}
+
+        def wider(dy, **kw):
+            out = form(dy=dy, **kw)
+            sums = form(**dict(ins, z=None), h0=kw["h0"])["y"]
+            value, err = out["dz"]
+            out["dz"] = (value, err + NOTHING * dy.abs() * (sums[0].abs() + sums[1]))
+            return out
+        M.scan = wider
+        try:
+            return super().check()
+        finally:
+            M.scan = form
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,N", [(3, 16), (8, 5), (30, 8), (100, 16), (40, 40)])
+def test_selective_scan(T, N, dtype):
+    """Short sequences and chunks; check() compares with the 64-bit form in both directions."""
+    c = Scan(3, T, 70, N, TYPES[dtype], seed=N)
+    none = plant(c.i["z"], T)
+    c.check()
+    assert not c.y[none].any() and not c.g["dz"][none].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_selective_scan_behind_shut_gates(dtype):
+    """Every gate at the type's lowest value: no output, and of the inputs' gradients what h_last has alone."""
+    c = Scan(2, 50, 70, 16, TYPES[dtype])
+    c.i["z"].fill_(torch.finfo(c.dtype).min)
+    c.check()
+    assert not any(t.any() for t in (c.y, c.g["dz"], c.g["dc"], c.g["dd"]))
+    c.dl = None
+    c.backward()
+    assert not any(c.g[k].any() for k in scan.GRADS)
