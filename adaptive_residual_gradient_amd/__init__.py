@@ -722,7 +722,8 @@ def linear_distillation(hidden, weight, ids, teacher, loss, lse, picked, ws, tem
                         stream=None) -> None:
     """loss = sum p (log p - log q) with p the softmax of the teacher's logits of the words ``ids`` and q that of
     hidden weight^T over the vocabulary, both at ``temperature``.  ids int64 and teacher float32 [rows, picks];
-    loss, lse [rows] and picked [rows, picks] float32 outputs.  Picks that are no word (-1, say) are left out."""
+    loss, lse [rows] and picked [rows, picks] float32 outputs.  Picks that are no word (-1, say) are left out; a row
+    without any, or whose teacher's logits are all -infinity, does not count: loss 0."""
     st = _operators().linear_distillation(hidden, weight, ids, teacher, loss, lse, picked, ws, temperature, stream)
     if st:
         raise AdaCompError("adacomp_linear_distillation", st)

@@ -59,7 +59,12 @@ struct LossArgs {
 
 __device__ __forceinline__ bool is_word(int64_t id, uint32_t words) { return uint64_t(id) < words; }
 
-// Whether a row's target is a word, or any of its picks.
+// Whether a pick has a part in p: a word whose teacher's logit is not -infinity.  NaN has one, and makes the row NaN.
+__device__ __forceinline__ bool is_pick(const LossArgs& a, uint64_t i) {
+    return is_word(a.ids[i], a.words) && a.teacher[i] != -__builtin_inff();
+}
+
+// Whether a row's target is a word, or any of its picks has a part in p.
 __device__ __forceinline__ bool row_counts(const LossArgs& a, uint32_t row) {
     return a.teacher ? a.counts[row] != 0 : is_word(a.ids[row], a.words);
 }
@@ -69,7 +74,7 @@ __global__ __launch_bounds__(256) void k_row_counts(LossArgs a) {
     const uint32_t row = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
     if (row >= a.rows) return;
     bool any = false;
-    for (uint32_t k = lane; k < a.picks; k += 64) any |= is_word(a.ids[uint64_t(row) * a.picks + k], a.words);
+    for (uint32_t k = lane; k < a.picks; k += 64) any |= is_pick(a, uint64_t(row) * a.picks + k);
     const bool counts = __any(any);
     if (lane == 0) a.counts[row] = counts;
 }
@@ -332,10 +337,10 @@ struct Teacher {
         sum = 0.f;
         const uint64_t first = uint64_t(row) * a.picks;
         for (uint32_t k = lane; k < a.picks; k += 64)
-            if (is_word(a.ids[first + k], a.words)) most = fmaxf(most, a.teacher[first + k]);
+            if (is_pick(a, first + k)) most = fmaxf(most, a.teacher[first + k]);
         for (int m = 32; m > 0; m /= 2) most = fmaxf(most, __shfl_xor(most, m));
         for (uint32_t k = lane; k < a.picks; k += 64)
-            if (is_word(a.ids[first + k], a.words)) sum += expf((a.teacher[first + k] - most) * a.sharp);
+            if (is_pick(a, first + k)) sum += expf((a.teacher[first + k] - most) * a.sharp);
         for (int m = 32; m > 0; m /= 2) sum += __shfl_xor(sum, m);
     }
     __device__ __forceinline__ float log_p(float logit, float sharp) const { return (logit - most) * sharp - logf(sum); }
@@ -374,9 +379,9 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a, uint32_t tiles) {
         const Teacher p(a, row, lane);
         for (uint32_t k = lane; k < a.picks; k += 64) {
             const uint64_t i = uint64_t(row) * a.picks + k;
-            if (!is_word(a.ids[i], a.words)) continue;
+            if (!is_pick(a, i)) continue;
             const float l = p.log_p(a.teacher[i], a.sharp);
-            if (l > -__builtin_inff()) loss += expf(l) * (l + (lse - a.picked[i]));   // p log p is 0 at p = 0
+            if (l != -__builtin_inff()) loss += expf(l) * (l + (lse - a.picked[i]));   // p log p is 0 at p = 0
         }
         for (int m = 32; m > 0; m /= 2) loss += __shfl_xor(loss, m);
     }
@@ -398,7 +403,7 @@ __global__ __launch_bounds__(256) void k_pick_grad(LossArgs a, uint32_t word0, u
         for (uint32_t k = lane; k < a.picks; k += 64) {
             const uint64_t i = uint64_t(row) * a.picks + k;
             ids[w][k] = a.ids[i];
-            ps[w][k] = is_word(a.ids[i], a.words) ? expf(p.log_p(a.teacher[i], a.sharp)) : 0.f;
+            ps[w][k] = is_pick(a, i) ? expf(p.log_p(a.teacher[i], a.sharp)) : 0.f;
         }
     }
     __syncthreads();

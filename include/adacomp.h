@@ -698,7 +698,8 @@ int adacomp_linear_cross_entropy_backward(const adacomp_head* head, const int64_
  *   dz_v = (exp(z_v - lse) - sum of the p_k of word v) * dloss / temperature
  *   ids      device int64[rows, picks]; picks that are no word are left out, and a row without
  *            any does not count.  A word may be picked more than once.
- *   teacher  device float32[rows, picks].
+ *   teacher  device float32[rows, picks].  A pick of -infinity has p = 0, a row of nothing else does
+ *            not count; NaN or +infinity at a word makes the row's loss and gradients NaN.
  *   picked   float32[rows, picks] output, z at the ids, for the gradients. */
 int adacomp_linear_distillation(const adacomp_head* head, const int64_t* ids, const float* teacher,
                                 uint32_t picks, float temperature, float* loss, float* lse,
