@@ -296,6 +296,15 @@ __global__ __launch_bounds__(256) void k_ssm_forward(SsmArgs a) {
         for (t = end > w.t0 ? end : w.t0; t < w.t1; ++t) SsmRows<T>(a.y, b).at(t, off) = T(0.f);
 }
 
+// h exp2(p) + add: the power of two goes to h's exponent, for float32 need not hold the decay of a whole chunk where it
+// holds h before and behind it.  Within 2^-600 .. 2^600 the decay is neither 0 nor infinite, as its steps' own need
+// not have been: an infinite state times 0, or none times infinity, would be NaN.
+__device__ __forceinline__ float decayed(float h, float p, float add) {
+    const float whole = floorf(fminf(fmaxf(p, -600.f), 600.f));   // a number of NaN too
+    p = __builtin_elementwise_minimum(__builtin_elementwise_maximum(p, -600.f), 600.f);   // NaN
+    return __builtin_fmaf(__builtin_amdgcn_exp2f(p - whole), __builtin_amdgcn_ldexpf(h, int(whole)), add);
+}
+
 // What is carried into each chunk takes the place of its end from 0; backward
 // (BACK) from the last chunk to the first.  One thread a sequence, state and channel.
 template <bool BACK>
@@ -337,11 +346,7 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmArgs a) {
             if (k + u >= a.chunks) continue;
             const uint32_t chunk = BACK ? a.chunks - 1 - (k + u) : k + u;
             ends[chunk * step] = h;
-            // not 0 and not infinite where the steps' own decays were neither: an infinite state times 0, or none
-            // times infinity, would be NaN
-            const float decay = __builtin_elementwise_minimum(
-                __builtin_elementwise_maximum(__builtin_amdgcn_exp2f(s[u] * a2), __uint_as_float(1u)), 3.40282347e38f);
-            h = __builtin_fmaf(decay, h, now[u]);
+            h = decayed(h, s[u] * a2, now[u]);
         }
     }
     if (a.last != nullptr && n < a.states) a.last[place] = h;

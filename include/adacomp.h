@@ -586,9 +586,9 @@ int adacomp_causal_conv_workspace_bytes(const adacomp_conv_shape* shape, uint64_
  *   h_n <- exp(s_t * a_n) * h_n + s_t * x_t * b_t,n
  *   y_t = (sum_n c_t,n * h_n + d * x_t) * (z_t / (1 + exp(-z_t)) with z, else 1)
  * in float32 whatever the type, y rounded once.  Long sequences are cut into
- * chunks whose decays exp(a_n * sum s_t) are formed from the sum.  (Where a state
- * is infinite they are taken into 2^-149 .. the largest float32 number: a product of 0 and
- * infinity then comes from a step's own decay alone.)
+ * chunks whose decays exp(a_n * sum s_t) are formed from the sum, with an exponent of
+ * their own.  (Within 2^-600 .. 2^600: a product of 0 and infinity comes from a step's
+ * own decay alone.)
  * ERR_TOO_LARGE: as for the gated scan's sizes and strides, states past
  * ADACOMP_SCAN_MAX_STATES, or 2^32 work-items and more (one for each step and state of b
  * and c, and one for each channel, state and sequence among them). */
