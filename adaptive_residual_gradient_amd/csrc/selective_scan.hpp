@@ -130,13 +130,17 @@ struct SsmPlace {
     }
 };
 
-// The rates a_n of a block in units of log 2; zeros behind the states.
+// A rate in units of log 2.  That of a state that keeps nothing, -infinity, is taken for the lowest number, whose decays
+// are 0 too: times no step at all, or in a gradient times 0, it would be NaN.
+__device__ __forceinline__ float ssm_rate(float a) { return __builtin_elementwise_maximum(a * kLog2e, -3.40282347e38f); }
+
+// The rates a_n of a block; zeros behind the states.
 template <int NB>
 __device__ __forceinline__ void ssm_rates(const SsmArgs& a, const SsmPlace& w, float (&a2)[NB]) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         const uint32_t at = w.block * NB + n;
-        a2[n] = at < a.states ? a.a[uint64_t(w.c) * a.states + at] * kLog2e : 0.f;
+        a2[n] = at < a.states ? ssm_rate(a.a[uint64_t(w.c) * a.states + at]) : 0.f;
     }
 }
 
@@ -316,7 +320,7 @@ __global__ __launch_bounds__(256) void k_ssm_join(SsmArgs a) {
     const uint64_t place = (b * a.channels + c) * a.states + n;
     float h = 0.f, a2 = 0.f;
     if (n < a.states) {
-        a2 = a.a[uint64_t(c) * a.states + n] * kLog2e;
+        a2 = ssm_rate(a.a[uint64_t(c) * a.states + n]);
         if (a.h0 != nullptr) h = a.h0[place];
     }
     constexpr uint32_t U = 16;   // chunks requested together, while the ones before are joined
@@ -396,7 +400,7 @@ __global__ __launch_bounds__(256) void k_ssm_short(SsmArgs a, uint32_t quads) {
         if (a.softplus) s = softplus(s);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * (a2[k] * kLog2e)), h[k], s * x * bv[k]);
+            h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * ssm_rate(a2[k])), h[k], s * x * bv[k]);
             y = __builtin_fmaf(cv[k], h[k], y);
         }
         for (uint32_t m = 1; m < quads; m *= 2) y += __shfl_xor(y, int(m));

@@ -608,7 +608,7 @@ typedef struct adacomp_ssm_shape {
 typedef struct adacomp_ssm_inputs {
     adacomp_view x, dt, b, c;
     adacomp_view z;          /* data NULL: no gate */
-    const float* a;          /* [channels, states] */
+    const float* a;          /* [channels, states]; -infinity: a state that keeps nothing */
     const float* d;          /* nullable [channels] (0) */
     const float* dt_bias;    /* nullable [channels] (0) */
     const int32_t* lengths;  /* nullable device int32[batch], as for the convolution */

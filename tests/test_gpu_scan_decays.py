@@ -51,3 +51,28 @@ def test_chunks_past_float32(step, first, last, N):
     assert A.selective_scan_workspace(1, 32, 64, N, device="cpu").numel() == (
         up(32 * 2 * padded) + up(4 * padded * 64) + up(4 * 64) + up(32 * 64))
     c.check()
+
+
+@pytest.mark.parametrize("T", [7, 100])
+def test_rates_of_minus_infinity(T):
+    """States that keep nothing: h is what the last step wrote, behind a sequence's end too."""
+    lengths = [T, 3, T // 2, 0]
+    c = Case(4, T, 64, 16, torch.float32, gated=False, lengths=lengths)
+    c.i["a"][::2] = float("-inf")
+    c.forward(kept=False)
+    d = {k: M.f64(v) for k, v in c.i.items()}
+    for b, n in enumerate(lengths):
+        if n == 0:
+            assert torch.equal(c.last[b], c.h0[b])
+            continue
+        raw = d["dt"][b, n - 1] + d["dt_bias"]
+        u = torch.logaddexp(raw, torch.zeros(()).double()) * d["x"][b, n - 1]
+        want = (u[:, None] * d["b"][b, n - 1])[::2]
+        # softplus: 12 roundings and that of its argument, and three products
+        M.assert_within(c.last[b, ::2], (want, (16 + raw.abs()[::2, None]) * M.U * want.abs()), f"h_last of sequence {b}")
+    assert not torch.isnan(c.y[:, :3]).any() and not torch.isnan(c.last).any()
+    c.forward()
+    c.backward()
+    assert not any(torch.isnan(g).any() for g in c.g.values() if g is not None)
+    # what h0 holds goes nowhere, and of the rates' gradients nothing is left
+    assert not c.g["dh0"][:3, ::2].any() and not c.g["da"][::2].any() and torch.equal(c.g["dh0"][3], c.dl[3])
