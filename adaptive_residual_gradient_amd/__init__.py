@@ -667,7 +667,8 @@ def selective_scan_states(batch: int, length: int, channels: int, states: int, d
     """What selective_scan keeps for selective_scan_backward."""
     import torch
     shape = _SsmShape(int(length), int(batch), int(channels), int(states), 0, 0)
-    return torch.empty(_bytes("adacomp_selective_scan_kept_bytes", ctypes.byref(shape)) // 4, device=device)
+    return torch.empty(_bytes("adacomp_selective_scan_kept_bytes", ctypes.byref(shape)) // 4, dtype=torch.float32,
+                       device=device)
 
 
 def selective_scan(x, dt, a, b, c, y, d=None, z=None, dt_bias=None, h0=None, h_last=None, states=None, lengths=None,
