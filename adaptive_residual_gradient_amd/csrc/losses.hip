@@ -56,6 +56,13 @@ int check_head(const adacomp_head* h, uint32_t picks) {
     constexpr uint64_t most = uint64_t(1) << 24;
     if (h->rows >= most || h->vocabulary >= most || h->width > 65536 || picks > ADACOMP_MAX_PICKS)
         return ADACOMP_ERR_TOO_LARGE;
+    // Work-items of a launch: a wavefront a pick, 4 elements of the hidden rows, and a workgroup a tile of the logits.
+    // (Smaller tiles than these are taken where there are few, and of 64 rows or fewer; the gradients' products have
+    // a piece's words or a row's width in place of the vocabulary.)
+    constexpr uint64_t items = uint64_t(1) << 32;
+    if (h->rows * picks * 64 >= items || h->rows * (up(h->width, 8) / 4) >= items ||
+        tiles(h->vocabulary, h->rows, 256) * 512 >= items)
+        return ADACOMP_ERR_TOO_LARGE;
     return ADACOMP_OK;
 }
 
@@ -309,11 +316,6 @@ int run_loss(const LossCall& c) {
     const HeadLayout l = head_layout(h, c.back);
     if (R > 0 && c.ws == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
     if (R > 0 && c.ws_bytes < l.bytes) return ADACOMP_ERR_CAPACITY;
-    // work-items of the launches that go over whole matrices, and of a wavefront a pick
-    constexpr uint64_t items = uint64_t(1) << 32;
-    if (R * (l.line / 4) >= items || uint64_t(l.piece) * (l.line / 8) >= items || R * c.picks * 64 >= items ||
-        up(h.vocabulary, 64) / 64 * (up(R, 64) / 64) * 512 >= items)
-        return ADACOMP_ERR_TOO_LARGE;
     const uint64_t rows4 = R * 4, picks4 = rows4 * c.picks;
     const Range r[12] = {range_of(c.back ? nullptr : c.loss, c.back || !c.loss ? 0 : rows4),
                          range_of(c.back ? nullptr : c.lse, c.back ? 0 : rows4),
@@ -335,8 +337,7 @@ int run_loss(const LossCall& c) {
     if (R == 0) {
         if (c.dweight == nullptr) return ADACOMP_OK;
         const uint64_t V = h.vocabulary;
-        if (V * h.width >= items) return ADACOMP_ERR_TOO_LARGE;
-        const dim3 grid(blocks_of(V * h.width)), block(256);
+        const dim3 grid(blocks_of(std::min<uint64_t>(V * h.width, 1 << 24))), block(256);
         if (h.type == ADACOMP_FLOAT)
             hipLaunchKernelGGL(k_zero_rows<float>, grid, block, 0, c.stream, static_cast<float*>(c.dweight), c.dweight_stride, V,
                                h.width);

@@ -512,8 +512,8 @@ __global__ __launch_bounds__(256) void k_join_shares(const float* part, uint32_t
 // A gradient that nothing adds to.
 template <typename T>
 __global__ __launch_bounds__(256) void k_zero_rows(T* out, uint64_t stride, uint64_t rows, uint32_t cols) {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i < rows * cols) out[i / cols * stride + i % cols] = T(0.f);
+    for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * cols; i += uint64_t(gridDim.x) * 256)
+        out[i / cols * stride + i % cols] = T(0.f);
 }
 
 }  // namespace adacomp

@@ -664,8 +664,9 @@ typedef struct adacomp_head {
     const void* weight;      /* [vocabulary, width], aligned to its element */
 } adacomp_head;
 /* Bytes of ws of the calls below, whatever the strides: of the losses (backward = 0) or of either
- * direction (1).  hidden and weight are not looked at.  ERR_TOO_LARGE for 2^24 rows, words or strides
- * and more, a width past 65536 or more than ADACOMP_MAX_PICKS picks. */
+ * direction (1).  hidden and weight are not looked at.  ERR_TOO_LARGE, here as in the calls, for 2^24
+ * rows, words or strides and more, a width past 65536, more than ADACOMP_MAX_PICKS picks of a row,
+ * and 2^26 picks, 2^34 elements of hidden rows in whole 8, or 2^23 tiles of 256 words and 256 rows and more. */
 #define ADACOMP_MAX_PICKS 1024u
 int adacomp_head_workspace_bytes(const adacomp_head* head, uint32_t picks, int backward,
                                  uint64_t* bytes);
