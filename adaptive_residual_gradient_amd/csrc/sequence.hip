@@ -149,17 +149,7 @@ void launch_conv_back(const ConvArgs& a, const ConvBackLayout& l, uint32_t vec, 
 struct SsmLayout {
     uint32_t padded, nb, groups, chunks, steps;   // nb: states of a forward wavefront
     uint64_t rows, ends, sums, steps_of, part_rows, part_a, bytes;   // byte offsets
-    bool brief;
 };
-
-int check_ssm(const adacomp_ssm_shape* s) {
-    if (s == nullptr || type_size(s->type) == 0 || s->states == 0 || (s->softplus != 0 && s->softplus != 1))
-        return ADACOMP_ERR_INVALID_ARGUMENT;
-    if (s->states > ADACOMP_SCAN_MAX_STATES) return ADACOMP_ERR_TOO_LARGE;
-    const int st = check_sizes(s->length, s->batch, s->channels);
-    if (st != ADACOMP_OK) return st;
-    return ADACOMP_OK;
-}
 
 SsmLayout ssm_layout(const adacomp_ssm_shape& s, bool back) {
     SsmLayout l{};
@@ -201,9 +191,19 @@ uint64_t ssm_kept_bytes(const adacomp_ssm_shape& s) {
 
 // The launches' grids fit in 32 bits of work-items.
 bool ssm_fits(const adacomp_ssm_shape& s, const SsmLayout& l) {
-    const uint64_t B = s.batch;
-    return B * s.length * 2 * l.padded < kItems && B * l.padded * s.channels < kItems &&
-           B * l.chunks * (l.groups + 4) * (l.padded / kSsmBackBlock) * 64 < kItems && B * s.channels * 16 < kItems;
+    const uint64_t B = s.batch, blocks = l.padded / l.nb, per = std::max<uint64_t>(4 / blocks, 1);   // as SsmGrid's
+    const uint64_t waves = std::max((l.groups + per - 1) / per * per * blocks, uint64_t(l.groups) * (l.padded / kSsmBackBlock));
+    return B * s.length * 2 * l.padded < kItems && B * l.padded * s.channels < kItems && B * l.chunks * waves * 64 < kItems &&
+           B * s.channels * 16 < kItems;
+}
+
+int check_ssm(const adacomp_ssm_shape* s) {
+    if (s == nullptr || type_size(s->type) == 0 || s->states == 0 || (s->softplus != 0 && s->softplus != 1))
+        return ADACOMP_ERR_INVALID_ARGUMENT;
+    if (s->states > ADACOMP_SCAN_MAX_STATES) return ADACOMP_ERR_TOO_LARGE;
+    const int st = check_sizes(s->length, s->batch, s->channels);
+    if (st != ADACOMP_OK) return st;
+    return ssm_fits(*s, ssm_layout(*s, false)) ? ADACOMP_OK : ADACOMP_ERR_TOO_LARGE;
 }
 
 void ssm_args(SsmArgs& a, const adacomp_ssm_shape& s, const adacomp_ssm_inputs& in, const SsmLayout& l, void* ws) {
@@ -463,7 +463,6 @@ int adacomp_selective_scan(const adacomp_ssm_shape* shape, const adacomp_ssm_inp
     if (s.length > 0 && y == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
     if (!aligned_to(h0, 4) || !aligned_to(h_last, 4) || !aligned16(kept) || !aligned16(ws)) return ADACOMP_ERR_MISALIGNED;
     const SsmLayout l = ssm_layout(s, false);
-    if (!ssm_fits(s, l)) return ADACOMP_ERR_TOO_LARGE;
     if (l.bytes > 0 && ws == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
     if (ws_bytes < l.bytes) return ADACOMP_ERR_CAPACITY;
     const uint64_t size = type_size(s.type), C = s.channels, state = 4 * uint64_t(s.batch) * C * s.states;
@@ -508,7 +507,6 @@ int adacomp_selective_scan_backward(const adacomp_ssm_shape* shape, const adacom
         l = SsmLayout{};
         l.padded = (s.states + 7) / 8 * 8;
     }
-    if (!ssm_fits(s, l)) return ADACOMP_ERR_TOO_LARGE;
     if (l.bytes > 0 && ws == nullptr) return ADACOMP_ERR_INVALID_ARGUMENT;
     if (ws_bytes < l.bytes) return ADACOMP_ERR_CAPACITY;
     const uint64_t size = type_size(s.type), C = s.channels, state = 4 * uint64_t(s.batch) * C * s.states;

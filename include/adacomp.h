@@ -590,8 +590,10 @@ int adacomp_causal_conv_workspace_bytes(const adacomp_conv_shape* shape, uint64_
  * their own.  (Within 2^-600 .. 2^600: a product of 0 and infinity comes from a step's
  * own decay alone.)
  * ERR_TOO_LARGE: as for the gated scan's sizes and strides, states past
- * ADACOMP_SCAN_MAX_STATES, or 2^32 work-items and more (one for each step and state of b
- * and c, and one for each channel, state and sequence among them). */
+ * ADACOMP_SCAN_MAX_STATES, or 2^32 work-items and more: one for each step and state of b and
+ * c; one for each channel, state and sequence; 16 for each channel and sequence; 64 for each 64
+ * channels (4 times as many), 4 states and chunk of a sequence.  States count in whole 8, past 8 in
+ * whole 16.  The queries of bytes refuse the same. */
 #define ADACOMP_SCAN_MAX_STATES 64u
 #define ADACOMP_SCAN_KEEP 8u   /* a state of every so many steps is kept for the gradients */
 typedef struct adacomp_ssm_shape {

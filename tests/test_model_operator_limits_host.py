@@ -63,3 +63,24 @@ def test_losses_query_and_calls_take_the_same_sizes(R, H, V, picks, fits, back):
     """2^26 picks, 2^34 elements of hidden rows in whole 8, 2^23 tiles of 256 words and rows."""
     assert head_query(R, H, V, picks=picks, back=int(back)) == (OK if fits else TOO_LARGE)
     assert head_call(R, H, V, picks, back) == (CAPACITY if fits else TOO_LARGE)
+
+
+@pytest.mark.parametrize("B,T,C,N,fits", [
+    (1, (1 << 27) - 8, 8, 16, True), (1, 1 << 27, 8, 16, False), (3, 1 << 26, 8, 16, False), (2, (1 << 25) - 8, 8, 24, True),
+    (2, 1 << 25, 8, 33, False), (1 << 20, 100, 64, 64, False), ((1 << 20) - 1, 4, 64, 64, True), (1 << 20, 0, 64, 64, False)])
+def test_scan_queries_and_calls_take_the_same_sizes(B, T, C, N, fits):
+    """2^32 steps and states of b and c, each in whole blocks, and of channels, states and sequences."""
+    L, n = A.lib(), ctypes.c_uint64()
+    s = A._SsmShape(T, B, C, N, 1, 1)
+    for back in (0, 1):
+        assert L.adacomp_selective_scan_workspace_bytes(ctypes.byref(s), back, ctypes.byref(n)) == (OK if fits else TOO_LARGE)
+    assert L.adacomp_selective_scan_kept_bytes(ctypes.byref(s), ctypes.byref(n)) == (OK if fits else TOO_LARGE)
+    at = [(k << 50) for k in range(1, 16)]
+    view = lambda p, width: A._View(p, T * width, width)
+    i = A._SsmInputs(view(at[0], C), view(at[1], C), view(at[2], N), view(at[3], N), view(None, C), at[4], None, None, None)
+    y = view(at[5], C)
+    call = L.adacomp_selective_scan(ctypes.byref(s), ctypes.byref(i), ctypes.byref(y), None, None, None, 1 << 20, 0, None)
+    g = A._SsmGradients(view(at[6], C), view(at[7], C), view(at[8], N), view(at[9], N), view(None, C), at[10], None, None, None)
+    back = L.adacomp_selective_scan_backward(ctypes.byref(s), ctypes.byref(i), ctypes.byref(y), at[11], None, ctypes.byref(g),
+                                             1 << 20, 0, None)
+    assert call == back == (CAPACITY if fits else TOO_LARGE)
