@@ -30,7 +30,8 @@
 // 12 to join them and 166 for y; backward 148, 11 and 479, and 25 us for
 // the joined sums of db, dc, da and dd.  The vector units are busy 63% of the
 // forward ends' time, 69% of y's, 73% of the backward ends' and 88% of the
-// gradients', which take 26 vector instructions a step and state.
+// gradients', which take 26 vector instructions a step and state, and spill 3 (not gated) or 6 of their 128
+// registers with 16 states a channel, 10 or 24 with 8, none with more.
 #pragma once
 
 #include "sequence.hpp"

@@ -18,12 +18,13 @@
 //
 // dz is rounded to the operands' 16 bits, for the matrix cores take no wider
 // ones: each term of the gradients' sums is off by at most half a step of its
-// type, as the rounded results are, which many rows' errors add to like random ones.
-// Of few rows, where they need not, dz has a second plane of what the first leaves
-// out.  The rows' factors are divided by the largest of them and brought up to 2^14:
-// half's smallest numbers would not hold a probability over the number of rows, and equal
-// factors are exact.  float32 calls split every operand, dz too, into three
-// bfloat16 planes (tile_product.hpp), and their products are as exact as float32's own.
+// type, as the rounded results are.  Of few rows, where it costs little, dz has a second
+// plane of what the first leaves out.  The rows' factors are divided by the largest of them and
+// brought up to 2^14: half's smallest numbers would not hold a probability over the number of
+// rows, and equal factors are exact.  (In half an element of dz keeps its 11 bits down to 2^-28 of
+// the largest factor: a probability of 2^-8 in a row whose factor is 2^-20 of that.)  float32 calls
+// split every operand, dz too, into three bfloat16 planes (tile_product.hpp), and their products
+// are as exact as float32's own.
 #pragma once
 
 #include "sequence.hpp"
@@ -32,7 +33,11 @@
 namespace adacomp {
 
 constexpr uint32_t kLossMaxPicks = 1024;
-constexpr uint32_t kLossFewRows = 512;   // most rows whose dz has a second plane
+// Most rows whose dz has a second plane.  Gradients of 512 x 1024 over 32000 words bf16 take 250 us with it and 155
+// without, of 4096 rows 1432 and 854: up to here it adds 0.1 ms, past it 1.6 times the call.  With it the distillation's
+// gradients are off by 0.0017 of their norm, as their own rounding is, without by 0.0023 to 0.0025, of 64 rows as of
+// 4096; the cross entropy's, whose largest elements are -dloss and nearly exact, by 0.0017 either way.
+constexpr uint32_t kLossFewRows = 512;
 
 // Where a matrix of the caller's lies; T elements.
 struct LossMatrix {
@@ -42,7 +47,7 @@ struct LossMatrix {
 
 struct LossArgs {
     LossMatrix hidden, weight;
-    Operand x, w;               // the same as operands, 16-bit
+    Operand x;                  // hidden as an operand, 16-bit
     const int64_t* ids;         // [rows][picks]; targets: one a row
     const float* teacher;       // [rows][picks], nullptr: cross entropy
     float* loss;

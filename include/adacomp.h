@@ -654,7 +654,8 @@ int adacomp_selective_scan_kept_bytes(const adacomp_ssm_shape* shape, uint64_t* 
 /* Losses over a vocabulary straight from the hidden states: the logits
  * z = hidden weight^T are formed in tiles and never kept.  Products of 16-bit
  * operands are summed in float32; float32 operands are split into three bfloat16
- * numbers each, which leaves out less than 2^-23 of a product. */
+ * numbers each, which leaves out less than 2^-23 of a product.  (An infinite float32 operand makes
+ * its logits NaN, for it meets the parts of the other one that are 0.) */
 typedef struct adacomp_head {
     uint64_t rows;           /* positions; may be 0 */
     uint32_t width;          /* >= 1 */
@@ -684,7 +685,9 @@ int adacomp_linear_cross_entropy(const adacomp_head* head, const int64_t* target
 /* Its gradients, with dz_v = (exp(z_v - lse) - [v = target]) * dloss:
  *   dhidden = dz weight,  dweight = dz^T hidden
  * dz is divided by the largest |dloss| and rounded once to the type; float32, and 16 bits of at
- * most 512 rows, have further numbers of what that leaves out (float32: 2^-23 of dz).
+ * most 512 rows, have further numbers of what that leaves out (float32: 2^-23 of dz).  In half
+ * elements of dz below 2^-28 of the largest |dloss| lose bits, and below 2^-39 of it are 0: give
+ * rows of very different weights in bfloat16 or float32.
  *   loss, lse  as the forward call wrote them;  dloss  [rows] float32.
  *   dhidden    nullable [rows, width] output, dhidden_stride elements from row to row.
  *   dweight    nullable [vocabulary, width] output.
